@@ -7,7 +7,9 @@ exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional, Tuple
@@ -27,7 +29,9 @@ EXPORTED = ("prism_plan_create", "prism_plan_bytes", "prism_plan_build", "prism_
             "prism_plan_set_timing", "prism_plan_read_timing", "prism_timer_name", "prism_zone_shapes_noalloc",
             "prism_plan_selftest_timeout", "prism_plan_update_qkv", "prism_step_host", "prism_step_join",
             "prism_step_wait", "prism_audio_norms", "prism_plan_build_stats", "prism_plan_stats_slice",
-            "prism_plan_build_finish", "prism_attn_fwd_taylor", "prism_plan_build_with_zones")
+            "prism_plan_build_finish", "prism_attn_fwd_taylor", "prism_plan_build_with_zones",
+            "prism_ckpt_bytes", "prism_ckpt_pack", "prism_ckpt_unpack", "prism_layer_norm_fwd",
+            "prism_layer_norm_bwd_workspace", "prism_layer_norm_bwd")
 NUM_TIMERS = 12
 
 
@@ -57,6 +61,15 @@ _lib = None
 class prism_host_io(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("Q", "K", "V", "a_norm", "dO", "O", "lse", "dQ", "dK", "dV")] + [
         ("taylor", ctypes.c_int)]
+
+
+class prism_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_longlong), ("group_stride", ctypes.c_longlong),
+                ("group", ctypes.c_int)]
+
+
+class prism_ckpt(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int)]
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -99,6 +112,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.prism_plan_build_with_zones.restype = ctypes.c_int
     lib.prism_audio_norms.argtypes = [P, P, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, P]
     lib.prism_audio_norms.restype = ctypes.c_int
+    R, K, LL, I = ctypes.POINTER(prism_rows), ctypes.POINTER(prism_ckpt), ctypes.c_longlong, ctypes.c_int
+    lib.prism_ckpt_bytes.argtypes = [LL, I, S, S]
+    lib.prism_ckpt_pack.argtypes = [R, I, LL, I, K, P]
+    lib.prism_ckpt_unpack.argtypes = [K, R, I, LL, I, P]
+    lib.prism_layer_norm_fwd.argtypes = [R, P, P, R, P, P, K, LL, I, ctypes.c_float, I, I, P]
+    lib.prism_layer_norm_bwd_workspace.argtypes = [LL, I]
+    lib.prism_layer_norm_bwd_workspace.restype = ctypes.c_size_t
+    lib.prism_layer_norm_bwd.argtypes = [R, K, R, P, P, P, R, P, P, P, ctypes.c_size_t, LL, I, I, I, P]
+    for name in ("prism_ckpt_bytes", "prism_ckpt_pack", "prism_ckpt_unpack", "prism_layer_norm_fwd",
+                 "prism_layer_norm_bwd"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.prism_plan_destroy.argtypes = [V]
     lib.prism_plan_destroy.restype = None
     lib.prism_last_error.restype = ctypes.c_char_p
@@ -499,6 +523,183 @@ def prism_audio_norms(h: torch.Tensor, T: int, H: int, W: int, a: Optional[torch
     _need(a, "a", torch.float32, (batch, T, H, W))
     _check(load_library().prism_audio_norms(_ptr(h), _ptr(a), batch, T, H, W, ch, _stream()))
     return a
+
+
+# -- rows of channels: layer norm and 8-bit checkpoints -----------------------
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_FORMATS = {"int8": 0, "e4m3": 1}
+
+
+def _on(device):
+    """Makes `device` current for the calls that launch on the current device."""
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _rows(t: torch.Tensor, name: str, device=None, dtype=None):
+    """(prism_rows, rows, channels) of a CUDA tensor whose last axis is the channels: its
+    leading axes must step evenly, or evenly within equal groups."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES or t.dim() == 0:
+        raise ValueError(f"{name} must be a bf16, fp16 or fp32 CUDA tensor with a channel axis")
+    if (device is not None and t.device != device) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    C = t.shape[-1]
+    if C < 1 or (C > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: channels must be consecutive elements of the last axis")
+    levels = []  # innermost first: [count, stride]
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if levels and st == levels[-1][0] * levels[-1][1]:
+            levels[-1][0] *= n
+        else:
+            levels.append([n, st])
+    count = math.prod(t.shape[:-1])
+    if count and (len(levels) > 2 or any(st < C for _, st in levels)):
+        raise ValueError(f"{name}: rows of shape {tuple(t.shape)} with strides {t.stride()} are not evenly spaced")
+    if not count or not levels:
+        return prism_rows(t.data_ptr(), C, 0, 0), count, C
+    if len(levels) == 1:
+        return prism_rows(t.data_ptr(), levels[0][1], 0, 0), count, C
+    return prism_rows(t.data_ptr(), levels[0][1], levels[1][1], levels[0][0]), count, C
+
+
+def _weight(t, name, x, channels):
+    if t is None:
+        return None
+    if (not t.is_cuda or t.device != x.device or t.dtype not in (x.dtype, torch.float32)
+            or tuple(t.shape) != (channels,) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous [{channels}] tensor on {x.device}, fp32 or {x.dtype}")
+    return t
+
+
+def _weights_dtype(x, *ws):
+    kinds = {w.dtype for w in ws if w is not None}
+    if len(kinds) > 1:
+        raise ValueError("the weights must have one dtype")
+    return kinds.pop() if kinds else torch.float32
+
+
+@dataclass
+class Checkpoint:
+    """Values kept in 8 bits: a code per value and a scale per 32 channels of a row.
+    shape and dtype are the tensor's it was made from."""
+    codes: torch.Tensor    # uint8 [rows, channels]
+    scales: torch.Tensor   # uint8 [rows, ceil(channels / 32)]
+    format: str            # "int8" or "e4m3"
+    shape: Tuple[int, ...]
+    dtype: torch.dtype
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.nbytes + self.scales.nbytes
+
+    def to_c(self) -> prism_ckpt:
+        rows, C = self.codes.shape
+        for t, n, sh in ((self.codes, "codes", (rows, C)), (self.scales, "scales", (rows, (C + 31) // 32))):
+            _need(t, n, torch.uint8, sh)
+        if self.format not in _FORMATS:
+            raise ValueError(f"checkpoint format {self.format!r} is not one of {sorted(_FORMATS)}")
+        if C != self.shape[-1] or rows != math.prod(self.shape[:-1]) or self.scales.device != self.device:
+            raise ValueError("codes, scales and shape do not belong together")
+        return prism_ckpt(self.codes.data_ptr(), self.scales.data_ptr(), _FORMATS[self.format])
+
+
+def _new_ckpt(x: torch.Tensor, rows: int, channels: int, fmt: str) -> Checkpoint:
+    if fmt not in _FORMATS:
+        raise ValueError(f"checkpoint format {fmt!r} is not one of {sorted(_FORMATS)}")
+    return Checkpoint(torch.empty((rows, channels), dtype=torch.uint8, device=x.device),
+                      torch.empty((rows, (channels + 31) // 32), dtype=torch.uint8, device=x.device),
+                      fmt, tuple(x.shape), x.dtype)
+
+
+def prism_ckpt_pack(x: torch.Tensor, fmt: str = "int8") -> Checkpoint:
+    """x [..., channels] in 8 bits (see prism.h: codes and power-of-two scales of 32 channels)."""
+    r, n, C = _rows(x, "x")
+    out = _new_ckpt(x, n, C, fmt)
+    with _on(x.device):
+        _check(load_library().prism_ckpt_pack(ctypes.byref(r), _DTYPES[x.dtype], n, C, ctypes.byref(out.to_c()),
+                                              _stream()))
+    return out
+
+
+def prism_ckpt_unpack(ckpt: Checkpoint, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values a checkpoint stands for, in its dtype (or `out`'s)."""
+    c = ckpt.to_c()
+    if out is None:
+        out = torch.empty(ckpt.shape, dtype=ckpt.dtype, device=ckpt.device)
+    elif tuple(out.shape) != ckpt.shape:
+        raise ValueError(f"out must have shape {ckpt.shape}")
+    r, n, C = _rows(out, "out", ckpt.device)
+    with _on(ckpt.device):
+        _check(load_library().prism_ckpt_unpack(ctypes.byref(c), ctypes.byref(r), _DTYPES[out.dtype], n, C, _stream()))
+    return out
+
+
+def prism_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                         eps: float = 1e-6, y: Optional[torch.Tensor] = None, ckpt: Optional[str] = None):
+    """Layer norm over x's last axis: (y, mean, rstd), mean and rstd fp32 of x's leading
+    shape.  With ckpt = "int8" or "e4m3" also x in 8 bits, written in the same pass:
+    (y, mean, rstd, Checkpoint) -- what prism_layer_norm_bwd can take in x's place."""
+    rx, n, C = _rows(x, "x")
+    gamma, beta = _weight(gamma, "gamma", x, C), _weight(beta, "beta", x, C)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif tuple(y.shape) != tuple(x.shape):
+        raise ValueError("y must have x's shape")
+    ry, _, _ = _rows(y, "y", x.device, x.dtype)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    kept = _new_ckpt(x, n, C, ckpt) if ckpt is not None else None
+    c = ctypes.byref(kept.to_c()) if kept is not None else None
+    with _on(x.device):
+        _check(load_library().prism_layer_norm_fwd(
+            ctypes.byref(rx), _ptr(gamma), _ptr(beta), ctypes.byref(ry), _ptr(mean), _ptr(rstd), c, n, C, float(eps),
+            _DTYPES[x.dtype], _DTYPES[_weights_dtype(x, gamma, beta)], _stream()))
+    return (y, mean, rstd) if kept is None else (y, mean, rstd, kept)
+
+
+def prism_layer_norm_bwd(dy: torch.Tensor, x, gamma: Optional[torch.Tensor], mean: torch.Tensor, rstd: torch.Tensor,
+                         dx: Optional[torch.Tensor] = None, weight_grads: bool = True):
+    """Gradients (dx, dgamma, dbeta) of prism_layer_norm_fwd; x is the forward's input or its
+    Checkpoint.  dgamma and dbeta have gamma's dtype (fp32 without a gamma); with
+    weight_grads = False only dx is computed, and they are None."""
+    rdy, n, C = _rows(dy, "dy")
+    gamma = _weight(gamma, "gamma", dy, C)
+    if tuple(x.shape) != tuple(dy.shape):
+        raise ValueError(f"x {tuple(x.shape)} must have dy's shape {tuple(dy.shape)}")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _need(t, name, torch.float32, dy.shape[:-1])
+        if t.device != dy.device:
+            raise ValueError(f"{name} must be on {dy.device}")
+    if isinstance(x, Checkpoint):
+        if x.device != dy.device:
+            raise ValueError(f"the checkpoint must be on {dy.device}")
+        rx, c = None, ctypes.byref(x.to_c())
+    else:
+        rx, c = ctypes.byref(_rows(x, "x", dy.device, dy.dtype)[0]), None
+    if dx is None:
+        dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    elif tuple(dx.shape) != tuple(dy.shape):
+        raise ValueError("dx must have dy's shape")
+    rdx, _, _ = _rows(dx, "dx", dy.device, dy.dtype)
+    wdt = _weights_dtype(dy, gamma)
+    lib = load_library()
+    dgamma = dbeta = work = None
+    nbytes = 0
+    if weight_grads:
+        dgamma = torch.empty(C, dtype=wdt, device=dy.device)
+        dbeta = torch.empty(C, dtype=wdt, device=dy.device)
+        nbytes = lib.prism_layer_norm_bwd_workspace(n, C)
+        work = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
+    with _on(dy.device):
+        _check(lib.prism_layer_norm_bwd(rx, c, ctypes.byref(rdy), _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                        ctypes.byref(rdx), _ptr(dgamma), _ptr(dbeta), _ptr(work), nbytes, n, C,
+                                        _DTYPES[dy.dtype], _DTYPES[wdt], _stream()))
+    return dx, dgamma, dbeta
 
 
 def prism_plan_create(params: Params) -> PrismPlan:

@@ -27,6 +27,8 @@ prism_status fail(prism_status s, const char *fmt, ...) {
     return s;
 }
 
+void clear_error() { g_last_error.clear(); }
+
 prism_status fail_cuda(cudaError_t e, const char *what, const char *file, int line) {
     const prism_status s = (e == cudaErrorMemoryAllocation) ? PRISM_ERR_NOMEM : PRISM_ERR_CUDA;
     return fail(s, "%s failed: %s (%s:%d)", what, cudaGetErrorString(e), file, line);

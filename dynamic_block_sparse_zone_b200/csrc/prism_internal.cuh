@@ -110,6 +110,7 @@ struct TimerScope {
     } while (0)
 
 prism_status fail(prism_status s, const char *fmt, ...);
+void clear_error();  // the start of an entry point: "" for the calling thread
 prism_status fail_cuda(cudaError_t e, const char *what, const char *file, int line);
 
 // Launchers (each returns PRISM_OK or an error after checking the launch).

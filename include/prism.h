@@ -253,6 +253,81 @@ PRISM_API prism_status prism_attn_bwd(prism_plan *plan, const void *O, const voi
 PRISM_API prism_status prism_audio_norms(const void *h, float *a, int batch, int T, int H, int W, int channels,
                                          void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Rows of channels: layer norm and 8-bit activation checkpoints.  No plan is
+ * needed; the calls enqueue kernels on `stream` on the current device, which
+ * must hold every tensor.  They allocate nothing and may be captured into a
+ * CUDA graph.
+ *
+ * A tensor is `rows` rows of `channels` consecutive elements (channels in
+ * [1, 2^20], rows in [0, 2^40]).  Row r starts at
+ *   data + (r / group) * group_stride + (r % group) * stride      (elements)
+ * with group = 0 meaning one group of all rows: a slice of wider rows has
+ * stride > channels, and Q inside a fused [tokens][3][heads][head_dim]
+ * projection has group = heads, stride = head_dim, group_stride =
+ * 3 * heads * head_dim.  group > 0 needs rows < 2^31.  data is aligned to the
+ * element; 16-byte aligned rows of a multiple of 16 bytes take the fast path.
+ * Outputs must not share elements with any other argument (tensors that lie
+ * in one buffer without sharing elements are fine).                        */
+typedef enum prism_dtype { PRISM_BF16 = 0, PRISM_FP16 = 1, PRISM_FP32 = 2 } prism_dtype;
+typedef struct prism_rows {
+    void *data;
+    long long stride, group_stride;
+    int group;
+} prism_rows;
+
+/* An 8-bit checkpoint of rows x channels values: codes [rows][channels], one
+ * byte each, and scales [rows][ceil(channels / 32)], one byte per 32
+ * consecutive channels of a row (16-byte aligned, device, the caller's; sizes
+ * prism_ckpt_bytes).  A group's values are code * 2^k: k is the least integer
+ * >= -127 with max|x| <= qmax * 2^k, the code is x * 2^-k rounded to the
+ * nearest (ties to even) signed integer (PRISM_CKPT_INT8, qmax 127) or e4m3
+ * float (PRISM_CKPT_E4M3, qmax 448), and the scale byte is k + 127.  An error
+ * is at most half a step: 2^(k-1) for int8, 2^-4 of the value for e4m3 (2^(k-10)
+ * below 2^(k-6)).  A group that holds an infinity or a NaN reads back as NaN. */
+typedef enum prism_ckpt_format { PRISM_CKPT_INT8 = 0, PRISM_CKPT_E4M3 = 1 } prism_ckpt_format;
+typedef struct prism_ckpt {
+    void *codes, *scales;
+    int format;
+} prism_ckpt;
+PRISM_API prism_status prism_ckpt_bytes(long long rows, int channels, size_t *codes, size_t *scales);
+
+/* x (dtype) into a checkpoint, and a checkpoint's values into y, rounded to
+ * dtype (only fp16 can need it; a value past dtype's largest reads back as
+ * that).                                                                     */
+PRISM_API prism_status prism_ckpt_pack(const prism_rows *x, int dtype, long long rows, int channels,
+                                       const prism_ckpt *out, void *stream);
+PRISM_API prism_status prism_ckpt_unpack(const prism_ckpt *in, const prism_rows *y, int dtype, long long rows,
+                                         int channels, void *stream);
+
+/* Layer norm over the channels of each row: y = (x - mean) rstd gamma + beta
+ * with mean = sum x / C, rstd = (sum (x - mean)^2 / C + eps)^(-1/2).  x and y
+ * have type dtype; gamma and beta [channels] have type weight_dtype (fp32, or
+ * dtype) and either may be NULL (1 and 0); mean and rstd (fp32 [rows]) are
+ * written for the backward pass.  ckpt, if not NULL, receives x in 8 bits in
+ * the same pass.  Sums are fp32 (the variance from x - mean); y is rounded
+ * once.                                                                      */
+PRISM_API prism_status prism_layer_norm_fwd(const prism_rows *x, const void *gamma, const void *beta,
+                                            const prism_rows *y, float *mean, float *rstd, const prism_ckpt *ckpt,
+                                            long long rows, int channels, float eps, int dtype, int weight_dtype,
+                                            void *stream);
+
+/* Its gradient: with g = dy gamma and xhat = (x - mean) rstd,
+ *   dx = rstd (g - mean(g) - xhat mean(g xhat)),
+ *   dgamma = sum over rows of dy xhat, dbeta = sum over rows of dy.
+ * x comes from exactly one of x (dtype) and ckpt (its 8-bit form, read
+ * directly).  dgamma and dbeta (weight_dtype, [channels]) may each be NULL;
+ * rows = 0 writes them as zero.  They are summed in fp32 in a fixed order:
+ * repeated calls give the same bits.  workspace: device, 16-byte aligned, at
+ * least prism_layer_norm_bwd_workspace bytes, used by this call until its
+ * work on `stream` is done (calls that overlap need one each).              */
+PRISM_API size_t prism_layer_norm_bwd_workspace(long long rows, int channels);
+PRISM_API prism_status prism_layer_norm_bwd(const prism_rows *x, const prism_ckpt *ckpt, const prism_rows *dy,
+                                            const void *gamma, const float *mean, const float *rstd,
+                                            const prism_rows *dx, void *dgamma, void *dbeta, void *workspace,
+                                            size_t workspace_bytes, long long rows, int channels, int dtype,
+                                            int weight_dtype, void *stream);
+
 /* One layer step from HOST buffers: copy the inputs to the device, build the
  * plan, run the forward and (when dO is given) the backward, and copy the
  * outputs back -- the same computation as prism_plan_build + prism_attn_fwd
