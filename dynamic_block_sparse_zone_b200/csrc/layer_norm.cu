@@ -137,27 +137,369 @@ __global__ void __launch_bounds__(kThreads) k_norm_dw_any(Source<T> x, RowPtr dy
     part[((size_t)blockIdx.y * 2 + 1) * C + c] = b;
 }
 
-// dgamma, dbeta = the P partials summed in order; 32 columns per CTA.
-__global__ void __launch_bounds__(kThreads) k_norm_dw_sum(const float *__restrict__ part, int P, void *dgamma,
-                                                          void *dbeta, int wdt, int C) {
-    __shared__ float red[2][kThreads / 32][32];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+// dgamma, dbeta = the P partials, 32 columns per CTA: warp w sums the partials
+// p = w mod 32, then the warps' sums are added in order.
+__global__ void __launch_bounds__(1024) k_norm_dw_sum(const float *__restrict__ part, int P, void *dgamma, void *dbeta,
+                                                      int wdt, int C) {
+    __shared__ float red[2][32][33];
+    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
     float a = 0.f, b = 0.f;
-    if (c < C)
-        for (int p = w; p < P; p += kThreads / 32) {
+    if (c < C) {
+#pragma unroll 8
+        for (int p = w; p < P; p += 32) {
             a += part[((size_t)p * 2) * C + c];
             b += part[((size_t)p * 2 + 1) * C + c];
         }
-    red[0][w][threadIdx.x & 31] = a;
-    red[1][w][threadIdx.x & 31] = b;
+    }
+    red[0][w][lane] = a;
+    red[1][w][lane] = b;
     __syncthreads();
     if (w < 2 && c < C) {
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < kThreads / 32; ++k) s += red[w][k][threadIdx.x & 31];
+        for (int k = 0; k < 32; ++k) s += red[w][k][lane];
         void *dst = w == 0 ? dgamma : dbeta;
         if (dst) weight_store(dst, wdt, c, s);
     }
+}
+
+// ---------------------------------------------------------------------------
+// Rows held in registers: one read of each input, one write of each output
+// (the floor of these HBM-bound operators).  A row's nvec vectors of VEC
+// elements are spread over `tpr` threads, NV each: lanes of one warp (tpr <=
+// 32, a power of two, 256 / tpr rows per CTA; only shuffles between the lanes)
+// or the whole CTA (one row at a time).  Every thread keeps its channels over
+// all of the rows that it takes, so weights and their gradients stay put.
+// ---------------------------------------------------------------------------
+
+// tpr lanes' sum, in each of them
+__device__ __forceinline__ float lanes_sum(float v, int tpr) {
+    for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// VEC weights from channel c0 on (NULL: `none` each); `vec`: 16-byte aligned
+template <int VEC>
+__device__ __forceinline__ void load_weights(const void *p, int dt, int c0, bool vec, float none, float (&w)[VEC]) {
+    if (!p) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = none;
+    } else if (VEC > 1 && vec && dt == PRISM_FP32) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c0 + e));
+            w[e] = f.x;
+            if (VEC > 1) w[(e + 1) % VEC] = f.y, w[(e + 2) % VEC] = f.z, w[(e + 3) % VEC] = f.w;
+        }
+    } else if (VEC == 8 && vec) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p) + c0));
+        const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const uint16_t h = (uint16_t)(a[e / 2] >> (16 * (e & 1)));
+            w[e] = dt == PRISM_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = weight_at(p, dt, c0 + e);
+    }
+}
+
+struct FwdArgs {
+    RowPtr x, y;
+    const void *gamma, *beta;
+    int wdt;
+    bool wvec;
+    float *mean, *rstd;
+    uint8_t *codes, *scales;
+    int fmt;
+    long long nrows;
+    int C, nvec, tpr;
+    float eps, invC;
+};
+
+template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
+__global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_fwd(FwdArgs a) {
+    using V = Pack<T, VEC>;
+    __shared__ float red[2][2][16];
+    const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
+    const int per = kCta ? 1 : 256 / tpr, sub = kCta ? 0 : threadIdx.x / tpr;
+    constexpr bool kKeep = NV * VEC <= 16;  // weights stay in registers; else they are read from L1 for each row
+    float gw[kKeep ? NV : 1][VEC], bw[kKeep ? NV : 1][VEC];
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * tpr + t;
+            if (v < a.nvec) {
+                load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.wvec, 1.f, gw[i]);
+                load_weights<VEC>(a.beta, a.wdt, v * VEC, a.wvec, 0.f, bw[i]);
+            }
+        }
+    }
+    int par = 0;
+    auto row_sum = [&](float s, int which) {
+        if constexpr (kCta) {  // a slot is written again two rows on, behind a barrier of the row between
+            s = warp_sum(s);
+            if ((threadIdx.x & 31) == 0) red[par][which][threadIdx.x >> 5] = s;
+            __syncthreads();
+            s = 0.f;
+            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += red[par][which][w];
+            return s;
+        } else {
+            return lanes_sum(s, tpr);
+        }
+    };
+    for (long long r0 = (long long)blockIdx.x * per; r0 < a.nrows; r0 += (long long)gridDim.x * per) {
+        const long long r = r0 + sub;
+        const bool live = kCta || r < a.nrows;
+        V x[NV];
+        const V *xr = reinterpret_cast<const V *>(a.x(live ? r : r0));
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * tpr + t;
+            if (v < a.nvec) x[i] = xr[v];
+            else
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x[i].v[e] = from_f<T>(0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s += to_f(x[i].v[e]);
+        const float mean = row_sum(s, 0) * a.invC;
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i * tpr + t < a.nvec) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float d = to_f(x[i].v[e]) - mean;
+                    q = fmaf(d, d, q);
+                }
+            }
+        const float rstd = rsqrtf(row_sum(q, 1) * a.invC + a.eps);
+        par ^= 1;
+        V *yr = reinterpret_cast<V *>(a.y(live ? r : r0));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * tpr + t;
+            const bool in = live && v < a.nvec;
+            if (in) {
+                if constexpr (!kKeep) {
+                    load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.wvec, 1.f, gw[0]);
+                    load_weights<VEC>(a.beta, a.wdt, v * VEC, a.wvec, 0.f, bw[0]);
+                }
+                V o;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    o.v[e] = from_f<T>(fmaf((to_f(x[i].v[e]) - mean) * rstd, gw[kKeep ? i : 0][e], bw[kKeep ? i : 0][e]));
+                yr[v] = o;
+            }
+            if constexpr (kCkpt) {  // 32 / VEC neighbouring lanes hold a scale group
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) top = max(top, __float_as_uint(fabsf(to_f(x[i].v[e]))));
+#pragma unroll
+                for (int o = 16 / VEC; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int k = code_exponent(__uint_as_float(top), a.fmt);
+                const float inv = code_inv_scale(k);
+                if (in) {
+                    Pack<uint8_t, VEC> code;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) code.v[e] = k == 128 ? 0 : encode1(to_f(x[i].v[e]), inv, a.fmt);
+                    reinterpret_cast<Pack<uint8_t, VEC> *>(a.codes + r * a.C)[v] = code;
+                    if (v % (kGroup / VEC) == 0)
+                        a.scales[r * ((a.C + kGroup - 1) / kGroup) + v / (kGroup / VEC)] = (uint8_t)(k + 127);
+                }
+            }
+        }
+        if (live && t == 0) {
+            a.mean[r] = mean;
+            a.rstd[r] = rstd;
+        }
+    }
+}
+
+struct BwdArgs {
+    RowPtr x, dy, dx;
+    const uint8_t *codes, *scales;
+    int fmt;
+    const void *gamma;
+    int wdt;
+    bool wvec;
+    const float *mean, *rstd;
+    float *part;  // [gridDim.x][2][C]; NULL: no weight gradients
+    long long nrows;
+    int C, nvec, tpr;
+    float invC;
+};
+
+// Each thread adds up dgamma and dbeta of its own channels over the CTA's rows
+// in registers; the CTA writes one partial.  The next row's inputs are fetched
+// before this row's sums are formed.
+template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
+__global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
+    using V = Pack<T, VEC>;
+    using K = Pack<uint8_t, VEC>;
+    __shared__ float red[2][16][2];
+    __shared__ float fold[kCta ? 1 : 256 * NV * VEC];
+    const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
+    const int per = kCta ? 1 : 256 / tpr, sub = kCta ? 0 : threadIdx.x / tpr;
+    const int ng = (a.C + kGroup - 1) / kGroup;
+    float gw[NV][VEC], dg[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = i * tpr + t;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) gw[i][e] = dg[i][e] = db[i][e] = 0.f;
+        if (v < a.nvec) load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.wvec, 1.f, gw[i]);
+    }
+    V x[NV], dy[NV];      // of this row (kCkpt: codes and scale bytes instead of x)
+    K xc[NV];
+    uint32_t xs[NV];
+    float mean = 0.f, rstd = 0.f;
+    const long long step = (long long)gridDim.x * per;
+    auto fetch = [&](long long r) {  // rows past the last one, and channels past C, count as dy = 0
+        const bool live = r < a.nrows;
+        const V *dyr = reinterpret_cast<const V *>(a.dy(live ? r : 0));
+        const V *xr = kCkpt ? nullptr : reinterpret_cast<const V *>(a.x(live ? r : 0));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * tpr + t;
+            if (live && v < a.nvec) {
+                dy[i] = dyr[v];
+                if constexpr (kCkpt) {
+                    xc[i] = reinterpret_cast<const K *>(a.codes + r * a.C)[v];
+                    xs[i] = a.scales[r * ng + v / (kGroup / VEC)];
+                } else {
+                    x[i] = xr[v];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    dy[i].v[e] = from_f<T>(0.f);
+                    if constexpr (kCkpt) xc[i].v[e] = 0;
+                    else x[i].v[e] = from_f<T>(0.f);
+                }
+                if constexpr (kCkpt) xs[i] = 0;
+            }
+        }
+        mean = live ? a.mean[r] : 0.f;
+        rstd = live ? a.rstd[r] : 0.f;
+    };
+    int par = 0;
+    long long r0 = (long long)blockIdx.x * per;
+    if (r0 < a.nrows) fetch(r0 + sub);
+    for (; r0 < a.nrows; r0 += step) {
+        const long long r = r0 + sub;
+        float xh[NV][VEC], g[NV][VEC];
+        const float rs = rstd;
+        float sa = 0.f, sb = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float sc = 0.f;
+            if constexpr (kCkpt) sc = code_scale(xs[i]);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float xv;
+                if constexpr (kCkpt) xv = saturate_to<float>(decode1(xc[i].v[e], a.fmt) * sc);
+                else xv = to_f(x[i].v[e]);
+                xh[i][e] = (xv - mean) * rs;
+                const float d = to_f(dy[i].v[e]);
+                dg[i][e] = fmaf(d, xh[i][e], dg[i][e]);
+                db[i][e] += d;
+                g[i][e] = d * gw[i][e];
+                sa += g[i][e];
+                sb = fmaf(g[i][e], xh[i][e], sb);
+            }
+        }
+        if (r0 + step < a.nrows) fetch(r + step);
+        if constexpr (kCta) {  // a slot is written again two rows on, behind the barrier of the row between
+            sa = warp_sum(sa);
+            sb = warp_sum(sb);
+            if ((threadIdx.x & 31) == 0) {
+                red[par][threadIdx.x >> 5][0] = sa;
+                red[par][threadIdx.x >> 5][1] = sb;
+            }
+            __syncthreads();
+            sa = sb = 0.f;
+            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+                sa += red[par][w][0];
+                sb += red[par][w][1];
+            }
+            par ^= 1;
+        } else {
+            sa = lanes_sum(sa, tpr);
+            sb = lanes_sum(sb, tpr);
+        }
+        sa *= a.invC;
+        sb *= a.invC;
+        if (kCta || r < a.nrows) {
+            V *dxr = reinterpret_cast<V *>(a.dx(r));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = i * tpr + t;
+                if (v < a.nvec) {
+                    V o;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o.v[e] = from_f<T>((g[i][e] - sa - xh[i][e] * sb) * rs);
+                    dxr[v] = o;
+                }
+            }
+        }
+    }
+    if (!a.part) return;
+    float *pg = a.part + (size_t)blockIdx.x * 2 * a.C;
+    if constexpr (kCta) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = i * tpr + t;
+            if (v < a.nvec)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    pg[v * VEC + e] = dg[i][e];
+                    pg[a.C + v * VEC + e] = db[i][e];
+                }
+        }
+    } else {  // the CTA's rows side by side: fold[row of the CTA][channel], summed in row order
+        const int width = tpr * NV * VEC;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) fold[sub * width + (i * tpr + t) * VEC + e] = which ? db[i][e] : dg[i][e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.C; c += 256) {
+                float s = 0.f;
+                for (int p = 0; p < per; ++p) s += fold[p * width + c];
+                pg[which * a.C + c] = s;
+            }
+        }
+    }
+}
+
+// How a row is laid over threads: VEC elements per access, NV accesses per
+// thread, tpr threads (0: the row does not fit, use the kernels for any size).
+struct Spread {
+    int nvec, nv, tpr;
+};
+template <int VEC>
+Spread spread(int C, const int *nvs, int n) {  // nvs: the NV to choose from, ascending
+    Spread s{(C + VEC - 1) / VEC, 0, 0};
+    for (int i = 0; i < n && !s.nv; ++i)  // one warp's lanes
+        if (s.nvec <= 32 * nvs[i]) {
+            s.nv = nvs[i];
+            s.tpr = kGroup / VEC;  // a scale group never leaves its row's lanes
+            while (s.tpr * s.nv < s.nvec) s.tpr *= 2;
+        }
+    return s;
+}
+
+bool aligned16(const RowPtr &p, size_t row_bytes) {
+    return (((uintptr_t)p.data | (uintptr_t)p.stride | (uintptr_t)p.group_stride | row_bytes) & 15) == 0;
 }
 
 // Partial weight gradients of the backward: one per CTA, at most 64 MB.
@@ -168,29 +510,108 @@ int partials(long long nrows, int C) {
     return p < 1 ? 1 : (int)p;
 }
 
+// ---- forward ----
+template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
+prism_status run_fwd(const FwdArgs &a, cudaStream_t st) {
+    const int per = kCta ? 1 : 256 / a.tpr;
+    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? 2048 / a.tpr : 8);
+    k_norm_fwd<T, VEC, NV, kCta, kCkpt><<<(int)(need < most ? need : most), kCta ? a.tpr : 256, 0, st>>>(a);
+    PRISM_CUDA_OK(cudaGetLastError());
+    return PRISM_OK;
+}
+template <typename T, int VEC, bool kCkpt>
+prism_status fwd_spread(FwdArgs &a, cudaStream_t st) {
+    static const int nvs[] = {1, 2, 4, 6, 8};
+    const Spread s = spread<VEC>(a.C, nvs, 5);
+    a.nvec = s.nvec;
+    a.tpr = s.tpr;
+    switch (s.nv) {
+        case 1: return run_fwd<T, VEC, 1, false, kCkpt>(a, st);
+        case 2: return run_fwd<T, VEC, 2, false, kCkpt>(a, st);
+        case 4: return run_fwd<T, VEC, 4, false, kCkpt>(a, st);
+        case 6: return run_fwd<T, VEC, 6, false, kCkpt>(a, st);
+        case 8: return run_fwd<T, VEC, 8, false, kCkpt>(a, st);
+    }
+    // one row per CTA of 128 to 512 threads
+    a.tpr = 128;
+    while (a.tpr < 512 && a.tpr * 4 < a.nvec) a.tpr *= 2;
+    if (a.nvec <= a.tpr * 4) return run_fwd<T, VEC, 4, true, kCkpt>(a, st);
+    return run_fwd<T, VEC, 8, true, kCkpt>(a, st);
+}
+
 template <typename T>
-prism_status fwd_impl(const NormFwd &a, cudaStream_t st) {
-    const int grid = (int)(a.nrows < 148 * 8 ? a.nrows : 148 * 8);
-    k_norm_fwd_any<T><<<grid, kThreads, 0, st>>>(a.x, a.y, a.gamma, a.beta, a.wdt, a.mean, a.rstd, a.codes, a.scales,
-                                                 a.fmt, a.nrows, a.C, a.eps);
+prism_status fwd_impl(const NormFwd &n, cudaStream_t st) {
+    constexpr int VEC = 16 / sizeof(T);
+    const size_t row = (size_t)n.C * sizeof(T);
+    const bool vec = aligned16(n.x, row) && aligned16(n.y, row);
+    if (n.C <= 512 * 8 * (vec ? VEC : 1)) {
+        FwdArgs a{n.x, n.y, n.gamma, n.beta, n.wdt, (((uintptr_t)n.gamma | (uintptr_t)n.beta) & 15) == 0,
+                  n.mean, n.rstd, n.codes, n.scales, n.fmt, n.nrows, n.C, 0, 0, n.eps, 1.f / (float)n.C};
+        if (vec) return n.codes ? fwd_spread<T, VEC, true>(a, st) : fwd_spread<T, VEC, false>(a, st);
+        return n.codes ? fwd_spread<T, 1, true>(a, st) : fwd_spread<T, 1, false>(a, st);
+    }
+    const int grid = (int)(n.nrows < 148 * 8 ? n.nrows : 148 * 8);
+    k_norm_fwd_any<T><<<grid, kThreads, 0, st>>>(n.x, n.y, n.gamma, n.beta, n.wdt, n.mean, n.rstd, n.codes, n.scales,
+                                                 n.fmt, n.nrows, n.C, n.eps);
     PRISM_CUDA_OK(cudaGetLastError());
     return PRISM_OK;
 }
 
-template <typename T>
-prism_status bwd_impl(const NormBwd &a, cudaStream_t st) {
-    const Source<T> src{a.x, a.codes, a.scales, a.fmt, a.C};
-    const int P = partials(a.nrows, a.C);
-    if (a.nrows > 0) {
-        const int grid = (int)(a.nrows < 148 * 8 ? a.nrows : 148 * 8);
-        k_norm_dx_any<T><<<grid, kThreads, 0, st>>>(src, a.dy, a.dx, a.gamma, a.wdt, a.mean, a.rstd, a.nrows, a.C);
-        PRISM_CUDA_OK(cudaGetLastError());
+// ---- backward ----
+template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
+prism_status run_bwd(const BwdArgs &a, int P, cudaStream_t st) {
+    k_norm_bwd<T, VEC, NV, kCta, kCkpt><<<P, kCta ? a.tpr : 256, 0, st>>>(a);
+    PRISM_CUDA_OK(cudaGetLastError());
+    return PRISM_OK;
+}
+// P: partials allowed; on return the partials written
+template <typename T, int VEC, bool kCkpt>
+prism_status bwd_spread(BwdArgs &a, int &P, cudaStream_t st) {
+    static const int nvs[] = {1, 2};
+    const Spread s = spread<VEC>(a.C, nvs, 2);
+    a.nvec = s.nvec;
+    a.tpr = s.tpr;
+    if (s.nv) {
+        const long long need = (a.nrows + 256 / a.tpr - 1) / (256 / a.tpr);
+        if (P > need) P = (int)need;
+        return s.nv == 1 ? run_bwd<T, VEC, 1, false, kCkpt>(a, P, st) : run_bwd<T, VEC, 2, false, kCkpt>(a, P, st);
     }
-    if (a.dgamma || a.dbeta) {
-        k_norm_dw_any<T><<<dim3((a.C + kThreads - 1) / kThreads, P), kThreads, 0, st>>>(src, a.dy, a.mean, a.rstd,
-                                                                                        a.part, a.nrows, a.C);
-        PRISM_CUDA_OK(cudaGetLastError());
-        k_norm_dw_sum<<<(a.C + 31) / 32, kThreads, 0, st>>>(a.part, P, a.dgamma, a.dbeta, a.wdt, a.C);
+    a.tpr = 64;
+    while (a.tpr < 512 && a.tpr * 2 < a.nvec) a.tpr *= 2;
+    if (a.nvec <= a.tpr * 2) return run_bwd<T, VEC, 2, true, kCkpt>(a, P, st);
+    return run_bwd<T, VEC, 4, true, kCkpt>(a, P, st);
+}
+
+template <typename T>
+prism_status bwd_impl(const NormBwd &n, cudaStream_t st) {
+    constexpr int VEC = 16 / sizeof(T);
+    int P = partials(n.nrows, n.C);
+    float *part = n.dgamma || n.dbeta ? n.part : nullptr;
+    const size_t row = (size_t)n.C * sizeof(T);
+    // codes and scales are 16-byte aligned and packed: a row of a multiple of VEC codes is aligned to VEC
+    const bool vec = (n.codes ? n.C % VEC == 0 : aligned16(n.x, row)) && aligned16(n.dy, row) && aligned16(n.dx, row);
+    if (n.nrows > 0 && n.C <= 512 * 4 * (vec ? VEC : 1)) {
+        BwdArgs a{n.x, n.dy, n.dx, n.codes, n.scales, n.fmt, n.gamma, n.wdt, ((uintptr_t)n.gamma & 15) == 0,
+                  n.mean, n.rstd, part, n.nrows, n.C, 0, 0, 1.f / (float)n.C};
+        prism_status s;
+        if (vec) s = n.codes ? bwd_spread<T, VEC, true>(a, P, st) : bwd_spread<T, VEC, false>(a, P, st);
+        else s = n.codes ? bwd_spread<T, 1, true>(a, P, st) : bwd_spread<T, 1, false>(a, P, st);
+        if (s != PRISM_OK) return s;
+    } else {
+        const Source<T> src{n.x, n.codes, n.scales, n.fmt, n.C};
+        if (n.nrows > 0) {
+            const int grid = (int)(n.nrows < 148 * 8 ? n.nrows : 148 * 8);
+            k_norm_dx_any<T><<<grid, kThreads, 0, st>>>(src, n.dy, n.dx, n.gamma, n.wdt, n.mean, n.rstd, n.nrows, n.C);
+            PRISM_CUDA_OK(cudaGetLastError());
+        }
+        if (part) {
+            k_norm_dw_any<T><<<dim3((n.C + kThreads - 1) / kThreads, P), kThreads, 0, st>>>(src, n.dy, n.mean, n.rstd,
+                                                                                            part, n.nrows, n.C);
+            PRISM_CUDA_OK(cudaGetLastError());
+        }
+    }
+    if (part) {
+        k_norm_dw_sum<<<(n.C + 31) / 32, 1024, 0, st>>>(part, P, n.dgamma, n.dbeta, n.wdt, n.C);
         PRISM_CUDA_OK(cudaGetLastError());
     }
     return PRISM_OK;
