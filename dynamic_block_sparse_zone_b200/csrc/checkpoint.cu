@@ -1,6 +1,12 @@
 // checkpoint.cu -- activations in 8 bits between the forward and the backward
 // pass: codes and one power-of-two scale per 32 channels (rows.cuh has the
 // code's definition).
+//
+// HBM-bound: one read and one write of each value.  Every lane moves vectors
+// of 16 bytes (one element where rows are not aligned to that); the 32 / VEC
+// neighbouring lanes that hold a scale group agree on its exponent by
+// shuffles.  Four vectors per lane are in flight.  Rows that follow each other
+// without a gap, with whole groups in each, are taken as one long row.
 #include "rows.cuh"
 
 namespace prism {
@@ -10,69 +16,151 @@ using namespace rows;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kU = 4;  // vectors in flight per lane
 
-// One warp per group of 32 channels of a row, one channel per lane.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_ckpt_pack(RowPtr x, long long nrows, int C, uint8_t *__restrict__ codes,
-                                                        uint8_t *__restrict__ scales, int fmt) {
-    const int lane = threadIdx.x & 31, ng = (C + kGroup - 1) / kGroup;
-    const long long total = nrows * ng, step = (long long)gridDim.x * (kThreads / 32);
-    for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < total; it += step) {
-        const long long r = it / ng;
-        const int grp = (int)(it - r * ng), c = grp * kGroup + lane;
-        const float v = c < C ? to_f(reinterpret_cast<const T *>(x(r))[c]) : 0.f;
-        uint32_t top = __float_as_uint(fabsf(v));  // orders like the value; NaN above all
+struct CkptArgs {
+    RowPtr x;
+    uint8_t *codes, *scales;
+    int fmt;
+    long long nrows, nvec;  // rows, vectors per row
+    long long C;
+    int lanes;              // lanes per row (a power of two; 32: a warp walks along a row)
+};
+
+// The row and the vector in it of this lane's u-th access in warp item `it`.
+struct Place {
+    long long r, v;
+    bool in;
+};
+__device__ __forceinline__ Place place(const CkptArgs &a, long long it, long long per_row, int u) {
+    const int lane = threadIdx.x & 31;
+    Place p;
+    if (a.lanes == 32) {
+        p.r = per_row == 1 ? it : it / per_row;
+        p.v = (it - p.r * per_row) * (32 * kU) + u * 32 + lane;
+    } else {
+        p.r = (it * kU + u) * (32 / a.lanes) + lane / a.lanes;
+        p.v = lane & (a.lanes - 1);
+    }
+    p.in = p.r < a.nrows && p.v < a.nvec;
+    return p;
+}
+__device__ __forceinline__ long long items(const CkptArgs &a, long long &per_row) {
+    per_row = (a.nvec + 32 * kU - 1) / (32 * kU);
+    const long long rows_per_item = (long long)kU * (32 / a.lanes);
+    return a.lanes == 32 ? a.nrows * per_row : (a.nrows + rows_per_item - 1) / rows_per_item;
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptArgs a) {
+    constexpr int VP = (VEC + 1) / 2, kPer = kGroup / VEC;
+    long long per_row;
+    const long long n = items(a, per_row), ng = (a.C + kGroup - 1) / kGroup;
+    for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < n;
+         it += (long long)gridDim.x * (kThreads / 32)) {
+        Vec<T, VEC> raw[kU];
+        Place p[kU];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int k = code_exponent(__uint_as_float(top), fmt);
-        if (c < C) codes[r * C + c] = k == 128 ? 0 : encode1(v, code_inv_scale(k), fmt);
-        if (lane == 0) scales[r * ng + grp] = (uint8_t)(k + 127);
+        for (int u = 0; u < kU; ++u) {
+            p[u] = place(a, it, per_row, u);
+            if (p[u].in) raw[u].load(a.x(p[u].r), p[u].v);
+            else raw[u].zero();
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            f2 x[VP];
+#pragma unroll
+            for (int e = 0; e < VP; ++e) x[e] = raw[u].pair(e);
+            const int k = group_exponent<VEC>(top_of(x), a.fmt);
+            if (p[u].in) {
+                Codes<VEC> c;
+                c.encode(x, code_inv_scale(k), a.fmt);
+                c.store(a.codes + p[u].r * a.C, p[u].v);
+                if (p[u].v % kPer == 0) a.scales[p[u].r * ng + p[u].v / kPer] = (uint8_t)(k + 127);
+            }
+        }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_ckpt_unpack(const uint8_t *__restrict__ codes,
-                                                          const uint8_t *__restrict__ scales, RowPtr y, long long nrows,
-                                                          int C, int fmt) {
-    const int lane = threadIdx.x & 31, ng = (C + kGroup - 1) / kGroup;
-    const long long total = nrows * ng, step = (long long)gridDim.x * (kThreads / 32);
-    for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < total; it += step) {
-        const long long r = it / ng;
-        const int grp = (int)(it - r * ng), c = grp * kGroup + lane;
-        if (c < C)
-            reinterpret_cast<T *>(y(r))[c] =
-                from_f<T>(saturate_to<T>(decode1(codes[r * C + c], fmt) * code_scale(scales[r * ng + grp])));
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) k_ckpt_unpack(CkptArgs a) {
+    constexpr int VP = (VEC + 1) / 2, kPer = kGroup / VEC;
+    long long per_row;
+    const long long n = items(a, per_row), ng = (a.C + kGroup - 1) / kGroup;
+    for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < n;
+         it += (long long)gridDim.x * (kThreads / 32)) {
+        Codes<VEC> c[kU];
+        uint32_t sb[kU];
+        Place p[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            p[u] = place(a, it, per_row, u);
+            if (p[u].in) {
+                c[u].load(a.codes + p[u].r * a.C, p[u].v);
+                sb[u] = a.scales[p[u].r * ng + p[u].v / kPer];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (p[u].in) {
+                f2 x[VP];
+                c[u].template decode<T>(sb[u], a.fmt, x);
+                Vec<T, VEC> o;
+#pragma unroll
+                for (int e = 0; e < VP; ++e) o.set_pair(e, x[e]);
+                o.store(a.x(p[u].r), p[u].v);
+            }
     }
 }
 
-int grid_for(long long warps) {
-    const long long b = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    return (int)(b < 148 * 8 ? b : 148 * 8);
+template <typename T, int VEC, bool kPack>
+prism_status run(CkptArgs a, bool dense, cudaStream_t st) {
+    if (dense && a.C % kGroup == 0) {
+        a.C *= a.nrows;
+        a.nrows = 1;
+    }
+    a.nvec = (a.C + VEC - 1) / VEC;
+    a.lanes = kGroup / VEC;
+    while (a.lanes < 32 && a.lanes < a.nvec) a.lanes *= 2;
+    const long long per = (long long)kU * (32 / a.lanes);
+    const long long n = a.lanes == 32 ? a.nrows * ((a.nvec + 32 * kU - 1) / (32 * kU)) : (a.nrows + per - 1) / per;
+    const long long ctas = (n + kThreads / 32 - 1) / (kThreads / 32), most = 148 * 16;
+    const int grid = (int)(ctas < most ? ctas : most);
+    if constexpr (kPack) k_ckpt_pack<T, VEC><<<grid, kThreads, 0, st>>>(a);
+    else k_ckpt_unpack<T, VEC><<<grid, kThreads, 0, st>>>(a);
+    PRISM_CUDA_OK(cudaGetLastError());
+    return PRISM_OK;
+}
+
+template <typename T, bool kPack>
+prism_status run_type(const RowPtr &x, long long nrows, int C, const prism_ckpt &k, cudaStream_t st) {
+    constexpr int VEC = 16 / sizeof(T);
+    const CkptArgs a{x, static_cast<uint8_t *>(k.codes), static_cast<uint8_t *>(k.scales), k.format, nrows, 0, C, 0};
+    const long long row = (long long)C * sizeof(T);
+    const bool dense = nrows == 1 || (x.stride == row && (x.group == 0 || x.group >= nrows));
+    // a dense tensor of whole groups needs only its first element aligned
+    const bool vec = dense && C % kGroup == 0 ? ((uintptr_t)x.data & 15) == 0
+                                              : (((uintptr_t)x.data | x.stride | x.group_stride | row) & 15) == 0;
+    return vec ? run<T, VEC, kPack>(a, dense, st) : run<T, 1, kPack>(a, dense, st);
+}
+
+template <bool kPack>
+prism_status run_any(const RowPtr &x, int dtype, long long nrows, int C, const prism_ckpt &k, cudaStream_t st) {
+    if (nrows == 0) return PRISM_OK;
+    if (dtype == PRISM_BF16) return run_type<__nv_bfloat16, kPack>(x, nrows, C, k, st);
+    if (dtype == PRISM_FP16) return run_type<__half, kPack>(x, nrows, C, k, st);
+    return run_type<float, kPack>(x, nrows, C, k, st);
 }
 
 }  // namespace
 
 prism_status launch_ckpt_pack(const RowPtr &x, int dtype, long long nrows, int C, const prism_ckpt &k, cudaStream_t st) {
-    if (nrows == 0) return PRISM_OK;
-    auto *codes = static_cast<uint8_t *>(k.codes), *scales = static_cast<uint8_t *>(k.scales);
-    const int grid = grid_for(nrows * ((C + kGroup - 1) / kGroup));
-    if (dtype == PRISM_BF16) k_ckpt_pack<__nv_bfloat16><<<grid, kThreads, 0, st>>>(x, nrows, C, codes, scales, k.format);
-    else if (dtype == PRISM_FP16) k_ckpt_pack<__half><<<grid, kThreads, 0, st>>>(x, nrows, C, codes, scales, k.format);
-    else k_ckpt_pack<float><<<grid, kThreads, 0, st>>>(x, nrows, C, codes, scales, k.format);
-    PRISM_CUDA_OK(cudaGetLastError());
-    return PRISM_OK;
+    return run_any<true>(x, dtype, nrows, C, k, st);
 }
 
 prism_status launch_ckpt_unpack(const prism_ckpt &k, const RowPtr &y, int dtype, long long nrows, int C,
                                 cudaStream_t st) {
-    if (nrows == 0) return PRISM_OK;
-    const auto *codes = static_cast<const uint8_t *>(k.codes), *scales = static_cast<const uint8_t *>(k.scales);
-    const int grid = grid_for(nrows * ((C + kGroup - 1) / kGroup));
-    if (dtype == PRISM_BF16) k_ckpt_unpack<__nv_bfloat16><<<grid, kThreads, 0, st>>>(codes, scales, y, nrows, C, k.format);
-    else if (dtype == PRISM_FP16) k_ckpt_unpack<__half><<<grid, kThreads, 0, st>>>(codes, scales, y, nrows, C, k.format);
-    else k_ckpt_unpack<float><<<grid, kThreads, 0, st>>>(codes, scales, y, nrows, C, k.format);
-    PRISM_CUDA_OK(cudaGetLastError());
-    return PRISM_OK;
+    return run_any<false>(y, dtype, nrows, C, k, st);
 }
 
 }  // namespace prism

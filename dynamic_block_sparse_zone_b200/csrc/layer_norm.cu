@@ -180,28 +180,28 @@ __device__ __forceinline__ float lanes_sum(float v, int tpr) {
 
 // VEC weights from channel c0 on (NULL: `none` each); `vec`: 16-byte aligned
 template <int VEC>
-__device__ __forceinline__ void load_weights(const void *p, int dt, int c0, bool vec, float none, float (&w)[VEC]) {
+__device__ __forceinline__ void load_weights(const void *p, int dt, int c0, bool vec, float none,
+                                             f2 (&w)[(VEC + 1) / 2]) {
     if (!p) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = none;
+        for (int i = 0; i < (VEC + 1) / 2; ++i) w[i] = both(none);
     } else if (VEC > 1 && vec && dt == PRISM_FP32) {
 #pragma unroll
-        for (int e = 0; e < VEC; e += 4) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c0 + e));
-            w[e] = f.x;
-            if (VEC > 1) w[(e + 1) % VEC] = f.y, w[(e + 2) % VEC] = f.z, w[(e + 3) % VEC] = f.w;
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c0) + i);
+            w[2 * i] = make2(f.x, f.y);
+            w[2 * i + 1] = make2(f.z, f.w);
         }
     } else if (VEC == 8 && vec) {
         const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p) + c0));
         const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const uint16_t h = (uint16_t)(a[e / 2] >> (16 * (e & 1)));
-            w[e] = dt == PRISM_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
-        }
+        for (int i = 0; i < (VEC + 1) / 2; ++i)
+            w[i] = dt == PRISM_BF16 ? widen<__nv_bfloat16>(a[i % 4]) : widen<__half>(a[i % 4]);
     } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = weight_at(p, dt, c0 + e);
+        for (int i = 0; i < (VEC + 1) / 2; ++i)
+            w[i] = make2(weight_at(p, dt, c0 + 2 * i), VEC > 1 ? weight_at(p, dt, c0 + 2 * i + 1) : 0.f);
     }
 }
 
@@ -220,12 +220,12 @@ struct FwdArgs {
 
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
 __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_fwd(FwdArgs a) {
-    using V = Pack<T, VEC>;
+    constexpr int VP = (VEC + 1) / 2;
     __shared__ float red[2][2][16];
     const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
     const int per = kCta ? 1 : 256 / tpr, sub = kCta ? 0 : threadIdx.x / tpr;
     constexpr bool kKeep = NV * VEC <= 16;  // weights stay in registers; else they are read from L1 for each row
-    float gw[kKeep ? NV : 1][VEC], bw[kKeep ? NV : 1][VEC];
+    f2 gw[kKeep ? NV : 1][VP], bw[kKeep ? NV : 1][VP];
     if constexpr (kKeep) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_fwd(FwdArgs a) {
         }
     }
     int par = 0;
-    auto row_sum = [&](float s, int which) {
+    auto row_sum = [&](f2 s2, int which) {
+        float s = low(s2) + high(s2);
         if constexpr (kCta) {  // a slot is written again two rows on, behind a barrier of the row between
             s = warp_sum(s);
             if ((threadIdx.x & 31) == 0) red[par][which][threadIdx.x >> 5] = s;
@@ -249,69 +250,62 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_fwd(FwdArgs a) {
             return lanes_sum(s, tpr);
         }
     };
+    const int ng = (a.C + kGroup - 1) / kGroup;
     for (long long r0 = (long long)blockIdx.x * per; r0 < a.nrows; r0 += (long long)gridDim.x * per) {
         const long long r = r0 + sub;
         const bool live = kCta || r < a.nrows;
-        V x[NV];
-        const V *xr = reinterpret_cast<const V *>(a.x(live ? r : r0));
-        float s = 0.f;
+        Vec<T, VEC> raw[NV];
+        const char *xr = a.x(live ? r : r0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * tpr + t;
-            if (v < a.nvec) x[i] = xr[v];
-            else
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) x[i].v[e] = from_f<T>(0.f);
+            if (v < a.nvec) raw[i].load(xr, v);
+            else raw[i].zero();
         }
+        f2 x[NV][VP], s = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s += to_f(x[i].v[e]);
-        const float mean = row_sum(s, 0) * a.invC;
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i * tpr + t < a.nvec) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float d = to_f(x[i].v[e]) - mean;
-                    q = fmaf(d, d, q);
+            for (int e = 0; e < VP; ++e) {
+                x[i][e] = raw[i].pair(e);
+                s = add2(s, x[i][e]);
+            }
+            if constexpr (kCkpt) {
+                const int v = i * tpr + t, k = group_exponent<VEC>(top_of(x[i]), a.fmt);
+                if (live && v < a.nvec) {
+                    Codes<VEC> c;
+                    c.encode(x[i], code_inv_scale(k), a.fmt);
+                    c.store(a.codes + r * a.C, v);
+                    if (v % (kGroup / VEC) == 0) a.scales[r * ng + v / (kGroup / VEC)] = (uint8_t)(k + 127);
                 }
+            }
+        }
+        const float mean = row_sum(s, 0) * a.invC;
+        f2 q = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VP; ++e) {  // x becomes x - mean; what lies past the row becomes 0
+                const bool in = i * tpr + t < a.nvec;
+                x[i][e] = in ? add2(x[i][e], make2(-mean, VEC > 1 ? -mean : 0.f)) : 0;
+                q = fma2(x[i][e], x[i][e], q);
             }
         const float rstd = rsqrtf(row_sum(q, 1) * a.invC + a.eps);
         par ^= 1;
-        V *yr = reinterpret_cast<V *>(a.y(live ? r : r0));
+        char *yr = a.y(live ? r : r0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * tpr + t;
-            const bool in = live && v < a.nvec;
-            if (in) {
+            if (live && v < a.nvec) {
                 if constexpr (!kKeep) {
                     load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.wvec, 1.f, gw[0]);
                     load_weights<VEC>(a.beta, a.wdt, v * VEC, a.wvec, 0.f, bw[0]);
                 }
-                V o;
+                Vec<T, VEC> o;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    o.v[e] = from_f<T>(fmaf((to_f(x[i].v[e]) - mean) * rstd, gw[kKeep ? i : 0][e], bw[kKeep ? i : 0][e]));
-                yr[v] = o;
-            }
-            if constexpr (kCkpt) {  // 32 / VEC neighbouring lanes hold a scale group
-                uint32_t top = 0;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) top = max(top, __float_as_uint(fabsf(to_f(x[i].v[e]))));
-#pragma unroll
-                for (int o = 16 / VEC; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int k = code_exponent(__uint_as_float(top), a.fmt);
-                const float inv = code_inv_scale(k);
-                if (in) {
-                    Pack<uint8_t, VEC> code;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) code.v[e] = k == 128 ? 0 : encode1(to_f(x[i].v[e]), inv, a.fmt);
-                    reinterpret_cast<Pack<uint8_t, VEC> *>(a.codes + r * a.C)[v] = code;
-                    if (v % (kGroup / VEC) == 0)
-                        a.scales[r * ((a.C + kGroup - 1) / kGroup) + v / (kGroup / VEC)] = (uint8_t)(k + 127);
-                }
+                for (int e = 0; e < VP; ++e)
+                    o.set_pair(e, fma2(x[i][e], mul2(gw[kKeep ? i : 0][e], both(rstd)), bw[kKeep ? i : 0][e]));
+                o.store(yr, v);
             }
         }
         if (live && t == 0) {
@@ -340,49 +334,47 @@ struct BwdArgs {
 // before this row's sums are formed.
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
 __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
-    using V = Pack<T, VEC>;
-    using K = Pack<uint8_t, VEC>;
+    constexpr int VP = (VEC + 1) / 2;
     __shared__ float red[2][16][2];
     __shared__ float fold[kCta ? 1 : 256 * NV * VEC];
     const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
     const int per = kCta ? 1 : 256 / tpr, sub = kCta ? 0 : threadIdx.x / tpr;
     const int ng = (a.C + kGroup - 1) / kGroup;
-    float gw[NV][VEC], dg[NV][VEC], db[NV][VEC];
+    f2 gw[NV][VP], dg[NV][VP], db[NV][VP];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int v = i * tpr + t;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) gw[i][e] = dg[i][e] = db[i][e] = 0.f;
+        for (int e = 0; e < VP; ++e) gw[i][e] = dg[i][e] = db[i][e] = 0;
         if (v < a.nvec) load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.wvec, 1.f, gw[i]);
     }
-    V x[NV], dy[NV];      // of this row (kCkpt: codes and scale bytes instead of x)
-    K xc[NV];
+    Vec<T, VEC> x[NV], dy[NV];  // of this row (kCkpt: codes and scale bytes instead of x)
+    Codes<VEC> xc[NV];
     uint32_t xs[NV];
     float mean = 0.f, rstd = 0.f;
     const long long step = (long long)gridDim.x * per;
     auto fetch = [&](long long r) {  // rows past the last one, and channels past C, count as dy = 0
-        const bool live = r < a.nrows;
-        const V *dyr = reinterpret_cast<const V *>(a.dy(live ? r : 0));
-        const V *xr = kCkpt ? nullptr : reinterpret_cast<const V *>(a.x(live ? r : 0));
+        const bool live = kCta || r < a.nrows;
+        const char *dyr = a.dy(live ? r : 0), *xr = kCkpt ? nullptr : a.x(live ? r : 0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * tpr + t;
             if (live && v < a.nvec) {
-                dy[i] = dyr[v];
+                dy[i].load(dyr, v);
                 if constexpr (kCkpt) {
-                    xc[i] = reinterpret_cast<const K *>(a.codes + r * a.C)[v];
+                    xc[i].load(a.codes + r * a.C, v);
                     xs[i] = a.scales[r * ng + v / (kGroup / VEC)];
                 } else {
-                    x[i] = xr[v];
+                    x[i].load(xr, v);
                 }
             } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    dy[i].v[e] = from_f<T>(0.f);
-                    if constexpr (kCkpt) xc[i].v[e] = 0;
-                    else x[i].v[e] = from_f<T>(0.f);
+                dy[i].zero();
+                if constexpr (kCkpt) {
+                    xc[i].zero();
+                    xs[i] = 0;
+                } else {
+                    x[i].zero();
                 }
-                if constexpr (kCkpt) xs[i] = 0;
             }
         }
         mean = live ? a.mean[r] : 0.f;
@@ -393,28 +385,25 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
     if (r0 < a.nrows) fetch(r0 + sub);
     for (; r0 < a.nrows; r0 += step) {
         const long long r = r0 + sub;
-        float xh[NV][VEC], g[NV][VEC];
+        f2 xh[NV][VP], g[NV][VP], sa2 = 0, sb2 = 0;
         const float rs = rstd;
-        float sa = 0.f, sb = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float sc = 0.f;
-            if constexpr (kCkpt) sc = code_scale(xs[i]);
+            if constexpr (kCkpt) xc[i].template decode<float>(xs[i], a.fmt, xh[i]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float xv;
-                if constexpr (kCkpt) xv = saturate_to<float>(decode1(xc[i].v[e], a.fmt) * sc);
-                else xv = to_f(x[i].v[e]);
-                xh[i][e] = (xv - mean) * rs;
-                const float d = to_f(dy[i].v[e]);
-                dg[i][e] = fmaf(d, xh[i][e], dg[i][e]);
-                db[i][e] += d;
-                g[i][e] = d * gw[i][e];
-                sa += g[i][e];
-                sb = fmaf(g[i][e], xh[i][e], sb);
+            for (int e = 0; e < VP; ++e) {
+                if constexpr (!kCkpt) xh[i][e] = x[i].pair(e);
+                xh[i][e] = mul2(add2(xh[i][e], both(-mean)), both(rs));
+                const f2 d = dy[i].pair(e);
+                dg[i][e] = fma2(d, xh[i][e], dg[i][e]);
+                db[i][e] = add2(db[i][e], d);
+                g[i][e] = mul2(d, gw[i][e]);
+                sa2 = add2(sa2, g[i][e]);
+                sb2 = fma2(g[i][e], xh[i][e], sb2);
             }
         }
         if (r0 + step < a.nrows) fetch(r + step);
+        float sa = low(sa2) + high(sa2), sb = low(sb2) + high(sb2);
         if constexpr (kCta) {  // a slot is written again two rows on, behind the barrier of the row between
             sa = warp_sum(sa);
             sb = warp_sum(sb);
@@ -433,18 +422,18 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
             sa = lanes_sum(sa, tpr);
             sb = lanes_sum(sb, tpr);
         }
-        sa *= a.invC;
-        sb *= a.invC;
         if (kCta || r < a.nrows) {
-            V *dxr = reinterpret_cast<V *>(a.dx(r));
+            const f2 ma = both(-sa * a.invC), mb = both(-sb * a.invC);
+            char *dxr = a.dx(r);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int v = i * tpr + t;
                 if (v < a.nvec) {
-                    V o;
+                    Vec<T, VEC> o;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) o.v[e] = from_f<T>((g[i][e] - sa - xh[i][e] * sb) * rs);
-                    dxr[v] = o;
+                    for (int e = 0; e < VP; ++e)
+                        o.set_pair(e, mul2(fma2(xh[i][e], mb, add2(g[i][e], ma)), both(rs)));
+                    o.store(dxr, v);
                 }
             }
         }
@@ -458,8 +447,8 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
             if (v < a.nvec)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    pg[v * VEC + e] = dg[i][e];
-                    pg[a.C + v * VEC + e] = db[i][e];
+                    pg[v * VEC + e] = e & 1 ? high(dg[i][e / 2]) : low(dg[i][e / 2]);
+                    pg[a.C + v * VEC + e] = e & 1 ? high(db[i][e / 2]) : low(db[i][e / 2]);
                 }
         }
     } else {  // the CTA's rows side by side: fold[row of the CTA][channel], summed in row order
@@ -470,7 +459,10 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) fold[sub * width + (i * tpr + t) * VEC + e] = which ? db[i][e] : dg[i][e];
+                for (int e = 0; e < VEC; ++e) {
+                    const f2 p = which ? db[i][e / 2] : dg[i][e / 2];
+                    fold[sub * width + (i * tpr + t) * VEC + e] = e & 1 ? high(p) : low(p);
+                }
             __syncthreads();
             for (int c = threadIdx.x; c < a.C; c += 256) {
                 float s = 0.f;
@@ -521,22 +513,22 @@ prism_status run_fwd(const FwdArgs &a, cudaStream_t st) {
 }
 template <typename T, int VEC, bool kCkpt>
 prism_status fwd_spread(FwdArgs &a, cudaStream_t st) {
-    static const int nvs[] = {1, 2, 4, 6, 8};
-    const Spread s = spread<VEC>(a.C, nvs, 5);
+    static const int nvs[] = {1, 2, 3, 4, 6, 8};
+    const Spread s = spread<VEC>(a.C, nvs, 6);
     a.nvec = s.nvec;
     a.tpr = s.tpr;
     switch (s.nv) {
         case 1: return run_fwd<T, VEC, 1, false, kCkpt>(a, st);
         case 2: return run_fwd<T, VEC, 2, false, kCkpt>(a, st);
+        case 3: return run_fwd<T, VEC, 3, false, kCkpt>(a, st);
         case 4: return run_fwd<T, VEC, 4, false, kCkpt>(a, st);
         case 6: return run_fwd<T, VEC, 6, false, kCkpt>(a, st);
         case 8: return run_fwd<T, VEC, 8, false, kCkpt>(a, st);
     }
     // one row per CTA of 128 to 512 threads
-    a.tpr = 128;
-    while (a.tpr < 512 && a.tpr * 4 < a.nvec) a.tpr *= 2;
-    if (a.nvec <= a.tpr * 4) return run_fwd<T, VEC, 4, true, kCkpt>(a, st);
-    return run_fwd<T, VEC, 8, true, kCkpt>(a, st);
+    const int nv = a.nvec <= 512 * 4 ? 4 : 8;
+    a.tpr = ((a.nvec + nv - 1) / nv + 31) / 32 * 32;
+    return nv == 4 ? run_fwd<T, VEC, 4, true, kCkpt>(a, st) : run_fwd<T, VEC, 8, true, kCkpt>(a, st);
 }
 
 template <typename T>
@@ -576,11 +568,14 @@ prism_status bwd_spread(BwdArgs &a, int &P, cudaStream_t st) {
         if (P > need) P = (int)need;
         return s.nv == 1 ? run_bwd<T, VEC, 1, false, kCkpt>(a, P, st) : run_bwd<T, VEC, 2, false, kCkpt>(a, P, st);
     }
-    a.tpr = 64;
-    while (a.tpr < 512 && a.tpr * 2 < a.nvec) a.tpr *= 2;
-    if (a.nvec <= a.tpr * 2) return run_bwd<T, VEC, 2, true, kCkpt>(a, P, st);
-    return run_bwd<T, VEC, 4, true, kCkpt>(a, P, st);
+    // one row per CTA; 16 channels per thread at most (three packed fp32 sets of them stay in registers)
+    constexpr int kMost = VEC == 8 ? 2 : VEC == 4 ? 4 : 8;
+    const int nv = a.nvec <= 512 * 2 ? 2 : kMost;
+    a.tpr = ((a.nvec + nv - 1) / nv + 31) / 32 * 32;
+    return nv == 2 ? run_bwd<T, VEC, 2, true, kCkpt>(a, P, st) : run_bwd<T, VEC, kMost, true, kCkpt>(a, P, st);
 }
+template <int VEC>
+constexpr int kBwdMost = 512 * (VEC == 8 ? 2 : VEC == 4 ? 4 : 8) * VEC;  // channels that bwd_spread takes
 
 template <typename T>
 prism_status bwd_impl(const NormBwd &n, cudaStream_t st) {
@@ -590,7 +585,7 @@ prism_status bwd_impl(const NormBwd &n, cudaStream_t st) {
     const size_t row = (size_t)n.C * sizeof(T);
     // codes and scales are 16-byte aligned and packed: a row of a multiple of VEC codes is aligned to VEC
     const bool vec = (n.codes ? n.C % VEC == 0 : aligned16(n.x, row)) && aligned16(n.dy, row) && aligned16(n.dx, row);
-    if (n.nrows > 0 && n.C <= 512 * 4 * (vec ? VEC : 1)) {
+    if (n.nrows > 0 && n.C <= (vec ? kBwdMost<VEC> : kBwdMost<1>)) {
         BwdArgs a{n.x, n.dy, n.dx, n.codes, n.scales, n.fmt, n.gamma, n.wdt, ((uintptr_t)n.gamma & 15) == 0,
                   n.mean, n.rstd, part, n.nrows, n.C, 0, 0, 1.f / (float)n.C};
         prism_status s;

@@ -38,12 +38,6 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 template <>
 __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 
-// VEC elements moved as one access (16 bytes, or 1 element).
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-    T v[VEC];
-};
-
 // A weight of type prism_dtype `dt` as fp32.
 __device__ __forceinline__ float weight_at(const void *p, int dt, long long c) {
     if (dt == PRISM_FP32) return static_cast<const float *>(p)[c];
@@ -72,8 +66,9 @@ __device__ __forceinline__ int code_exponent(float amax, int fmt) {
     const int k = fmt == PRISM_CKPT_INT8 ? ex - 6 + (mant > 0x7e0000u) : ex - 8 + (mant > 0x600000u);
     return k < -127 ? -127 : k;
 }
-// 2^-k for k in [-127, 126]
-__device__ __forceinline__ float code_inv_scale(int k) { return __uint_as_float((uint32_t)(127 - k) << 23); }
+// 2^-k for k in [-127, 126]; 0 for k = 128 (a group that is not finite: its
+// codes say nothing)
+__device__ __forceinline__ float code_inv_scale(int k) { return k == 128 ? 0.f : __uint_as_float((uint32_t)(127 - k) << 23); }
 // 2^k of a scale byte
 __device__ __forceinline__ float code_scale(uint32_t byte) {
     if (byte == 255u) return __uint_as_float(0x7fc00000u);
@@ -92,7 +87,6 @@ template <typename T>
 __device__ __forceinline__ float saturate_to(float v) {  // NaN stays NaN
     return fabsf(v) > largest<T>() ? copysignf(largest<T>(), v) : v;
 }
-// A group with k = 128 (not finite) is given codes of 0.
 __device__ __forceinline__ uint8_t encode1(float x, float inv, int fmt) {
     const float y = x * inv;
     if (fmt == PRISM_CKPT_INT8) return (uint8_t)(int8_t)__float2int_rn(y);
@@ -102,6 +96,192 @@ __device__ __forceinline__ float decode1(uint8_t code, int fmt) {
     if (fmt == PRISM_CKPT_INT8) return (float)(int8_t)code;
     const __half_raw h = __nv_cvt_fp8_to_halfraw(code, __NV_E4M3);
     return __half2float(__half(h));
+}
+
+// ---- packed fp32 pairs (f32x2 arithmetic): one instruction for two values ----
+// The row kernels would be bound by instruction issue before HBM with one
+// instruction per value; with VEC = 1 the upper half idles.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 make2(float lo, float hi) {
+    return (f2)__float_as_uint(lo) | ((f2)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ f2 both(float v) { return make2(v, v); }
+__device__ __forceinline__ float low(f2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(f2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// two neighbouring elements in one word <-> a pair
+template <typename T>
+__device__ __forceinline__ f2 widen(uint32_t w);
+template <>
+__device__ __forceinline__ f2 widen<__nv_bfloat16>(uint32_t w) { return (f2)(w << 16) | ((f2)(w & 0xffff0000u) << 32); }
+template <>
+__device__ __forceinline__ f2 widen<__half>(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make2(f.x, f.y);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t narrow(f2 v);
+template <>
+__device__ __forceinline__ uint32_t narrow<__nv_bfloat16>(f2 v) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(low(v), high(v));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t narrow<__half>(f2 v) {
+    const __half2 h = __floats2half2_rn(low(v), high(v));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A vector access: VEC elements in W words, as VP pairs.
+template <typename T, int VEC>
+struct Vec {
+    static constexpr int VP = (VEC + 1) / 2, W = VEC * sizeof(T) >= 4 ? VEC * sizeof(T) / 4 : 1;
+    uint32_t w[W];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const char *row, long long v) {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 2) w[0] = reinterpret_cast<const uint16_t *>(row)[v];
+            else w[0] = reinterpret_cast<const uint32_t *>(row)[v];
+        } else {
+            static_assert(VEC * sizeof(T) == 16, "16-byte accesses");
+            const uint4 u = reinterpret_cast<const uint4 *>(row)[v];
+            w[0] = u.x, w[1 % W] = u.y, w[2 % W] = u.z, w[3 % W] = u.w;
+        }
+    }
+    __device__ __forceinline__ void store(char *row, long long v) const {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 2) reinterpret_cast<uint16_t *>(row)[v] = (uint16_t)w[0];
+            else reinterpret_cast<uint32_t *>(row)[v] = w[0];
+        } else {
+            reinterpret_cast<uint4 *>(row)[v] = make_uint4(w[0], w[1 % W], w[2 % W], w[3 % W]);
+        }
+    }
+    __device__ __forceinline__ f2 pair(int i) const {  // VEC = 1: (x, 0)
+        if constexpr (sizeof(T) == 4) return (f2)w[2 * i % W] | (VEC == 1 ? 0 : (f2)w[(2 * i + 1) % W] << 32);
+        else return widen<T>(w[i]);
+    }
+    __device__ __forceinline__ void set_pair(int i, f2 v) {
+        if constexpr (sizeof(T) == 4) {
+            w[2 * i % W] = (uint32_t)v;
+            if (VEC > 1) w[(2 * i + 1) % W] = (uint32_t)(v >> 32);
+        } else {
+            w[i] = narrow<T>(v);
+        }
+    }
+};
+
+// The 8-bit codes of a vector, one byte each.
+template <int VEC>
+struct Codes {
+    static constexpr int VP = (VEC + 1) / 2, W = (VEC + 3) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const uint8_t *row, long long v) {
+        if constexpr (VEC == 1) w[0] = row[v];
+        else if constexpr (VEC == 4) w[0] = reinterpret_cast<const uint32_t *>(row)[v];
+        else {
+            const uint2 u = reinterpret_cast<const uint2 *>(row)[v];
+            w[0] = u.x, w[1 % W] = u.y;
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t *row, long long v) const {
+        if constexpr (VEC == 1) row[v] = (uint8_t)w[0];
+        else if constexpr (VEC == 4) reinterpret_cast<uint32_t *>(row)[v] = w[0];
+        else reinterpret_cast<uint2 *>(row)[v] = make_uint2(w[0], w[1 % W]);
+    }
+    // x * inv to the nearest codes.  int8: adding 1.5 * 2^23 rounds to a whole
+    // number (|x inv| <= 127) and leaves its two's complement in the low byte.
+    __device__ __forceinline__ void encode(const f2 (&x)[VP], float inv, int fmt) {
+        if (fmt == PRISM_CKPT_INT8) {
+            f2 y[VP];
+#pragma unroll
+            for (int i = 0; i < VP; ++i) y[i] = fma2(x[i], both(inv), both(12582912.f));
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const f2 a = y[2 * i], b = y[(2 * i + 1) % VP];
+                const uint32_t lo = __byte_perm((uint32_t)a, (uint32_t)(a >> 32), 0x0040);
+                const uint32_t hi = __byte_perm((uint32_t)b, (uint32_t)(b >> 32), 0x0040);
+                w[i] = __byte_perm(lo, hi, 0x5410);
+            }
+        } else {
+            uint32_t h[VP];
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                const f2 y = mul2(x[i], both(inv));
+                h[i] = __nv_cvt_float2_to_fp8x2(make_float2(low(y), high(y)), __NV_SATFINITE, __NV_E4M3);
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = h[2 * i] | (h[(2 * i + 1) % VP] << 16);
+        }
+    }
+    // the values q 2^k of the codes, scale byte sb, held within T's range
+    template <typename T>
+    __device__ __forceinline__ void decode(uint32_t sb, int fmt, f2 (&x)[VP]) const {
+        const f2 sc = both(code_scale(sb));
+        if (fmt == PRISM_CKPT_INT8) {  // byte + 128 in the mantissa of 2^23
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const uint32_t u = w[i] ^ 0x80808080u;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (2 * i + j < VP) {
+                        const uint32_t lo = __byte_perm(u, 0x4b000000u, 0x7540 + 2 * j);
+                        const uint32_t hi = __byte_perm(u, 0x4b000000u, 0x7541 + 2 * j);
+                        x[(2 * i + j) % VP] = mul2(add2((f2)lo | ((f2)hi << 32), both(-8388736.f)), sc);
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+                const float2 f = __half22float2(__half2(h));
+                x[i] = mul2(make2(f.x, f.y), sc);
+            }
+        }
+        // 127 * 2^119 and 448 * 2^119 are finite; fp16 ends sooner
+        if (sb >= (sizeof(T) == 2 && largest<T>() < 1e5f ? 128u : 247u) && sb != 255u) {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) x[i] = make2(saturate_to<T>(low(x[i])), saturate_to<T>(high(x[i])));
+        }
+    }
+};
+
+// The largest magnitude of a vector's pairs, NaN if any is (max.NaN, three inputs).
+template <int VP>
+__device__ __forceinline__ float top_of(const f2 (&x)[VP]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < VP; ++i)
+        asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(low(x[i])), "f"(high(x[i])));
+    return m;
+}
+// A scale group's exponent from the 32 / VEC neighbouring lanes that hold it
+template <int VEC>
+__device__ __forceinline__ int group_exponent(float m, int fmt) {
+    uint32_t top = __float_as_uint(m) & 0x7fffffffu;  // orders like the value; NaN above all
+#pragma unroll
+    for (int o = 16 / VEC; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return code_exponent(__uint_as_float(top), fmt);
 }
 
 // ---- launchers (arguments checked by the caller) ----
