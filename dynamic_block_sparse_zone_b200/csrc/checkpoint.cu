@@ -3,7 +3,7 @@
 // code's definition).
 //
 // HBM-bound: one read and one write of each value.  Every lane moves vectors
-// of 16 bytes (one element where rows are not aligned to that); the 32 / VEC
+// of 16 bytes (two single elements where rows are not aligned to that); the 32 / VEC
 // neighbouring lanes that hold a scale group agree on its exponent by
 // shuffles.  Four vectors per lane are in flight.  Rows that follow each other
 // without a gap, with whole groups in each, are taken as one long row.
@@ -53,7 +53,7 @@ __device__ __forceinline__ long long items(const CkptArgs &a, long long &per_row
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptArgs a) {
-    constexpr int VP = (VEC + 1) / 2, kPer = kGroup / VEC;
+    constexpr int VP = VEC / 2, kPer = kGroup / VEC;
     long long per_row;
     const long long n = items(a, per_row), ng = (a.C + kGroup - 1) / kGroup;
     for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < n;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptArgs a) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             p[u] = place(a, it, per_row, u);
-            if (p[u].in) raw[u].load(a.x(p[u].r), p[u].v);
+            if (p[u].in) raw[u].load(a.x(p[u].r), p[u].v, a.C);
             else raw[u].zero();
         }
 #pragma unroll
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptArgs a) {
             if (p[u].in) {
                 Codes<VEC> c;
                 c.encode(x, code_inv_scale(k), a.fmt);
-                c.store(a.codes + p[u].r * a.C, p[u].v);
+                c.store(a.codes + p[u].r * a.C, p[u].v, a.C);
                 if (p[u].v % kPer == 0) a.scales[p[u].r * ng + p[u].v / kPer] = (uint8_t)(k + 127);
             }
         }
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptArgs a) {
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) k_ckpt_unpack(CkptArgs a) {
-    constexpr int VP = (VEC + 1) / 2, kPer = kGroup / VEC;
+    constexpr int VP = VEC / 2, kPer = kGroup / VEC;
     long long per_row;
     const long long n = items(a, per_row), ng = (a.C + kGroup - 1) / kGroup;
     for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < n;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_unpack(CkptArgs a) {
         for (int u = 0; u < kU; ++u) {
             p[u] = place(a, it, per_row, u);
             if (p[u].in) {
-                c[u].load(a.codes + p[u].r * a.C, p[u].v);
+                c[u].load(a.codes + p[u].r * a.C, p[u].v, a.C);
                 sb[u] = a.scales[p[u].r * ng + p[u].v / kPer];
             }
         }
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_unpack(CkptArgs a) {
                 Vec<T, VEC> o;
 #pragma unroll
                 for (int e = 0; e < VP; ++e) o.set_pair(e, x[e]);
-                o.store(a.x(p[u].r), p[u].v);
+                o.store(a.x(p[u].r), p[u].v, a.C);
             }
     }
 }
@@ -141,7 +141,7 @@ prism_status run_type(const RowPtr &x, long long nrows, int C, const prism_ckpt 
     // a dense tensor of whole groups needs only its first element aligned
     const bool vec = dense && C % kGroup == 0 ? ((uintptr_t)x.data & 15) == 0
                                               : (((uintptr_t)x.data | x.stride | x.group_stride | row) & 15) == 0;
-    return vec ? run<T, VEC, kPack>(a, dense, st) : run<T, 1, kPack>(a, dense, st);
+    return vec ? run<T, VEC, kPack>(a, dense, st) : run<T, 2, kPack>(a, dense, st);
 }
 
 template <bool kPack>

@@ -10,6 +10,8 @@
 // second look at the row), not from squares, so an offset costs no digits.
 // The weight gradients are summed in a fixed order: every run gives the same
 // bits.
+#include <atomic>
+
 #include "rows.cuh"
 
 namespace prism {
@@ -165,11 +167,16 @@ __global__ void __launch_bounds__(1024) k_norm_dw_sum(const float *__restrict__ 
 
 // ---------------------------------------------------------------------------
 // Rows held in registers: one read of each input, one write of each output
-// (the floor of these HBM-bound operators).  A row's nvec vectors of VEC
+// (the floor of these HBM-bound operators).  A row's nvec pieces of VEC
 // elements are spread over `tpr` threads, NV each: lanes of one warp (tpr <=
 // 32, a power of two, 256 / tpr rows per CTA; only shuffles between the lanes)
 // or the whole CTA (one row at a time).  Every thread keeps its channels over
 // all of the rows that it takes, so weights and their gradients stay put.
+//
+// The grid is resident and walks the rows.  A row's chain (fetch, one or two
+// reductions, write) is long against its share of the bandwidth, so the rows
+// to come are fetched kS - 1 ahead by cp.async, each thread into slots of its
+// own (no barrier): what is in flight does not cost registers.
 // ---------------------------------------------------------------------------
 
 // tpr lanes' sum, in each of them
@@ -180,12 +187,12 @@ __device__ __forceinline__ float lanes_sum(float v, int tpr) {
 
 // VEC weights from channel c0 on (NULL: `none` each); `vec`: 16-byte aligned
 template <int VEC>
-__device__ __forceinline__ void load_weights(const void *p, int dt, int c0, bool vec, float none,
-                                             f2 (&w)[(VEC + 1) / 2]) {
+__device__ __forceinline__ void load_weights(const void *p, int dt, int c0, int C, bool vec, float none,
+                                             f2 (&w)[VEC / 2]) {
     if (!p) {
 #pragma unroll
-        for (int i = 0; i < (VEC + 1) / 2; ++i) w[i] = both(none);
-    } else if (VEC > 1 && vec && dt == PRISM_FP32) {
+        for (int i = 0; i < VEC / 2; ++i) w[i] = both(none);
+    } else if (VEC > 2 && vec && dt == PRISM_FP32) {
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i) {
             const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c0) + i);
@@ -196,14 +203,20 @@ __device__ __forceinline__ void load_weights(const void *p, int dt, int c0, bool
         const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p) + c0));
         const uint32_t a[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < (VEC + 1) / 2; ++i)
+        for (int i = 0; i < VEC / 2; ++i)
             w[i] = dt == PRISM_BF16 ? widen<__nv_bfloat16>(a[i % 4]) : widen<__half>(a[i % 4]);
     } else {
 #pragma unroll
-        for (int i = 0; i < (VEC + 1) / 2; ++i)
-            w[i] = make2(weight_at(p, dt, c0 + 2 * i), VEC > 1 ? weight_at(p, dt, c0 + 2 * i + 1) : 0.f);
+        for (int i = 0; i < VEC / 2; ++i) {
+            const int c = c0 + 2 * i;
+            w[i] = make2(weight_at(p, dt, c), c + 1 < C ? weight_at(p, dt, c + 1) : 0.f);
+        }
     }
 }
+
+// kS: rows in a thread's ring, by what a thread holds per row (bytes); at 512
+// to 1024 threads per SM this keeps 64 to 128 KB in flight.
+constexpr int ring(int bytes) { return bytes <= 64 ? 4 : bytes <= 96 ? 3 : 2; }
 
 struct FwdArgs {
     RowPtr x, y;
@@ -219,24 +232,63 @@ struct FwdArgs {
 };
 
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
-__global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_fwd(FwdArgs a) {
-    constexpr int VP = (VEC + 1) / 2;
+__global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_fwd(FwdArgs a) {
+    constexpr int VP = VEC / 2, kS = ring(NV * 16);
+    constexpr bool kRing = VEC * sizeof(T) == 16;
+    // weights stay in registers, or (more than 16 channels per thread) in shared memory as fp32
+    constexpr bool kKeep = NV * VEC <= 16;
+    extern __shared__ uint4 slots[];  // [kS][NV][threads] if kRing, then gamma and beta unless kKeep
     __shared__ float red[2][2][16];
     const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
     const int per = kCta ? 1 : 256 / tpr, sub = kCta ? 0 : threadIdx.x / tpr;
-    constexpr bool kKeep = NV * VEC <= 16;  // weights stay in registers; else they are read from L1 for each row
     f2 gw[kKeep ? NV : 1][VP], bw[kKeep ? NV : 1][VP];
+    f2 *wsm = reinterpret_cast<f2 *>(slots + (kRing ? kS * NV * blockDim.x : 0));  // [2][nvec][VP]
+    const long long step = (long long)gridDim.x * per, xinc = step * a.x.stride, yinc = step * a.y.stride;
+    auto slot = [&](int s, int i) -> uint4 & { return slots[(s * NV + i) * blockDim.x + threadIdx.x]; };
+    long long r0 = (long long)blockIdx.x * per;
+    RowWalk xw, yw;  // the next row to fetch, the row to write
+    long long xr = r0 + sub;
+    if (xr < a.nrows) {
+        xw.start(a.x, xr);
+        yw.start(a.y, xr);
+    }
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) in[i] = i * tpr + t < a.nvec;
+    auto issue = [&](int s) {
+        if (xr < a.nrows) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) copy_async<16>(&slot(s, i), xw.p + (i * tpr + t) * 16);
+        }
+        copy_commit();
+        xr += step;
+        if (xr < a.nrows) xw.next(a.x, xinc, xr);
+    };
+    if constexpr (kRing) {
+#pragma unroll
+        for (int s = 0; s < kS - 1; ++s) issue(s);
+    }
     if constexpr (kKeep) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = i * tpr + t;
-            if (v < a.nvec) {
-                load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.wvec, 1.f, gw[i]);
-                load_weights<VEC>(a.beta, a.wdt, v * VEC, a.wvec, 0.f, bw[i]);
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                load_weights<VEC>(a.gamma, a.wdt, (i * tpr + t) * VEC, a.C, a.wvec, 1.f, gw[i]);
+                load_weights<VEC>(a.beta, a.wdt, (i * tpr + t) * VEC, a.C, a.wvec, 0.f, bw[i]);
             }
+    } else {
+        for (int v = threadIdx.x; v < a.nvec; v += blockDim.x) {
+            f2 w[VP];
+            load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.C, a.wvec, 1.f, w);
+#pragma unroll
+            for (int e = 0; e < VP; ++e) wsm[v * VP + e] = w[e];
+            load_weights<VEC>(a.beta, a.wdt, v * VEC, a.C, a.wvec, 0.f, w);
+#pragma unroll
+            for (int e = 0; e < VP; ++e) wsm[(a.nvec + v) * VP + e] = w[e];
         }
+        __syncthreads();
     }
-    int par = 0;
+    int par = 0, cur = 0;
     auto row_sum = [&](f2 s2, int which) {
         float s = low(s2) + high(s2);
         if constexpr (kCta) {  // a slot is written again two rows on, behind a barrier of the row between
@@ -251,31 +303,40 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_fwd(FwdArgs a) {
         }
     };
     const int ng = (a.C + kGroup - 1) / kGroup;
-    for (long long r0 = (long long)blockIdx.x * per; r0 < a.nrows; r0 += (long long)gridDim.x * per) {
+    for (; r0 < a.nrows; r0 += step) {
         const long long r = r0 + sub;
         const bool live = kCta || r < a.nrows;
-        Vec<T, VEC> raw[NV];
-        const char *xr = a.x(live ? r : r0);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = i * tpr + t;
-            if (v < a.nvec) raw[i].load(xr, v);
-            else raw[i].zero();
-        }
         f2 x[NV][VP], s = 0;
+        if constexpr (kRing) copy_wait<kS - 2>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            Vec<T, VEC> raw;
+            raw.zero();
+            if (in[i] && live) {
+                if constexpr (kRing) raw.set(slot(cur, i));
+                else raw.load(xw.p, i * tpr + t, a.C);
+            }
 #pragma unroll
             for (int e = 0; e < VP; ++e) {
-                x[i][e] = raw[i].pair(e);
+                x[i][e] = raw.pair(e);
                 s = add2(s, x[i][e]);
             }
-            if constexpr (kCkpt) {
+        }
+        if constexpr (kRing) {  // into the slots that the row before has been read from
+            issue(cur == 0 ? kS - 1 : cur - 1);
+            cur = cur == kS - 1 ? 0 : cur + 1;
+        } else {
+            xr += step;
+            if (xr < a.nrows) xw.next(a.x, xinc, xr);
+        }
+        if constexpr (kCkpt) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
                 const int v = i * tpr + t, k = group_exponent<VEC>(top_of(x[i]), a.fmt);
-                if (live && v < a.nvec) {
+                if (in[i] && live) {
                     Codes<VEC> c;
                     c.encode(x[i], code_inv_scale(k), a.fmt);
-                    c.store(a.codes + r * a.C, v);
+                    c.store(a.codes + r * a.C, v, a.C);
                     if (v % (kGroup / VEC) == 0) a.scales[r * ng + v / (kGroup / VEC)] = (uint8_t)(k + 127);
                 }
             }
@@ -283,36 +344,40 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_fwd(FwdArgs a) {
         const float mean = row_sum(s, 0) * a.invC;
         f2 q = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {  // x becomes x - mean; what lies past the row stays 0
+            const float m0 = in[i] ? -mean : 0.f;
+            const f2 m = make2(m0, VEC == 2 && 2 * (i * tpr + t) + 1 >= a.C ? 0.f : m0);
 #pragma unroll
-            for (int e = 0; e < VP; ++e) {  // x becomes x - mean; what lies past the row becomes 0
-                const bool in = i * tpr + t < a.nvec;
-                x[i][e] = in ? add2(x[i][e], make2(-mean, VEC > 1 ? -mean : 0.f)) : 0;
+            for (int e = 0; e < VP; ++e) {
+                x[i][e] = add2(x[i][e], m);
                 q = fma2(x[i][e], x[i][e], q);
             }
+        }
         const float rstd = rsqrtf(row_sum(q, 1) * a.invC + a.eps);
         par ^= 1;
-        char *yr = a.y(live ? r : r0);
+        if (live) {
+            const f2 rs = both(rstd);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = i * tpr + t;
-            if (live && v < a.nvec) {
-                if constexpr (!kKeep) {
-                    load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.wvec, 1.f, gw[0]);
-                    load_weights<VEC>(a.beta, a.wdt, v * VEC, a.wvec, 0.f, bw[0]);
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+                    const int v = i * tpr + t;
+                    Vec<T, VEC> o;
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) {
+                        const f2 g = kKeep ? gw[kKeep ? i : 0][e] : wsm[v * VP + e];
+                        const f2 b = kKeep ? bw[kKeep ? i : 0][e] : wsm[(a.nvec + v) * VP + e];
+                        o.set_pair(e, fma2(x[i][e], mul2(g, rs), b));
+                    }
+                    o.store(yw.p, v, a.C);
                 }
-                Vec<T, VEC> o;
-#pragma unroll
-                for (int e = 0; e < VP; ++e)
-                    o.set_pair(e, fma2(x[i][e], mul2(gw[kKeep ? i : 0][e], both(rstd)), bw[kKeep ? i : 0][e]));
-                o.store(yr, v);
+            if (t == 0) {
+                a.mean[r] = mean;
+                a.rstd[r] = rstd;
             }
-        }
-        if (live && t == 0) {
-            a.mean[r] = mean;
-            a.rstd[r] = rstd;
+            if (r + step < a.nrows) yw.next(a.y, yinc, r + step);
         }
     }
+    if constexpr (kRing) copy_wait<0>();
 }
 
 struct BwdArgs {
@@ -330,71 +395,123 @@ struct BwdArgs {
 };
 
 // Each thread adds up dgamma and dbeta of its own channels over the CTA's rows
-// in registers; the CTA writes one partial.  The next row's inputs are fetched
-// before this row's sums are formed.
+// in registers; the CTA writes one partial.
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
-__global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
-    constexpr int VP = (VEC + 1) / 2;
+__global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(BwdArgs a) {
+    constexpr int VP = VEC / 2, kS = ring(NV * 32);
+    constexpr bool kRing = VEC * sizeof(T) == 16;
+    extern __shared__ uint4 slots[];  // [kS][2 NV][threads]: dy, then x or its codes
     __shared__ float red[2][16][2];
     __shared__ float fold[kCta ? 1 : 256 * NV * VEC];
     const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
     const int per = kCta ? 1 : 256 / tpr, sub = kCta ? 0 : threadIdx.x / tpr;
     const int ng = (a.C + kGroup - 1) / kGroup;
-    f2 gw[NV][VP], dg[NV][VP], db[NV][VP];
+    const long long step = (long long)gridDim.x * per;
+    const long long dyinc = step * a.dy.stride, xinc = step * (kCkpt ? a.C : a.x.stride), dxinc = step * a.dx.stride;
+    auto slot = [&](int s, int i) -> uint4 & { return slots[(s * 2 * NV + i) * blockDim.x + threadIdx.x]; };
+    bool in[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = i * tpr + t;
-#pragma unroll
-        for (int e = 0; e < VP; ++e) gw[i][e] = dg[i][e] = db[i][e] = 0;
-        if (v < a.nvec) load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.wvec, 1.f, gw[i]);
+    for (int i = 0; i < NV; ++i) in[i] = i * tpr + t < a.nvec;
+    long long r0 = (long long)blockIdx.x * per;
+    RowWalk dyw, xw, dxw;  // the next row to fetch (kCkpt: xw walks the codes), the row to write
+    long long fr = r0 + sub;
+    if (fr < a.nrows) {
+        dyw.start(a.dy, fr);
+        if constexpr (kCkpt) xw.p = (char *)a.codes + fr * a.C;
+        else xw.start(a.x, fr);
+        dxw.start(a.dx, fr);
     }
-    Vec<T, VEC> x[NV], dy[NV];  // of this row (kCkpt: codes and scale bytes instead of x)
-    Codes<VEC> xc[NV];
+    auto advance = [&]() {
+        fr += step;
+        if (fr < a.nrows) {
+            dyw.next(a.dy, dyinc, fr);
+            if constexpr (kCkpt) xw.p += xinc;
+            else xw.next(a.x, xinc, fr);
+        }
+    };
+    auto issue = [&](int s) {
+        if (fr < a.nrows) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+                    copy_async<16>(&slot(s, i), dyw.p + (i * tpr + t) * 16);
+                    if constexpr (kCkpt) copy_async<VEC>(&slot(s, NV + i), xw.p + (i * tpr + t) * VEC);
+                    else copy_async<16>(&slot(s, NV + i), xw.p + (i * tpr + t) * 16);
+                }
+        }
+        copy_commit();
+        advance();
+    };
+    // what has no slots comes one row ahead in registers
+    Vec<T, VEC> ndy[kRing ? 1 : NV], nx[kRing || kCkpt ? 1 : NV];
+    Codes<VEC> nc[kRing || !kCkpt ? 1 : NV];
     uint32_t xs[NV];
     float mean = 0.f, rstd = 0.f;
-    const long long step = (long long)gridDim.x * per;
-    auto fetch = [&](long long r) {  // rows past the last one, and channels past C, count as dy = 0
-        const bool live = kCta || r < a.nrows;
-        const char *dyr = a.dy(live ? r : 0), *xr = kCkpt ? nullptr : a.x(live ? r : 0);
+    auto ahead = [&](long long r) {  // rows past the last one, and channels past C, count as dy = 0
+        const bool live = r < a.nrows;
+        mean = live ? a.mean[r] : 0.f;
+        rstd = live ? a.rstd[r] : 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = i * tpr + t;
-            if (live && v < a.nvec) {
-                dy[i].load(dyr, v);
-                if constexpr (kCkpt) {
-                    xc[i].load(a.codes + r * a.C, v);
-                    xs[i] = a.scales[r * ng + v / (kGroup / VEC)];
-                } else {
-                    x[i].load(xr, v);
-                }
-            } else {
-                dy[i].zero();
-                if constexpr (kCkpt) {
-                    xc[i].zero();
-                    xs[i] = 0;
-                } else {
-                    x[i].zero();
+            if constexpr (kCkpt) xs[i] = live && in[i] ? a.scales[r * ng + v / (kGroup / VEC)] : 0u;
+            if constexpr (!kRing) {
+                ndy[i].zero();
+                if constexpr (kCkpt) nc[i].zero();
+                else nx[i].zero();
+                if (live && in[i]) {
+                    ndy[i].load(dyw.p, v, a.C);
+                    if constexpr (kCkpt) nc[i].load((const uint8_t *)xw.p, v, a.C);
+                    else nx[i].load(xw.p, v, a.C);
                 }
             }
         }
-        mean = live ? a.mean[r] : 0.f;
-        rstd = live ? a.rstd[r] : 0.f;
+        if constexpr (!kRing) advance();
     };
-    int par = 0;
-    long long r0 = (long long)blockIdx.x * per;
-    if (r0 < a.nrows) fetch(r0 + sub);
+    if constexpr (kRing) {
+#pragma unroll
+        for (int s = 0; s < kS - 1; ++s) issue(s);
+    }
+    f2 gw[NV][VP], dg[NV][VP], db[NV][VP];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int e = 0; e < VP; ++e) gw[i][e] = dg[i][e] = db[i][e] = 0;
+        if (in[i]) load_weights<VEC>(a.gamma, a.wdt, (i * tpr + t) * VEC, a.C, a.wvec, 1.f, gw[i]);
+    }
+    int par = 0, cur = 0;
+    ahead(r0 + sub);
     for (; r0 < a.nrows; r0 += step) {
         const long long r = r0 + sub;
+        const bool live = kCta || r < a.nrows;
         f2 xh[NV][VP], g[NV][VP], sa2 = 0, sb2 = 0;
-        const float rs = rstd;
+        const f2 rs = both(rstd), mm = both(-mean);
+        if constexpr (kRing) copy_wait<kS - 2>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if constexpr (kCkpt) xc[i].template decode<float>(xs[i], a.fmt, xh[i]);
+            const bool use = live && in[i];
+            Vec<T, VEC> dy;
+            dy.zero();
+            if constexpr (!kRing) dy = ndy[i];
+            else if (use) dy.set(slot(cur, i));
+            if constexpr (kCkpt) {
+                Codes<VEC> c;
+                c.zero();
+                if constexpr (!kRing) c = nc[i];
+                else if (use) c.load(reinterpret_cast<const uint8_t *>(&slot(cur, NV + i)), 0, VEC);
+                c.template decode<float>(xs[i], a.fmt, xh[i]);
+            } else {
+                Vec<T, VEC> x;
+                x.zero();
+                if constexpr (!kRing) x = nx[i];
+                else if (use) x.set(slot(cur, NV + i));
+#pragma unroll
+                for (int e = 0; e < VP; ++e) xh[i][e] = x.pair(e);
+            }
 #pragma unroll
             for (int e = 0; e < VP; ++e) {
-                if constexpr (!kCkpt) xh[i][e] = x[i].pair(e);
-                xh[i][e] = mul2(add2(xh[i][e], both(-mean)), both(rs));
-                const f2 d = dy[i].pair(e);
+                xh[i][e] = mul2(add2(xh[i][e], mm), rs);
+                const f2 d = dy.pair(e);
                 dg[i][e] = fma2(d, xh[i][e], dg[i][e]);
                 db[i][e] = add2(db[i][e], d);
                 g[i][e] = mul2(d, gw[i][e]);
@@ -402,7 +519,11 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
                 sb2 = fma2(g[i][e], xh[i][e], sb2);
             }
         }
-        if (r0 + step < a.nrows) fetch(r + step);
+        if constexpr (kRing) {  // into the slots that the row before has been read from
+            issue(cur == 0 ? kS - 1 : cur - 1);
+            cur = cur == kS - 1 ? 0 : cur + 1;
+        }
+        ahead(r + step);
         float sa = low(sa2) + high(sa2), sb = low(sb2) + high(sb2);
         if constexpr (kCta) {  // a slot is written again two rows on, behind the barrier of the row between
             sa = warp_sum(sa);
@@ -422,35 +543,34 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
             sa = lanes_sum(sa, tpr);
             sb = lanes_sum(sb, tpr);
         }
-        if (kCta || r < a.nrows) {
+        if (live) {
             const f2 ma = both(-sa * a.invC), mb = both(-sb * a.invC);
-            char *dxr = a.dx(r);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = i * tpr + t;
-                if (v < a.nvec) {
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
                     Vec<T, VEC> o;
 #pragma unroll
                     for (int e = 0; e < VP; ++e)
-                        o.set_pair(e, mul2(fma2(xh[i][e], mb, add2(g[i][e], ma)), both(rs)));
-                    o.store(dxr, v);
+                        o.set_pair(e, mul2(fma2(xh[i][e], mb, add2(g[i][e], ma)), rs));
+                    o.store(dxw.p, i * tpr + t, a.C);
                 }
-            }
+            if (r + step < a.nrows) dxw.next(a.dx, dxinc, r + step);
         }
     }
+    if constexpr (kRing) copy_wait<0>();
     if (!a.part) return;
     float *pg = a.part + (size_t)blockIdx.x * 2 * a.C;
     if constexpr (kCta) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = i * tpr + t;
-            if (v < a.nvec)
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    pg[v * VEC + e] = e & 1 ? high(dg[i][e / 2]) : low(dg[i][e / 2]);
-                    pg[a.C + v * VEC + e] = e & 1 ? high(db[i][e / 2]) : low(db[i][e / 2]);
+            for (int e = 0; e < VEC; ++e) {
+                const int c = (i * tpr + t) * VEC + e;
+                if (c < a.C) {
+                    pg[c] = e & 1 ? high(dg[i][e / 2]) : low(dg[i][e / 2]);
+                    pg[a.C + c] = e & 1 ? high(db[i][e / 2]) : low(db[i][e / 2]);
                 }
-        }
+            }
     } else {  // the CTA's rows side by side: fold[row of the CTA][channel], summed in row order
         const int width = tpr * NV * VEC;
 #pragma unroll
@@ -473,21 +593,40 @@ __global__ void __launch_bounds__(kCta ? 512 : 256) k_norm_bwd(BwdArgs a) {
     }
 }
 
-// How a row is laid over threads: VEC elements per access, NV accesses per
-// thread, tpr threads (0: the row does not fit, use the kernels for any size).
+// How a row is laid over one warp's lanes: NV pieces per lane, tpr lanes (nv =
+// 0: it does not fit).  nvs: the NV to choose from, ascending.
 struct Spread {
     int nvec, nv, tpr;
 };
-template <int VEC>
-Spread spread(int C, const int *nvs, int n) {  // nvs: the NV to choose from, ascending
+template <int VEC, int N>
+Spread spread(int C, const int (&nvs)[N]) {
     Spread s{(C + VEC - 1) / VEC, 0, 0};
-    for (int i = 0; i < n && !s.nv; ++i)  // one warp's lanes
+    for (int i = 0; i < N && !s.nv; ++i)
         if (s.nvec <= 32 * nvs[i]) {
             s.nv = nvs[i];
             s.tpr = kGroup / VEC;  // a scale group never leaves its row's lanes
             while (s.tpr * s.nv < s.nvec) s.tpr *= 2;
         }
     return s;
+}
+
+// Launches with dynamic shared memory; above 48 KB it has to be asked for,
+// once per kernel and device.
+template <typename Args>
+prism_status launch(void (*kernel)(Args), const Args &a, int grid, int threads, size_t smem,
+                    std::atomic<unsigned long long> &asked, cudaStream_t st) {
+    if (smem > 48 * 1024 - 1024) {  // the kernels' static shared memory counts too
+        int dev = 0;
+        PRISM_CUDA_OK(cudaGetDevice(&dev));
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (!(asked.load(std::memory_order_relaxed) & bit)) {
+            PRISM_CUDA_OK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+            asked.fetch_or(bit, std::memory_order_relaxed);
+        }
+    }
+    kernel<<<grid, threads, smem, st>>>(a);
+    PRISM_CUDA_OK(cudaGetLastError());
+    return PRISM_OK;
 }
 
 bool aligned16(const RowPtr &p, size_t row_bytes) {
@@ -505,16 +644,22 @@ int partials(long long nrows, int C) {
 // ---- forward ----
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
 prism_status run_fwd(const FwdArgs &a, cudaStream_t st) {
-    const int per = kCta ? 1 : 256 / a.tpr;
-    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? 2048 / a.tpr : 8);
-    k_norm_fwd<T, VEC, NV, kCta, kCkpt><<<(int)(need < most ? need : most), kCta ? a.tpr : 256, 0, st>>>(a);
-    PRISM_CUDA_OK(cudaGetLastError());
-    return PRISM_OK;
+    // CTAs of 256 threads per SM by what NV costs in registers; with one row
+    // per CTA, 512 threads' worth
+    // (rows without a ring: many more, which hides the fetches)
+    constexpr bool kRing = VEC * sizeof(T) == 16;
+    constexpr int kPerSm = !kRing ? 16 : NV * VEC <= 8 ? 5 : NV * VEC <= 16 ? 3 : 2;
+    static std::atomic<unsigned long long> asked{0};
+    const int per = kCta ? 1 : 256 / a.tpr, threads = kCta ? a.tpr : 256;
+    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? (kRing ? 512 : 4096) / a.tpr : kPerSm);
+    size_t smem = kRing ? (size_t)ring(NV * 16) * NV * 16 * threads : 0;
+    if (NV * VEC > 16) smem += (size_t)a.nvec * VEC * 8;  // gamma and beta
+    return launch(k_norm_fwd<T, VEC, NV, kCta, kCkpt>, a, (int)(need < most ? need : most), threads, smem, asked, st);
 }
 template <typename T, int VEC, bool kCkpt>
 prism_status fwd_spread(FwdArgs &a, cudaStream_t st) {
     static const int nvs[] = {1, 2, 3, 4, 6, 8};
-    const Spread s = spread<VEC>(a.C, nvs, 6);
+    const Spread s = spread<VEC>(a.C, nvs);
     a.nvec = s.nvec;
     a.tpr = s.tpr;
     switch (s.nv) {
@@ -525,7 +670,7 @@ prism_status fwd_spread(FwdArgs &a, cudaStream_t st) {
         case 6: return run_fwd<T, VEC, 6, false, kCkpt>(a, st);
         case 8: return run_fwd<T, VEC, 8, false, kCkpt>(a, st);
     }
-    // one row per CTA of 128 to 512 threads
+    // one row per CTA of up to 512 threads
     const int nv = a.nvec <= 512 * 4 ? 4 : 8;
     a.tpr = ((a.nvec + nv - 1) / nv + 31) / 32 * 32;
     return nv == 4 ? run_fwd<T, VEC, 4, true, kCkpt>(a, st) : run_fwd<T, VEC, 8, true, kCkpt>(a, st);
@@ -536,11 +681,11 @@ prism_status fwd_impl(const NormFwd &n, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
     const size_t row = (size_t)n.C * sizeof(T);
     const bool vec = aligned16(n.x, row) && aligned16(n.y, row);
-    if (n.C <= 512 * 8 * (vec ? VEC : 1)) {
+    if (n.C <= 512 * 8 * (vec ? VEC : 2)) {
         FwdArgs a{n.x, n.y, n.gamma, n.beta, n.wdt, (((uintptr_t)n.gamma | (uintptr_t)n.beta) & 15) == 0,
                   n.mean, n.rstd, n.codes, n.scales, n.fmt, n.nrows, n.C, 0, 0, n.eps, 1.f / (float)n.C};
         if (vec) return n.codes ? fwd_spread<T, VEC, true>(a, st) : fwd_spread<T, VEC, false>(a, st);
-        return n.codes ? fwd_spread<T, 1, true>(a, st) : fwd_spread<T, 1, false>(a, st);
+        return n.codes ? fwd_spread<T, 2, true>(a, st) : fwd_spread<T, 2, false>(a, st);
     }
     const int grid = (int)(n.nrows < 148 * 8 ? n.nrows : 148 * 8);
     k_norm_fwd_any<T><<<grid, kThreads, 0, st>>>(n.x, n.y, n.gamma, n.beta, n.wdt, n.mean, n.rstd, n.codes, n.scales,
@@ -550,32 +695,35 @@ prism_status fwd_impl(const NormFwd &n, cudaStream_t st) {
 }
 
 // ---- backward ----
+// Pieces per thread with one row per CTA: 16 channels at most (dgamma, dbeta
+// and gamma of each stay in registers).
+template <int VEC>
+constexpr int kBwdNV = VEC == 8 ? 2 : VEC == 4 ? 4 : 8;
+
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
-prism_status run_bwd(const BwdArgs &a, int P, cudaStream_t st) {
-    k_norm_bwd<T, VEC, NV, kCta, kCkpt><<<P, kCta ? a.tpr : 256, 0, st>>>(a);
-    PRISM_CUDA_OK(cudaGetLastError());
-    return PRISM_OK;
+prism_status run_bwd(const BwdArgs &a, int &P, cudaStream_t st) {
+    constexpr int kPerSm = NV * VEC <= 8 ? 3 : 2;
+    static std::atomic<unsigned long long> asked{0};
+    const int per = kCta ? 1 : 256 / a.tpr, threads = kCta ? a.tpr : 256;
+    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? 512 / a.tpr : kPerSm);
+    if (P > need) P = (int)need;
+    if (P > most) P = (int)most;
+    const size_t smem = VEC * sizeof(T) == 16 ? (size_t)ring(NV * 32) * NV * 32 * threads : 0;
+    return launch(k_norm_bwd<T, VEC, NV, kCta, kCkpt>, a, P, threads, smem, asked, st);
 }
 // P: partials allowed; on return the partials written
 template <typename T, int VEC, bool kCkpt>
 prism_status bwd_spread(BwdArgs &a, int &P, cudaStream_t st) {
-    static const int nvs[] = {1, 2};
-    const Spread s = spread<VEC>(a.C, nvs, 2);
+    constexpr int kMost = kBwdNV<VEC>;
+    static const int nvs[] = {kMost / 2, kMost};
+    const Spread s = spread<VEC>(a.C, nvs);
     a.nvec = s.nvec;
     a.tpr = s.tpr;
-    if (s.nv) {
-        const long long need = (a.nrows + 256 / a.tpr - 1) / (256 / a.tpr);
-        if (P > need) P = (int)need;
-        return s.nv == 1 ? run_bwd<T, VEC, 1, false, kCkpt>(a, P, st) : run_bwd<T, VEC, 2, false, kCkpt>(a, P, st);
-    }
-    // one row per CTA; 16 channels per thread at most (three packed fp32 sets of them stay in registers)
-    constexpr int kMost = VEC == 8 ? 2 : VEC == 4 ? 4 : 8;
-    const int nv = a.nvec <= 512 * 2 ? 2 : kMost;
-    a.tpr = ((a.nvec + nv - 1) / nv + 31) / 32 * 32;
-    return nv == 2 ? run_bwd<T, VEC, 2, true, kCkpt>(a, P, st) : run_bwd<T, VEC, kMost, true, kCkpt>(a, P, st);
+    if (s.nv) return s.nv == kMost ? run_bwd<T, VEC, kMost, false, kCkpt>(a, P, st)
+                                   : run_bwd<T, VEC, kMost / 2, false, kCkpt>(a, P, st);
+    a.tpr = ((a.nvec + kMost - 1) / kMost + 31) / 32 * 32;
+    return run_bwd<T, VEC, kMost, true, kCkpt>(a, P, st);
 }
-template <int VEC>
-constexpr int kBwdMost = 512 * (VEC == 8 ? 2 : VEC == 4 ? 4 : 8) * VEC;  // channels that bwd_spread takes
 
 template <typename T>
 prism_status bwd_impl(const NormBwd &n, cudaStream_t st) {
@@ -585,12 +733,12 @@ prism_status bwd_impl(const NormBwd &n, cudaStream_t st) {
     const size_t row = (size_t)n.C * sizeof(T);
     // codes and scales are 16-byte aligned and packed: a row of a multiple of VEC codes is aligned to VEC
     const bool vec = (n.codes ? n.C % VEC == 0 : aligned16(n.x, row)) && aligned16(n.dy, row) && aligned16(n.dx, row);
-    if (n.nrows > 0 && n.C <= (vec ? kBwdMost<VEC> : kBwdMost<1>)) {
+    if (n.nrows > 0 && n.C <= 512 * 16) {
         BwdArgs a{n.x, n.dy, n.dx, n.codes, n.scales, n.fmt, n.gamma, n.wdt, ((uintptr_t)n.gamma & 15) == 0,
                   n.mean, n.rstd, part, n.nrows, n.C, 0, 0, 1.f / (float)n.C};
         prism_status s;
         if (vec) s = n.codes ? bwd_spread<T, VEC, true>(a, P, st) : bwd_spread<T, VEC, false>(a, P, st);
-        else s = n.codes ? bwd_spread<T, 1, true>(a, P, st) : bwd_spread<T, 1, false>(a, P, st);
+        else s = n.codes ? bwd_spread<T, 2, true>(a, P, st) : bwd_spread<T, 2, false>(a, P, st);
         if (s != PRISM_OK) return s;
     } else {
         const Source<T> src{n.x, n.codes, n.scales, n.fmt, n.C};

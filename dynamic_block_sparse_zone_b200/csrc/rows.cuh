@@ -26,6 +26,16 @@ struct RowPtr {
     }
 };
 
+// The rows r, r + step, r + 2 step, ... one after another: an addition each
+// where the rows are evenly spaced.
+struct RowWalk {
+    char *p;
+    __device__ __forceinline__ void start(const RowPtr &q, long long r) { p = q(r); }
+    __device__ __forceinline__ void next(const RowPtr &q, long long inc, long long r) {  // inc = step * q.stride
+        p = q.group == 0 ? p + inc : q(r);
+    }
+};
+
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -146,68 +156,103 @@ __device__ __forceinline__ uint32_t narrow<__half>(f2 v) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A vector access: VEC elements in W words, as VP pairs.
+// cp.async of a thread's own bytes into its own shared-memory slot (N = 4, 8 or
+// 16, both sides aligned to N); a thread that has waited may read its slots.
+template <int N>
+__device__ __forceinline__ void copy_async(void *smem, const void *g) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(d), "l"(g) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(d), "l"(g), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+// all but the last N groups of this thread have landed
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+
+// A thread's piece of a row, VEC elements as VEC / 2 pairs: one 16-byte access,
+// or (VEC = 2: rows of any alignment and length) two elements fetched one by
+// one, of which the second may lie past the row's C channels.
 template <typename T, int VEC>
 struct Vec {
-    static constexpr int VP = (VEC + 1) / 2, W = VEC * sizeof(T) >= 4 ? VEC * sizeof(T) / 4 : 1;
+    static_assert(VEC * sizeof(T) == 16 || VEC == 2, "16-byte accesses, or pairs");
+    static constexpr int VP = VEC / 2, W = VEC * sizeof(T) / 4;
     uint32_t w[W];
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = 0;
     }
-    __device__ __forceinline__ void load(const char *row, long long v) {
-        if constexpr (VEC == 1) {
-            if constexpr (sizeof(T) == 2) w[0] = reinterpret_cast<const uint16_t *>(row)[v];
-            else w[0] = reinterpret_cast<const uint32_t *>(row)[v];
+    __device__ __forceinline__ void set(const uint4 &u) { w[0] = u.x, w[1 % W] = u.y, w[2 % W] = u.z, w[3 % W] = u.w; }
+    __device__ __forceinline__ void load(const char *row, long long v, long long C) {
+        if constexpr (VEC == 2) {
+            const bool second = 2 * v + 1 < C;
+            if constexpr (sizeof(T) == 2) {
+                const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + 2 * v;
+                w[0] = p[0] | (second ? (uint32_t)p[1] << 16 : 0u);
+            } else {
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(row) + 2 * v;
+                w[0] = p[0];
+                w[1 % W] = second ? p[1] : 0u;
+            }
         } else {
-            static_assert(VEC * sizeof(T) == 16, "16-byte accesses");
-            const uint4 u = reinterpret_cast<const uint4 *>(row)[v];
-            w[0] = u.x, w[1 % W] = u.y, w[2 % W] = u.z, w[3 % W] = u.w;
+            set(reinterpret_cast<const uint4 *>(row)[v]);
         }
     }
-    __device__ __forceinline__ void store(char *row, long long v) const {
-        if constexpr (VEC == 1) {
-            if constexpr (sizeof(T) == 2) reinterpret_cast<uint16_t *>(row)[v] = (uint16_t)w[0];
-            else reinterpret_cast<uint32_t *>(row)[v] = w[0];
+    __device__ __forceinline__ void store(char *row, long long v, long long C) const {
+        if constexpr (VEC == 2) {
+            const bool second = 2 * v + 1 < C;
+            if constexpr (sizeof(T) == 2) {
+                uint16_t *p = reinterpret_cast<uint16_t *>(row) + 2 * v;
+                p[0] = (uint16_t)w[0];
+                if (second) p[1] = (uint16_t)(w[0] >> 16);
+            } else {
+                uint32_t *p = reinterpret_cast<uint32_t *>(row) + 2 * v;
+                p[0] = w[0];
+                if (second) p[1] = w[1 % W];
+            }
         } else {
             reinterpret_cast<uint4 *>(row)[v] = make_uint4(w[0], w[1 % W], w[2 % W], w[3 % W]);
         }
     }
-    __device__ __forceinline__ f2 pair(int i) const {  // VEC = 1: (x, 0)
-        if constexpr (sizeof(T) == 4) return (f2)w[2 * i % W] | (VEC == 1 ? 0 : (f2)w[(2 * i + 1) % W] << 32);
+    __device__ __forceinline__ f2 pair(int i) const {
+        if constexpr (sizeof(T) == 4) return (f2)w[2 * i] | (f2)w[2 * i + 1] << 32;
         else return widen<T>(w[i]);
     }
     __device__ __forceinline__ void set_pair(int i, f2 v) {
         if constexpr (sizeof(T) == 4) {
-            w[2 * i % W] = (uint32_t)v;
-            if (VEC > 1) w[(2 * i + 1) % W] = (uint32_t)(v >> 32);
+            w[2 * i] = (uint32_t)v;
+            w[2 * i + 1] = (uint32_t)(v >> 32);
         } else {
             w[i] = narrow<T>(v);
         }
     }
 };
 
-// The 8-bit codes of a vector, one byte each.
+// The 8-bit codes of such a piece, one byte each.
 template <int VEC>
 struct Codes {
-    static constexpr int VP = (VEC + 1) / 2, W = (VEC + 3) / 4;
+    static constexpr int VP = VEC / 2, W = (VEC + 3) / 4;
     uint32_t w[W];
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = 0;
     }
-    __device__ __forceinline__ void load(const uint8_t *row, long long v) {
-        if constexpr (VEC == 1) w[0] = row[v];
+    __device__ __forceinline__ void load(const uint8_t *row, long long v, long long C) {
+        if constexpr (VEC == 2) w[0] = row[2 * v] | (2 * v + 1 < C ? (uint32_t)row[2 * v + 1] << 8 : 0u);
         else if constexpr (VEC == 4) w[0] = reinterpret_cast<const uint32_t *>(row)[v];
         else {
             const uint2 u = reinterpret_cast<const uint2 *>(row)[v];
             w[0] = u.x, w[1 % W] = u.y;
         }
     }
-    __device__ __forceinline__ void store(uint8_t *row, long long v) const {
-        if constexpr (VEC == 1) row[v] = (uint8_t)w[0];
-        else if constexpr (VEC == 4) reinterpret_cast<uint32_t *>(row)[v] = w[0];
-        else reinterpret_cast<uint2 *>(row)[v] = make_uint2(w[0], w[1 % W]);
+    __device__ __forceinline__ void store(uint8_t *row, long long v, long long C) const {
+        if constexpr (VEC == 2) {
+            row[2 * v] = (uint8_t)w[0];
+            if (2 * v + 1 < C) row[2 * v + 1] = (uint8_t)(w[0] >> 8);
+        } else if constexpr (VEC == 4) {
+            reinterpret_cast<uint32_t *>(row)[v] = w[0];
+        } else {
+            reinterpret_cast<uint2 *>(row)[v] = make_uint2(w[0], w[1 % W]);
+        }
     }
     // x * inv to the nearest codes.  int8: adding 1.5 * 2^23 rounds to a whole
     // number (|x inv| <= 127) and leaves its two's complement in the low byte.
@@ -240,15 +285,11 @@ struct Codes {
         const f2 sc = both(code_scale(sb));
         if (fmt == PRISM_CKPT_INT8) {  // byte + 128 in the mantissa of 2^23
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const uint32_t u = w[i] ^ 0x80808080u;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (2 * i + j < VP) {
-                        const uint32_t lo = __byte_perm(u, 0x4b000000u, 0x7540 + 2 * j);
-                        const uint32_t hi = __byte_perm(u, 0x4b000000u, 0x7541 + 2 * j);
-                        x[(2 * i + j) % VP] = mul2(add2((f2)lo | ((f2)hi << 32), both(-8388736.f)), sc);
-                    }
+            for (int i = 0; i < VP; ++i) {
+                const uint32_t u = w[i / 2] ^ 0x80808080u;
+                const uint32_t lo = __byte_perm(u, 0x4b000000u, i & 1 ? 0x7542 : 0x7540);
+                const uint32_t hi = __byte_perm(u, 0x4b000000u, i & 1 ? 0x7543 : 0x7541);
+                x[i] = mul2(add2((f2)lo | ((f2)hi << 32), both(-8388736.f)), sc);
             }
         } else {
 #pragma unroll
