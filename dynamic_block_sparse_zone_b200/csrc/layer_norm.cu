@@ -179,10 +179,31 @@ __global__ void __launch_bounds__(1024) k_norm_dw_sum(const float *__restrict__ 
 // own (no barrier): what is in flight does not cost registers.
 // ---------------------------------------------------------------------------
 
-// tpr lanes' sum, in each of them
-__device__ __forceinline__ float lanes_sum(float v, int tpr) {
-    for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// N sums over tpr lanes, in each of them
+template <int N>
+__device__ __forceinline__ void lanes_sum(float (&v)[N], int tpr) {
+    for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+}
+// N sums over the CTA's threads (at most 512, red zeroed past its warps), one barrier
+template <int N>
+__device__ __forceinline__ void rows_cta_sum(float (&v)[N], float (&red)[N][16]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) red[k][threadIdx.x >> 5] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = 0.f;
+    for (int q = 0; q < (int)(blockDim.x + 127) / 128; ++q)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float4 f = reinterpret_cast<const float4 *>(red[k])[q];
+            v[k] += (f.x + f.y) + (f.z + f.w);
+        }
 }
 
 // VEC weights from channel c0 on (NULL: `none` each); `vec`: 16-byte aligned
@@ -214,9 +235,45 @@ __device__ __forceinline__ void load_weights(const void *p, int dt, int c0, int 
     }
 }
 
-// kS: rows in a thread's ring, by what a thread holds per row (bytes); at 512
-// to 1024 threads per SM this keeps 64 to 128 KB in flight.
+// kS: steps in a thread's ring, by what a thread holds per step (bytes); at 512
+// to 1280 threads per SM this keeps 64 to 128 KB in flight.
 constexpr int ring(int bytes) { return bytes <= 64 ? 4 : bytes <= 96 ? 3 : 2; }
+// NR: rows that a group of threads takes at once, so that short rows share the
+// cost of a step and their reductions overlap.
+constexpr int fwd_rows(int channels, bool cta) { return cta || channels > 16 ? 1 : channels > 8 ? 2 : 4; }
+constexpr int bwd_rows(int channels, bool cta) { return cta || channels > 8 ? 1 : 2; }
+
+// A CTA's walk over the rows: step `it` takes rows it * step + j * per + sub
+// (j < NR) past its first; all of them exist except in the last step.
+struct Walk {
+    long long first, step;
+    int steps, last, per, sub;  // last: rows from the last step's first row on
+    __device__ __forceinline__ void init(long long nrows, int per_, int nr, int sub_) {
+        per = per_;
+        sub = sub_;
+        step = (long long)gridDim.x * per * nr;
+        first = (long long)blockIdx.x * per * nr;
+        steps = (int)((nrows - first + step - 1) / step);  // >= 1: the grid has no CTA without rows
+        const long long left = nrows - first - (steps - 1) * step;
+        last = left < per * nr ? (int)left : per * nr;
+    }
+    __device__ __forceinline__ bool live(int it, int j) const { return it < steps - 1 || (it < steps && j * per + sub < last); }
+    __device__ __forceinline__ long long row(int it, int j) const { return first + it * step + j * per + sub; }
+};
+// The address of a step's rows: one addition per step where rows are evenly spaced.
+struct RowWalk {
+    char *p;
+    long long inc, jinc;
+    __device__ __forceinline__ void start(const RowPtr &q, const Walk &w) {
+        inc = w.step * q.stride;
+        jinc = (long long)w.per * q.stride;
+        p = q.data + (w.first + w.sub) * q.stride;
+    }
+    __device__ __forceinline__ char *at(const RowPtr &q, const Walk &w, int it, int j) const {
+        return q.group == 0 ? p + j * jinc : q(w.row(it, j));
+    }
+    __device__ __forceinline__ void next() { p += inc; }
+};
 
 struct FwdArgs {
     RowPtr x, y;
@@ -233,42 +290,55 @@ struct FwdArgs {
 
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
 __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_fwd(FwdArgs a) {
-    constexpr int VP = VEC / 2, kS = ring(NV * 16);
+    constexpr int VP = VEC / 2, NR = fwd_rows(NV * VEC, kCta), NP = NR * NV, kS = ring(NP * 16);
     constexpr bool kRing = VEC * sizeof(T) == 16;
     // weights stay in registers, or (more than 16 channels per thread) in shared memory as fp32
     constexpr bool kKeep = NV * VEC <= 16;
-    extern __shared__ uint4 slots[];  // [kS][NV][threads] if kRing, then gamma and beta unless kKeep
-    __shared__ float red[2][2][16];
+    extern __shared__ uint4 slots[];  // [kS][NP][threads] if kRing, then gamma and beta unless kKeep
+    __shared__ __align__(16) float red[2][2][1][16];  // [row's parity][which sum]
+    if (kCta && threadIdx.x < 64) (&red[0][0][0][0])[threadIdx.x] = 0.f;
     const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
-    const int per = kCta ? 1 : 256 / tpr, sub = kCta ? 0 : threadIdx.x / tpr;
-    f2 gw[kKeep ? NV : 1][VP], bw[kKeep ? NV : 1][VP];
-    f2 *wsm = reinterpret_cast<f2 *>(slots + (kRing ? kS * NV * blockDim.x : 0));  // [2][nvec][VP]
-    const long long step = (long long)gridDim.x * per, xinc = step * a.x.stride, yinc = step * a.y.stride;
-    auto slot = [&](int s, int i) -> uint4 & { return slots[(s * NV + i) * blockDim.x + threadIdx.x]; };
-    long long r0 = (long long)blockIdx.x * per;
-    RowWalk xw, yw;  // the next row to fetch, the row to write
-    long long xr = r0 + sub;
-    if (xr < a.nrows) {
-        xw.start(a.x, xr);
-        yw.start(a.y, xr);
-    }
+    Walk w;
+    w.init(a.nrows, kCta ? 1 : 256 / tpr, NR, kCta ? 0 : threadIdx.x / tpr);
+    RowWalk xw, yw;
+    xw.start(a.x, w);
+    yw.start(a.y, w);
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) in[i] = i * tpr + t < a.nvec;
-    auto issue = [&](int s) {
-        if (xr < a.nrows) {
+    auto slot = [&](int s, int p) -> uint4 & { return slots[(s * NP + p) * blockDim.x + threadIdx.x]; };
+    Vec<T, VEC> ahead[kRing ? 1 : NP];  // without a ring: one step ahead in registers
+    int fit = 0;                        // the step to fetch
+    auto fetch = [&](int s) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (in[i]) copy_async<16>(&slot(s, i), xw.p + (i * tpr + t) * 16);
+        for (int j = 0; j < NR; ++j) {
+            const bool live = w.live(fit, j);
+            const char *xr = xw.at(a.x, w, fit, j);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int p = j * NV + i;
+                if constexpr (kRing) {
+                    if (live && in[i]) copy_async<16>(&slot(s, p), xr + (i * tpr + t) * 16);
+                } else {
+                    ahead[p].zero();
+                    if (live && in[i]) ahead[p].load(xr, i * tpr + t, a.C);
+                }
+            }
         }
-        copy_commit();
-        xr += step;
-        if (xr < a.nrows) xw.next(a.x, xinc, xr);
+        if constexpr (kRing) copy_commit();
+        xw.next();
+        ++fit;
     };
-    if constexpr (kRing) {
+    if constexpr (kRing) {  // slots that are not fetched into hold zeros
 #pragma unroll
-        for (int s = 0; s < kS - 1; ++s) issue(s);
+        for (int p = 0; p < kS * NP; ++p) slot(0, p) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int s = 0; s < kS - 1; ++s) fetch(s);
+    } else {
+        fetch(0);
     }
+    f2 gw[kKeep ? NV : 1][VP], bw[kKeep ? NV : 1][VP];
+    f2 *wsm = reinterpret_cast<f2 *>(slots + (kRing ? kS * NP * blockDim.x : 0));  // [2][nvec][VP]
     if constexpr (kKeep) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -278,111 +348,121 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_fwd(Fwd
             }
     } else {
         for (int v = threadIdx.x; v < a.nvec; v += blockDim.x) {
-            f2 w[VP];
-            load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.C, a.wvec, 1.f, w);
+            f2 u[VP];
+            load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.C, a.wvec, 1.f, u);
 #pragma unroll
-            for (int e = 0; e < VP; ++e) wsm[v * VP + e] = w[e];
-            load_weights<VEC>(a.beta, a.wdt, v * VEC, a.C, a.wvec, 0.f, w);
+            for (int e = 0; e < VP; ++e) wsm[v * VP + e] = u[e];
+            load_weights<VEC>(a.beta, a.wdt, v * VEC, a.C, a.wvec, 0.f, u);
 #pragma unroll
-            for (int e = 0; e < VP; ++e) wsm[(a.nvec + v) * VP + e] = w[e];
+            for (int e = 0; e < VP; ++e) wsm[(a.nvec + v) * VP + e] = u[e];
         }
         __syncthreads();
     }
     int par = 0, cur = 0;
-    auto row_sum = [&](f2 s2, int which) {
-        float s = low(s2) + high(s2);
-        if constexpr (kCta) {  // a slot is written again two rows on, behind a barrier of the row between
-            s = warp_sum(s);
-            if ((threadIdx.x & 31) == 0) red[par][which][threadIdx.x >> 5] = s;
-            __syncthreads();
-            s = 0.f;
-            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += red[par][which][w];
-            return s;
-        } else {
-            return lanes_sum(s, tpr);
-        }
+    // a slot of red is written again two rows on, behind the barriers of the row between
+    auto row_sums = [&](float (&v)[NR], int which) {
+        if constexpr (kCta) rows_cta_sum(v, red[par][which]);
+        else lanes_sum(v, tpr);
     };
+    if (kCta) __syncthreads();
     const int ng = (a.C + kGroup - 1) / kGroup;
-    for (; r0 < a.nrows; r0 += step) {
-        const long long r = r0 + sub;
-        const bool live = kCta || r < a.nrows;
-        f2 x[NV][VP], s = 0;
+    for (int it = 0; it < w.steps; ++it) {
+        f2 x[NP][VP];
         if constexpr (kRing) copy_wait<kS - 2>();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
+        for (int p = 0; p < NP; ++p) {
             Vec<T, VEC> raw;
-            raw.zero();
-            if (in[i] && live) {
-                if constexpr (kRing) raw.set(slot(cur, i));
-                else raw.load(xw.p, i * tpr + t, a.C);
-            }
+            if constexpr (kRing) raw.set(slot(cur, p));
+            else raw = ahead[p];
 #pragma unroll
-            for (int e = 0; e < VP; ++e) {
-                x[i][e] = raw.pair(e);
-                s = add2(s, x[i][e]);
-            }
+            for (int e = 0; e < VP; ++e) x[p][e] = raw.pair(e);
         }
-        if constexpr (kRing) {  // into the slots that the row before has been read from
-            issue(cur == 0 ? kS - 1 : cur - 1);
+        if constexpr (kRing) {  // into the slots that the step before has been read from
+            fetch(cur == 0 ? kS - 1 : cur - 1);
             cur = cur == kS - 1 ? 0 : cur + 1;
         } else {
-            xr += step;
-            if (xr < a.nrows) xw.next(a.x, xinc, xr);
+            fetch(0);
         }
-        if constexpr (kCkpt) {
+        float mean[NR], rstd[NR];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = i * tpr + t, k = group_exponent<VEC>(top_of(x[i]), a.fmt);
-                if (in[i] && live) {
-                    Codes<VEC> c;
-                    c.encode(x[i], code_inv_scale(k), a.fmt);
-                    c.store(a.codes + r * a.C, v, a.C);
-                    if (v % (kGroup / VEC) == 0) a.scales[r * ng + v / (kGroup / VEC)] = (uint8_t)(k + 127);
-                }
-            }
-        }
-        const float mean = row_sum(s, 0) * a.invC;
-        f2 q = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {  // x becomes x - mean; what lies past the row stays 0
-            const float m0 = in[i] ? -mean : 0.f;
-            const f2 m = make2(m0, VEC == 2 && 2 * (i * tpr + t) + 1 >= a.C ? 0.f : m0);
-#pragma unroll
-            for (int e = 0; e < VP; ++e) {
-                x[i][e] = add2(x[i][e], m);
-                q = fma2(x[i][e], x[i][e], q);
-            }
-        }
-        const float rstd = rsqrtf(row_sum(q, 1) * a.invC + a.eps);
-        par ^= 1;
-        if (live) {
-            const f2 rs = both(rstd);
+        for (int j = 0; j < NR; ++j) {
+            f2 s = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (in[i]) {
-                    const int v = i * tpr + t;
-                    Vec<T, VEC> o;
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) {
-                        const f2 g = kKeep ? gw[kKeep ? i : 0][e] : wsm[v * VP + e];
-                        const f2 b = kKeep ? bw[kKeep ? i : 0][e] : wsm[(a.nvec + v) * VP + e];
-                        o.set_pair(e, fma2(x[i][e], mul2(g, rs), b));
-                    }
-                    o.store(yw.p, v, a.C);
-                }
-            if (t == 0) {
-                a.mean[r] = mean;
-                a.rstd[r] = rstd;
-            }
-            if (r + step < a.nrows) yw.next(a.y, yinc, r + step);
+                for (int e = 0; e < VP; ++e) s = add2(s, x[j * NV + i][e]);
+            mean[j] = low(s) + high(s);
         }
+        row_sums(mean, 0);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) mean[j] *= a.invC;
+        if constexpr (kCkpt) {
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                const bool live = w.live(it, j);
+                const long long r = w.row(it, j);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int v = i * tpr + t, k = group_exponent<VEC>(top_of(x[j * NV + i]), a.fmt);
+                    if (in[i] && live) {
+                        Codes<VEC> c;
+                        c.encode(x[j * NV + i], code_inv_scale(k), a.fmt);
+                        c.store(a.codes + r * a.C, v, a.C);
+                        if (v % (kGroup / VEC) == 0) a.scales[r * ng + v / (kGroup / VEC)] = (uint8_t)(k + 127);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            f2 q = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {  // x becomes x - mean; what lies past the row stays 0
+                const float m0 = in[i] ? -mean[j] : 0.f;
+                const f2 m = make2(m0, VEC == 2 && 2 * (i * tpr + t) + 1 >= a.C ? 0.f : m0);
+#pragma unroll
+                for (int e = 0; e < VP; ++e) {
+                    x[j * NV + i][e] = add2(x[j * NV + i][e], m);
+                    q = fma2(x[j * NV + i][e], x[j * NV + i][e], q);
+                }
+            }
+            rstd[j] = low(q) + high(q);
+        }
+        row_sums(rstd, 1);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) rstd[j] = rsqrtf(rstd[j] * a.invC + a.eps);
+        par ^= 1;
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+            if (w.live(it, j)) {
+                const f2 rs = both(rstd[j]);
+                char *yr = yw.at(a.y, w, it, j);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (in[i]) {
+                        const int v = i * tpr + t;
+                        Vec<T, VEC> o;
+#pragma unroll
+                        for (int e = 0; e < VP; ++e) {
+                            const f2 g = kKeep ? gw[kKeep ? i : 0][e] : wsm[v * VP + e];
+                            const f2 b = kKeep ? bw[kKeep ? i : 0][e] : wsm[(a.nvec + v) * VP + e];
+                            o.set_pair(e, fma2(x[j * NV + i][e], mul2(g, rs), b));
+                        }
+                        o.store(yr, v, a.C);
+                    }
+                if (t == 0) {
+                    a.mean[w.row(it, j)] = mean[j];
+                    a.rstd[w.row(it, j)] = rstd[j];
+                }
+            }
+        yw.next();
     }
     if constexpr (kRing) copy_wait<0>();
 }
 
 struct BwdArgs {
-    RowPtr x, dy, dx;
-    const uint8_t *codes, *scales;
+    RowPtr x, dy, dx;  // with a checkpoint, x walks its codes
+    const uint8_t *scales;
     int fmt;
     const void *gamma;
     int wdt;
@@ -395,83 +475,91 @@ struct BwdArgs {
 };
 
 // Each thread adds up dgamma and dbeta of its own channels over the CTA's rows
-// in registers; the CTA writes one partial.
+// in registers; the CTA writes one partial.  Rows past the last one, and
+// channels past C, count as dy = 0.
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
 __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(BwdArgs a) {
-    constexpr int VP = VEC / 2, kS = ring(NV * 32);
+    constexpr int VP = VEC / 2, NR = bwd_rows(NV * VEC, kCta), NP = NR * NV, kS = ring(NP * 32);
     constexpr bool kRing = VEC * sizeof(T) == 16;
-    extern __shared__ uint4 slots[];  // [kS][2 NV][threads]: dy, then x or its codes
-    __shared__ float red[2][16][2];
+    extern __shared__ uint4 slots[];  // [kS][dy, x or its codes][NP][threads]
+    __shared__ __align__(16) float red[2][2][16];  // [row's parity]
     __shared__ float fold[kCta ? 1 : 256 * NV * VEC];
+    if (kCta && threadIdx.x < 64) (&red[0][0][0])[threadIdx.x] = 0.f;
     const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
-    const int per = kCta ? 1 : 256 / tpr, sub = kCta ? 0 : threadIdx.x / tpr;
-    const int ng = (a.C + kGroup - 1) / kGroup;
-    const long long step = (long long)gridDim.x * per;
-    const long long dyinc = step * a.dy.stride, xinc = step * (kCkpt ? a.C : a.x.stride), dxinc = step * a.dx.stride;
-    auto slot = [&](int s, int i) -> uint4 & { return slots[(s * 2 * NV + i) * blockDim.x + threadIdx.x]; };
+    Walk w;
+    w.init(a.nrows, kCta ? 1 : 256 / tpr, NR, kCta ? 0 : threadIdx.x / tpr);
+    RowWalk dyw, xw, dxw;
+    dyw.start(a.dy, w);
+    xw.start(a.x, w);
+    dxw.start(a.dx, w);
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) in[i] = i * tpr + t < a.nvec;
-    long long r0 = (long long)blockIdx.x * per;
-    RowWalk dyw, xw, dxw;  // the next row to fetch (kCkpt: xw walks the codes), the row to write
-    long long fr = r0 + sub;
-    if (fr < a.nrows) {
-        dyw.start(a.dy, fr);
-        if constexpr (kCkpt) xw.p = (char *)a.codes + fr * a.C;
-        else xw.start(a.x, fr);
-        dxw.start(a.dx, fr);
-    }
-    auto advance = [&]() {
-        fr += step;
-        if (fr < a.nrows) {
-            dyw.next(a.dy, dyinc, fr);
-            if constexpr (kCkpt) xw.p += xinc;
-            else xw.next(a.x, xinc, fr);
-        }
-    };
-    auto issue = [&](int s) {
-        if (fr < a.nrows) {
+    auto slot = [&](int s, int p) -> uint4 & { return slots[(s * 2 * NP + p) * blockDim.x + threadIdx.x]; };
+    // without a ring: one step ahead in registers
+    Vec<T, VEC> ndy[kRing ? 1 : NP], nx[kRing || kCkpt ? 1 : NP];
+    Codes<VEC> nc[kRing || !kCkpt ? 1 : NP];
+    int fit = 0;  // the step to fetch
+    auto fetch = [&](int s) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (in[i]) {
-                    copy_async<16>(&slot(s, i), dyw.p + (i * tpr + t) * 16);
-                    if constexpr (kCkpt) copy_async<VEC>(&slot(s, NV + i), xw.p + (i * tpr + t) * VEC);
-                    else copy_async<16>(&slot(s, NV + i), xw.p + (i * tpr + t) * 16);
-                }
-        }
-        copy_commit();
-        advance();
-    };
-    // what has no slots comes one row ahead in registers
-    Vec<T, VEC> ndy[kRing ? 1 : NV], nx[kRing || kCkpt ? 1 : NV];
-    Codes<VEC> nc[kRing || !kCkpt ? 1 : NV];
-    uint32_t xs[NV];
-    float mean = 0.f, rstd = 0.f;
-    auto ahead = [&](long long r) {  // rows past the last one, and channels past C, count as dy = 0
-        const bool live = r < a.nrows;
-        mean = live ? a.mean[r] : 0.f;
-        rstd = live ? a.rstd[r] : 0.f;
+        for (int j = 0; j < NR; ++j) {
+            const bool live = w.live(fit, j);
+            const char *dyr = dyw.at(a.dy, w, fit, j), *xr = xw.at(a.x, w, fit, j);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = i * tpr + t;
-            if constexpr (kCkpt) xs[i] = live && in[i] ? a.scales[r * ng + v / (kGroup / VEC)] : 0u;
-            if constexpr (!kRing) {
-                ndy[i].zero();
-                if constexpr (kCkpt) nc[i].zero();
-                else nx[i].zero();
-                if (live && in[i]) {
-                    ndy[i].load(dyw.p, v, a.C);
-                    if constexpr (kCkpt) nc[i].load((const uint8_t *)xw.p, v, a.C);
-                    else nx[i].load(xw.p, v, a.C);
+            for (int i = 0; i < NV; ++i) {
+                const int p = j * NV + i, v = i * tpr + t;
+                if constexpr (kRing) {
+                    if (live && in[i]) {
+                        copy_async<16>(&slot(s, p), dyr + v * 16);
+                        if constexpr (kCkpt) copy_async<VEC>(&slot(s, NP + p), xr + v * VEC);
+                        else copy_async<16>(&slot(s, NP + p), xr + v * 16);
+                    } else if (!kCta) {  // rows past the last: zeros over what an earlier step left
+                        slot(s, p) = make_uint4(0, 0, 0, 0);
+                    }
+                } else {
+                    ndy[p].zero();
+                    if constexpr (kCkpt) nc[p].zero();
+                    else nx[p].zero();
+                    if (live && in[i]) {
+                        ndy[p].load(dyr, v, a.C);
+                        if constexpr (kCkpt) nc[p].load((const uint8_t *)xr, v, a.C);
+                        else nx[p].load(xr, v, a.C);
+                    }
                 }
             }
         }
-        if constexpr (!kRing) advance();
+        if constexpr (kRing) copy_commit();
+        dyw.next();
+        xw.next();
+        ++fit;
     };
     if constexpr (kRing) {
 #pragma unroll
-        for (int s = 0; s < kS - 1; ++s) issue(s);
+        for (int p = 0; p < kS * 2 * NP; ++p) slot(0, p) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int s = 0; s < kS - 1; ++s) fetch(s);
+    } else {
+        fetch(0);
     }
+    const int ng = (a.C + kGroup - 1) / kGroup;
+    uint32_t xs[NP];
+    float mean[NR], rstd[NR];
+    auto ahead = [&](int it) {  // what is small: one step ahead in registers
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const bool live = w.live(it, j);
+            const long long r = w.row(it, j);
+            mean[j] = live ? a.mean[r] : 0.f;
+            rstd[j] = live ? a.rstd[r] : 0.f;
+            if constexpr (kCkpt) {
+                const uint8_t *sr = a.scales + r * ng;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    xs[j * NV + i] = live && in[i] ? sr[(i * tpr + t) / (kGroup / VEC)] : 0u;
+            }
+        }
+    };
+    ahead(0);
     f2 gw[NV][VP], dg[NV][VP], db[NV][VP];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -480,82 +568,78 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(Bwd
         if (in[i]) load_weights<VEC>(a.gamma, a.wdt, (i * tpr + t) * VEC, a.C, a.wvec, 1.f, gw[i]);
     }
     int par = 0, cur = 0;
-    ahead(r0 + sub);
-    for (; r0 < a.nrows; r0 += step) {
-        const long long r = r0 + sub;
-        const bool live = kCta || r < a.nrows;
-        f2 xh[NV][VP], g[NV][VP], sa2 = 0, sb2 = 0;
-        const f2 rs = both(rstd), mm = both(-mean);
+    if (kCta) __syncthreads();
+    for (int it = 0; it < w.steps; ++it) {
+        f2 xh[NP][VP], g[NP][VP];
+        float sum[2 * NR], rs[NR];  // of g and of g xhat
         if constexpr (kRing) copy_wait<kS - 2>();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool use = live && in[i];
-            Vec<T, VEC> dy;
-            dy.zero();
-            if constexpr (!kRing) dy = ndy[i];
-            else if (use) dy.set(slot(cur, i));
-            if constexpr (kCkpt) {
-                Codes<VEC> c;
-                c.zero();
-                if constexpr (!kRing) c = nc[i];
-                else if (use) c.load(reinterpret_cast<const uint8_t *>(&slot(cur, NV + i)), 0, VEC);
-                c.template decode<float>(xs[i], a.fmt, xh[i]);
-            } else {
-                Vec<T, VEC> x;
-                x.zero();
-                if constexpr (!kRing) x = nx[i];
-                else if (use) x.set(slot(cur, NV + i));
+        for (int j = 0; j < NR; ++j) {
+            rs[j] = rstd[j];
+            const f2 r2 = both(rs[j]), mm = both(-mean[j]);
+            f2 sa2 = 0, sb2 = 0;
 #pragma unroll
-                for (int e = 0; e < VP; ++e) xh[i][e] = x.pair(e);
-            }
+            for (int i = 0; i < NV; ++i) {
+                const int p = j * NV + i;
+                Vec<T, VEC> dy;
+                if constexpr (kRing) dy.set(slot(cur, p));
+                else dy = ndy[p];
+                if constexpr (kCkpt) {
+                    Codes<VEC> c;
+                    if constexpr (kRing) c.load(reinterpret_cast<const uint8_t *>(&slot(cur, NP + p)), 0, VEC);
+                    else c = nc[p];
+                    c.template decode<float>(xs[p], a.fmt, xh[p]);
+                } else {
+                    Vec<T, VEC> x;
+                    if constexpr (kRing) x.set(slot(cur, NP + p));
+                    else x = nx[p];
 #pragma unroll
-            for (int e = 0; e < VP; ++e) {
-                xh[i][e] = mul2(add2(xh[i][e], mm), rs);
-                const f2 d = dy.pair(e);
-                dg[i][e] = fma2(d, xh[i][e], dg[i][e]);
-                db[i][e] = add2(db[i][e], d);
-                g[i][e] = mul2(d, gw[i][e]);
-                sa2 = add2(sa2, g[i][e]);
-                sb2 = fma2(g[i][e], xh[i][e], sb2);
+                    for (int e = 0; e < VP; ++e) xh[p][e] = x.pair(e);
+                }
+#pragma unroll
+                for (int e = 0; e < VP; ++e) {
+                    xh[p][e] = mul2(add2(xh[p][e], mm), r2);
+                    const f2 d = dy.pair(e);
+                    dg[i][e] = fma2(d, xh[p][e], dg[i][e]);
+                    db[i][e] = add2(db[i][e], d);
+                    g[p][e] = mul2(d, gw[i][e]);
+                    sa2 = add2(sa2, g[p][e]);
+                    sb2 = fma2(g[p][e], xh[p][e], sb2);
+                }
             }
+            sum[2 * j] = low(sa2) + high(sa2);
+            sum[2 * j + 1] = low(sb2) + high(sb2);
         }
-        if constexpr (kRing) {  // into the slots that the row before has been read from
-            issue(cur == 0 ? kS - 1 : cur - 1);
+        if constexpr (kRing) {  // into the slots that the step before has been read from
+            fetch(cur == 0 ? kS - 1 : cur - 1);
             cur = cur == kS - 1 ? 0 : cur + 1;
+        } else {
+            fetch(0);
         }
-        ahead(r + step);
-        float sa = low(sa2) + high(sa2), sb = low(sb2) + high(sb2);
+        ahead(it + 1);
         if constexpr (kCta) {  // a slot is written again two rows on, behind the barrier of the row between
-            sa = warp_sum(sa);
-            sb = warp_sum(sb);
-            if ((threadIdx.x & 31) == 0) {
-                red[par][threadIdx.x >> 5][0] = sa;
-                red[par][threadIdx.x >> 5][1] = sb;
-            }
-            __syncthreads();
-            sa = sb = 0.f;
-            for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-                sa += red[par][w][0];
-                sb += red[par][w][1];
-            }
+            rows_cta_sum(sum, red[par]);
             par ^= 1;
         } else {
-            sa = lanes_sum(sa, tpr);
-            sb = lanes_sum(sb, tpr);
+            lanes_sum(sum, tpr);
         }
-        if (live) {
-            const f2 ma = both(-sa * a.invC), mb = both(-sb * a.invC);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (in[i]) {
-                    Vec<T, VEC> o;
+        for (int j = 0; j < NR; ++j)
+            if (w.live(it, j)) {
+                const f2 ma = both(-sum[2 * j] * a.invC), mb = both(-sum[2 * j + 1] * a.invC), r2 = both(rs[j]);
+                char *dxr = dxw.at(a.dx, w, it, j);
 #pragma unroll
-                    for (int e = 0; e < VP; ++e)
-                        o.set_pair(e, mul2(fma2(xh[i][e], mb, add2(g[i][e], ma)), rs));
-                    o.store(dxw.p, i * tpr + t, a.C);
-                }
-            if (r + step < a.nrows) dxw.next(a.dx, dxinc, r + step);
-        }
+                for (int i = 0; i < NV; ++i)
+                    if (in[i]) {
+                        const int p = j * NV + i;
+                        Vec<T, VEC> o;
+#pragma unroll
+                        for (int e = 0; e < VP; ++e)
+                            o.set_pair(e, mul2(fma2(xh[p][e], mb, add2(g[p][e], ma)), r2));
+                        o.store(dxr, i * tpr + t, a.C);
+                    }
+            }
+        dxw.next();
     }
     if constexpr (kRing) copy_wait<0>();
     if (!a.part) return;
@@ -581,12 +665,12 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(Bwd
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const f2 p = which ? db[i][e / 2] : dg[i][e / 2];
-                    fold[sub * width + (i * tpr + t) * VEC + e] = e & 1 ? high(p) : low(p);
+                    fold[w.sub * width + (i * tpr + t) * VEC + e] = e & 1 ? high(p) : low(p);
                 }
             __syncthreads();
             for (int c = threadIdx.x; c < a.C; c += 256) {
                 float s = 0.f;
-                for (int p = 0; p < per; ++p) s += fold[p * width + c];
+                for (int p = 0; p < w.per; ++p) s += fold[p * width + c];
                 pg[which * a.C + c] = s;
             }
         }
@@ -645,20 +729,20 @@ int partials(long long nrows, int C) {
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
 prism_status run_fwd(const FwdArgs &a, cudaStream_t st) {
     // CTAs of 256 threads per SM by what NV costs in registers; with one row
-    // per CTA, 512 threads' worth
-    // (rows without a ring: many more, which hides the fetches)
+    // per CTA, 512 threads' worth.  (Rows without a ring: what fits, and more.)
     constexpr bool kRing = VEC * sizeof(T) == 16;
-    constexpr int kPerSm = !kRing ? 16 : NV * VEC <= 8 ? 5 : NV * VEC <= 16 ? 3 : 2;
+    constexpr int kNR = fwd_rows(NV * VEC, kCta);
+    constexpr int kPerSm = !kRing ? 8 : NV * VEC <= 16 ? 3 : 2;
     static std::atomic<unsigned long long> asked{0};
-    const int per = kCta ? 1 : 256 / a.tpr, threads = kCta ? a.tpr : 256;
-    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? (kRing ? 512 : 4096) / a.tpr : kPerSm);
-    size_t smem = kRing ? (size_t)ring(NV * 16) * NV * 16 * threads : 0;
+    const int per = (kCta ? 1 : 256 / a.tpr) * kNR, threads = kCta ? a.tpr : 256;
+    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? (kRing ? 768 : 2048) / a.tpr : kPerSm);
+    size_t smem = kRing ? (size_t)ring(kNR * NV * 16) * kNR * NV * 16 * threads : 0;
     if (NV * VEC > 16) smem += (size_t)a.nvec * VEC * 8;  // gamma and beta
     return launch(k_norm_fwd<T, VEC, NV, kCta, kCkpt>, a, (int)(need < most ? need : most), threads, smem, asked, st);
 }
 template <typename T, int VEC, bool kCkpt>
 prism_status fwd_spread(FwdArgs &a, cudaStream_t st) {
-    static const int nvs[] = {1, 2, 3, 4, 6, 8};
+    static const int nvs[] = {1, 2, 3, 4, 6, 8, VEC == 2 ? 16 : 8};
     const Spread s = spread<VEC>(a.C, nvs);
     a.nvec = s.nvec;
     a.tpr = s.tpr;
@@ -669,6 +753,8 @@ prism_status fwd_spread(FwdArgs &a, cudaStream_t st) {
         case 4: return run_fwd<T, VEC, 4, false, kCkpt>(a, st);
         case 6: return run_fwd<T, VEC, 6, false, kCkpt>(a, st);
         case 8: return run_fwd<T, VEC, 8, false, kCkpt>(a, st);
+        case 16:
+            if constexpr (VEC == 2) return run_fwd<T, VEC, 16, false, kCkpt>(a, st);
     }
     // one row per CTA of up to 512 threads
     const int nv = a.nvec <= 512 * 4 ? 4 : 8;
@@ -695,20 +781,21 @@ prism_status fwd_impl(const NormFwd &n, cudaStream_t st) {
 }
 
 // ---- backward ----
-// Pieces per thread with one row per CTA: 16 channels at most (dgamma, dbeta
-// and gamma of each stay in registers).
+// Pieces per thread at most: 16 channels (dgamma, dbeta and gamma of each stay
+// in registers), 8 where the next row waits in registers too.
 template <int VEC>
-constexpr int kBwdNV = VEC == 8 ? 2 : VEC == 4 ? 4 : 8;
+constexpr int kBwdNV = VEC == 8 ? 2 : 4;
 
 template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
 prism_status run_bwd(const BwdArgs &a, int &P, cudaStream_t st) {
-    constexpr int kPerSm = NV * VEC <= 8 ? 3 : 2;
+    constexpr bool kRing = VEC * sizeof(T) == 16;
+    constexpr int kNR = bwd_rows(NV * VEC, kCta);
     static std::atomic<unsigned long long> asked{0};
-    const int per = kCta ? 1 : 256 / a.tpr, threads = kCta ? a.tpr : 256;
-    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? 512 / a.tpr : kPerSm);
+    const int per = (kCta ? 1 : 256 / a.tpr) * kNR, threads = kCta ? a.tpr : 256;
+    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? (kRing ? 512 : 768) / a.tpr : 2);
     if (P > need) P = (int)need;
     if (P > most) P = (int)most;
-    const size_t smem = VEC * sizeof(T) == 16 ? (size_t)ring(NV * 32) * NV * 32 * threads : 0;
+    const size_t smem = kRing ? (size_t)ring(kNR * NV * 32) * kNR * NV * 32 * threads : 0;
     return launch(k_norm_bwd<T, VEC, NV, kCta, kCkpt>, a, P, threads, smem, asked, st);
 }
 // P: partials allowed; on return the partials written
@@ -733,8 +820,10 @@ prism_status bwd_impl(const NormBwd &n, cudaStream_t st) {
     const size_t row = (size_t)n.C * sizeof(T);
     // codes and scales are 16-byte aligned and packed: a row of a multiple of VEC codes is aligned to VEC
     const bool vec = (n.codes ? n.C % VEC == 0 : aligned16(n.x, row)) && aligned16(n.dy, row) && aligned16(n.dx, row);
-    if (n.nrows > 0 && n.C <= 512 * 16) {
-        BwdArgs a{n.x, n.dy, n.dx, n.codes, n.scales, n.fmt, n.gamma, n.wdt, ((uintptr_t)n.gamma & 15) == 0,
+    if (n.nrows > 0 && n.C <= 512 * (vec ? 16 : 8)) {
+        RowPtr x = n.x;
+        if (n.codes) x = RowPtr{(char *)n.codes, n.C, 0, 0};
+        BwdArgs a{x, n.dy, n.dx, n.scales, n.fmt, n.gamma, n.wdt, ((uintptr_t)n.gamma & 15) == 0,
                   n.mean, n.rstd, part, n.nrows, n.C, 0, 0, 1.f / (float)n.C};
         prism_status s;
         if (vec) s = n.codes ? bwd_spread<T, VEC, true>(a, P, st) : bwd_spread<T, VEC, false>(a, P, st);

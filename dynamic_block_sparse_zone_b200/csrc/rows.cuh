@@ -7,6 +7,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "prism_internal.cuh"
 
 namespace prism {
@@ -23,16 +25,6 @@ struct RowPtr {
         if (group == 0) return data + r * stride;
         const unsigned q = (unsigned)r / group;  // with groups, rows < 2^31 (checked on the host)
         return data + (long long)q * group_stride + (long long)((unsigned)r - q * group) * stride;
-    }
-};
-
-// The rows r, r + step, r + 2 step, ... one after another: an addition each
-// where the rows are evenly spaced.
-struct RowWalk {
-    char *p;
-    __device__ __forceinline__ void start(const RowPtr &q, long long r) { p = q(r); }
-    __device__ __forceinline__ void next(const RowPtr &q, long long inc, long long r) {  // inc = step * q.stride
-        p = q.group == 0 ? p + inc : q(r);
     }
 };
 
@@ -175,7 +167,8 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 template <typename T, int VEC>
 struct Vec {
     static_assert(VEC * sizeof(T) == 16 || VEC == 2, "16-byte accesses, or pairs");
-    static constexpr int VP = VEC / 2, W = VEC * sizeof(T) / 4;
+    // the two single elements stay apart until they are used: a fetch ahead must not wait for its data
+    static constexpr int VP = VEC / 2, W = VEC == 2 ? 2 : VEC * sizeof(T) / 4;
     uint32_t w[W];
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -184,38 +177,27 @@ struct Vec {
     __device__ __forceinline__ void set(const uint4 &u) { w[0] = u.x, w[1 % W] = u.y, w[2 % W] = u.z, w[3 % W] = u.w; }
     __device__ __forceinline__ void load(const char *row, long long v, long long C) {
         if constexpr (VEC == 2) {
-            const bool second = 2 * v + 1 < C;
-            if constexpr (sizeof(T) == 2) {
-                const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + 2 * v;
-                w[0] = p[0] | (second ? (uint32_t)p[1] << 16 : 0u);
-            } else {
-                const uint32_t *p = reinterpret_cast<const uint32_t *>(row) + 2 * v;
-                w[0] = p[0];
-                w[1 % W] = second ? p[1] : 0u;
-            }
+            using E = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+            const E *p = reinterpret_cast<const E *>(row) + 2 * v;
+            w[0] = p[0];
+            w[1] = 2 * v + 1 < C ? p[1] : 0;
         } else {
             set(reinterpret_cast<const uint4 *>(row)[v]);
         }
     }
     __device__ __forceinline__ void store(char *row, long long v, long long C) const {
         if constexpr (VEC == 2) {
-            const bool second = 2 * v + 1 < C;
-            if constexpr (sizeof(T) == 2) {
-                uint16_t *p = reinterpret_cast<uint16_t *>(row) + 2 * v;
-                p[0] = (uint16_t)w[0];
-                if (second) p[1] = (uint16_t)(w[0] >> 16);
-            } else {
-                uint32_t *p = reinterpret_cast<uint32_t *>(row) + 2 * v;
-                p[0] = w[0];
-                if (second) p[1] = w[1 % W];
-            }
+            using E = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+            E *p = reinterpret_cast<E *>(row) + 2 * v;
+            p[0] = (E)w[0];
+            if (2 * v + 1 < C) p[1] = (E)w[1];
         } else {
             reinterpret_cast<uint4 *>(row)[v] = make_uint4(w[0], w[1 % W], w[2 % W], w[3 % W]);
         }
     }
     __device__ __forceinline__ f2 pair(int i) const {
         if constexpr (sizeof(T) == 4) return (f2)w[2 * i] | (f2)w[2 * i + 1] << 32;
-        else return widen<T>(w[i]);
+        else return widen<T>(VEC == 2 ? w[0] | w[1 % W] << 16 : w[i]);
     }
     __device__ __forceinline__ void set_pair(int i, f2 v) {
         if constexpr (sizeof(T) == 4) {
@@ -223,6 +205,7 @@ struct Vec {
             w[2 * i + 1] = (uint32_t)(v >> 32);
         } else {
             w[i] = narrow<T>(v);
+            if (VEC == 2) w[1 % W] = w[i] >> 16;
         }
     }
 };
@@ -231,13 +214,16 @@ struct Vec {
 template <int VEC>
 struct Codes {
     static constexpr int VP = VEC / 2, W = (VEC + 3) / 4;
-    uint32_t w[W];
+    uint32_t w[W], second = 0;  // VEC = 2: the second code apart, as above
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = 0;
     }
     __device__ __forceinline__ void load(const uint8_t *row, long long v, long long C) {
-        if constexpr (VEC == 2) w[0] = row[2 * v] | (2 * v + 1 < C ? (uint32_t)row[2 * v + 1] << 8 : 0u);
+        if constexpr (VEC == 2) {
+            w[0] = row[2 * v];
+            second = 2 * v + 1 < C ? row[2 * v + 1] : 0;
+        }
         else if constexpr (VEC == 4) w[0] = reinterpret_cast<const uint32_t *>(row)[v];
         else {
             const uint2 u = reinterpret_cast<const uint2 *>(row)[v];
@@ -286,7 +272,7 @@ struct Codes {
         if (fmt == PRISM_CKPT_INT8) {  // byte + 128 in the mantissa of 2^23
 #pragma unroll
             for (int i = 0; i < VP; ++i) {
-                const uint32_t u = w[i / 2] ^ 0x80808080u;
+                const uint32_t u = (VEC == 2 ? w[0] | second << 8 : w[i / 2]) ^ 0x80808080u;
                 const uint32_t lo = __byte_perm(u, 0x4b000000u, i & 1 ? 0x7542 : 0x7540);
                 const uint32_t hi = __byte_perm(u, 0x4b000000u, i & 1 ? 0x7543 : 0x7541);
                 x[i] = mul2(add2((f2)lo | ((f2)hi << 32), both(-8388736.f)), sc);
@@ -294,7 +280,8 @@ struct Codes {
         } else {
 #pragma unroll
             for (int i = 0; i < VP; ++i) {
-                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)(VEC == 2 ? w[0] | second << 8 : w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
                 const float2 f = __half22float2(__half2(h));
                 x[i] = mul2(make2(f.x, f.y), sc);
             }
