@@ -31,7 +31,8 @@ EXPORTED = ("prism_plan_create", "prism_plan_bytes", "prism_plan_build", "prism_
             "prism_step_wait", "prism_audio_norms", "prism_plan_build_stats", "prism_plan_stats_slice",
             "prism_plan_build_finish", "prism_attn_fwd_taylor", "prism_plan_build_with_zones",
             "prism_ckpt_bytes", "prism_ckpt_pack", "prism_ckpt_unpack", "prism_layer_norm_fwd",
-            "prism_layer_norm_bwd_workspace", "prism_layer_norm_bwd")
+            "prism_layer_norm_bwd_workspace", "prism_layer_norm_bwd",
+            "prism_plan_set_score", "prism_attn_fwd_scored", "prism_attn_bwd_scored")
 NUM_TIMERS = 12
 
 
@@ -70,6 +71,11 @@ class prism_rows(ctypes.Structure):
 
 class prism_ckpt(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int)]
+
+
+class prism_score(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("doc", ctypes.c_void_p), ("causal", ctypes.c_int), ("prefix", ctypes.c_void_p)]
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -120,8 +126,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.prism_layer_norm_bwd_workspace.argtypes = [LL, I]
     lib.prism_layer_norm_bwd_workspace.restype = ctypes.c_size_t
     lib.prism_layer_norm_bwd.argtypes = [R, K, R, P, P, P, R, P, P, P, ctypes.c_size_t, LL, I, I, I, P]
+    lib.prism_plan_set_score.argtypes = [V, ctypes.POINTER(prism_score), P]
+    lib.prism_attn_fwd_scored.argtypes = [V, P, P, P]
+    lib.prism_attn_bwd_scored.argtypes = [V, P, P, P, P, P, P]
     for name in ("prism_ckpt_bytes", "prism_ckpt_pack", "prism_ckpt_unpack", "prism_layer_norm_fwd",
-                 "prism_layer_norm_bwd"):
+                 "prism_layer_norm_bwd", "prism_plan_set_score", "prism_attn_fwd_scored", "prism_attn_bwd_scored"):
         getattr(lib, name).restype = ctypes.c_int
     lib.prism_plan_destroy.argtypes = [V]
     lib.prism_plan_destroy.restype = None
@@ -300,11 +309,29 @@ class PrismPlan:
         _check(load_library().prism_plan_update_qkv(self._h, _ptr(Q), _ptr(K), _ptr(V), _stream()))
         return self
 
-    def fwd(self, O: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, want_lse: bool = True,
-            taylor: bool = False):
-        """Sparse forward over S_i; with taylor=True the blocks outside S_i are
-        added through their pooled keys and mean values (prism_attn_fwd_taylor)."""
+    def set_score(self, cap: float = 0.0, slopes: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                  doc: Optional[torch.Tensor] = None, causal: bool = False, prefix: Optional[torch.Tensor] = None):
+        """Scores and masks for fwd(scored=True) and bwd(scored=True) on the current build: logits
+        cap tanh(s / cap) - slopes[h] |pos_q - pos_k|, tokens of one doc (negative: padding),
+        causal by pos with keys below prefix visible to all (prism_plan_set_score)."""
         p = self.params
+        for t, n, dt, sh in ((slopes, "slopes", torch.float32, (p.heads,)), (pos, "pos", torch.float32, (p.batch, p.N)),
+                             (doc, "doc", torch.int32, (p.batch, p.N)), (prefix, "prefix", torch.float32, (p.batch,))):
+            if t is not None:
+                _need(t, n, dt, sh)
+        c = prism_score(float(cap), *(None if t is None else t.data_ptr() for t in (slopes, pos, doc)), int(bool(causal)),
+                        None if prefix is None else prefix.data_ptr())
+        _check(load_library().prism_plan_set_score(self._h, ctypes.byref(c), _stream()))
+        return self
+
+    def fwd(self, O: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+            taylor: bool = False, scored: bool = False):
+        """Sparse forward over S_i; with taylor=True the blocks outside S_i are
+        added through their pooled keys and mean values (prism_attn_fwd_taylor);
+        with scored=True under the scores and masks of set_score."""
+        p = self.params
+        if taylor and scored:
+            raise ValueError("the Taylor forward has no scored form")
         if O is None:
             O = torch.empty(self._qkv_shape(), dtype=torch.bfloat16, device="cuda")
         _need(O, "O", torch.bfloat16, self._qkv_shape())
@@ -312,11 +339,13 @@ class PrismPlan:
             lse = torch.empty((p.batch, p.heads, p.N), dtype=torch.float32, device="cuda")
         if lse is not None:
             _need(lse, "lse", torch.float32, (p.batch, p.heads, p.N))
-        fn = load_library().prism_attn_fwd_taylor if taylor else load_library().prism_attn_fwd
+        lib = load_library()
+        fn = lib.prism_attn_fwd_taylor if taylor else lib.prism_attn_fwd_scored if scored else lib.prism_attn_fwd
         _check(fn(self._h, _ptr(O), _ptr(lse), _stream()))
         return O, lse
 
-    def bwd(self, O: torch.Tensor, dO: torch.Tensor, dQ=None, dK=None, dV=None):
+    def bwd(self, O: torch.Tensor, dO: torch.Tensor, dQ=None, dK=None, dV=None, scored: bool = False):
+        """Gradients of the last forward, which was a scored one if and only if scored=True."""
         shp = self._qkv_shape()
         _need(O, "O", torch.bfloat16, shp)
         _need(dO, "dO", torch.bfloat16, shp)
@@ -325,7 +354,8 @@ class PrismPlan:
         dV = torch.empty(shp, dtype=torch.bfloat16, device="cuda") if dV is None else dV
         for t, n in ((dQ, "dQ"), (dK, "dK"), (dV, "dV")):
             _need(t, n, torch.bfloat16, shp)
-        _check(load_library().prism_attn_bwd(self._h, _ptr(O), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV), _stream()))
+        fn = load_library().prism_attn_bwd_scored if scored else load_library().prism_attn_bwd
+        _check(fn(self._h, _ptr(O), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV), _stream()))
         return dQ, dK, dV
 
     # -- steps from host memory (pipelined across calls) ---------------------

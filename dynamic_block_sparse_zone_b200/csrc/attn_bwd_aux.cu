@@ -17,11 +17,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // ---------------------------------------------------------------------------
 // backward, part 1: Delta = rowsum(dO * O) and the permuted copy of dO
 // ---------------------------------------------------------------------------
+// (doc, scored attention: a padding token's row counts as dO = 0, whatever it holds.)
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_bwd_pre(Geo g, const __nv_bfloat16 *__restrict__ O,
                                                       const __nv_bfloat16 *__restrict__ dO,
-                                                      const int *__restrict__ perm, __nv_bfloat16 *__restrict__ dOp,
-                                                      float *__restrict__ delta) {
+                                                      const int *__restrict__ perm, const int *__restrict__ doc,
+                                                      __nv_bfloat16 *__restrict__ dOp, float *__restrict__ delta) {
     constexpr int L = D / 8;  // lanes per (token, head)
     const int b = blockIdx.y;
     const int G = g.C / 8;
@@ -31,8 +32,9 @@ __global__ void __launch_bounds__(256) k_attn_bwd_pre(Geo g, const __nv_bfloat16
         const int n = blockIdx.x * kTile + nl;
         const int tok = perm[(size_t)b * g.N + n];
         const size_t src = ((size_t)b * g.N + tok) * g.C + grp * 8;
-        const uint4 ov = *reinterpret_cast<const uint4 *>(O + src);
-        const uint4 dv = *reinterpret_cast<const uint4 *>(dO + src);
+        uint4 ov = *reinterpret_cast<const uint4 *>(O + src);
+        uint4 dv = *reinterpret_cast<const uint4 *>(dO + src);
+        if (doc && doc[(size_t)b * g.N + n] < 0) ov = dv = make_uint4(0, 0, 0, 0);
         const int hd = grp * 8 / D, d0 = grp * 8 % D;
         const size_t bh = (size_t)b * g.heads + hd;
         *reinterpret_cast<uint4 *>(dOp + (bh * g.N + n) * D + d0) = dv;
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(256) k_dq_finalize(Geo g, const float *__restr
 // launcher
 // ---------------------------------------------------------------------------
 template <int D>
-static prism_status bwd_impl(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
+static prism_status bwd_impl(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV, bool scored,
                              cudaStream_t st) {
     const Geo &g = pl.g;
     PRISM_CUDA_OK(cudaMemsetAsync(pl.dQacc, 0, (size_t)g.batch * g.heads * g.N * D * sizeof(float), st));
@@ -85,10 +87,11 @@ static prism_status bwd_impl(Plan &pl, const void *O, const void *dO, void *dQ, 
         TimerScope ts(pl, kTBwdPre, st);
         k_attn_bwd_pre<D><<<dim3(g.nbmax, g.batch), 256, 0, st>>>(g, static_cast<const __nv_bfloat16 *>(O),
                                                                  static_cast<const __nv_bfloat16 *>(dO), pl.perm,
+                                                                 scored && pl.score.has_doc ? pl.score.doc : nullptr,
                                                                  pl.dOp, pl.delta);
         PRISM_CUDA_OK(cudaGetLastError());
     }
-    prism_status s = launch_attn_bwd_tc_main(pl, dK, dV, st);
+    prism_status s = scored ? launch_attn_bwd_tc_scored(pl, dK, dV, st) : launch_attn_bwd_tc_main(pl, dK, dV, st);
     if (s != PRISM_OK) return s;
     TimerScope ts(pl, kTDqFinal, st);
     k_dq_finalize<D><<<dim3(g.nbmax, g.batch), 256, 0, st>>>(g, pl.dQacc, pl.perm,
@@ -99,7 +102,14 @@ static prism_status bwd_impl(Plan &pl, const void *O, const void *dO, void *dQ, 
 
 prism_status launch_attn_bwd(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
                              cudaStream_t st) {
-    return pl.g.D == 64 ? bwd_impl<64>(pl, O, dO, dQ, dK, dV, st) : bwd_impl<128>(pl, O, dO, dQ, dK, dV, st);
+    return pl.g.D == 64 ? bwd_impl<64>(pl, O, dO, dQ, dK, dV, false, st)
+                        : bwd_impl<128>(pl, O, dO, dQ, dK, dV, false, st);
+}
+
+prism_status launch_attn_bwd_scored(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
+                                    cudaStream_t st) {
+    return pl.g.D == 64 ? bwd_impl<64>(pl, O, dO, dQ, dK, dV, true, st)
+                        : bwd_impl<128>(pl, O, dO, dQ, dK, dV, true, st);
 }
 
 }  // namespace prism

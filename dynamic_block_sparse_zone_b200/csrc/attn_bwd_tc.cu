@@ -47,6 +47,13 @@
 // keeps them in chunk order (deterministic sums), and dK and dV start from zero
 // (written by the drain warps before the first chunk), so no product needs to
 // know whether it is the first.
+// Scored variants (kScore): the columns without hidden block pairs (score.cu);
+// S becomes cap tanh(S / cap) - slope_h |p_q - p_k|, dS gets the factor
+// 1 - tanh^2, and in a pair that is only partly visible a hidden key's P and dS
+// are 0.  A key's position, visibility and document stay in its row's
+// registers; those of a chunk's queries come from global memory (L1: the
+// shared memory is full), one broadcast load per four.
+//
 // Warp roles (704 threads): warp 0 TMA producer (K, V once; Q, dO, LSE,
 // Delta per chunk into a three-stage ring; LSE is kept negated, in log2
 // units), warp 1 idle, warps 2..17 softmax and MMA issue, warps 18..21 dQ
@@ -85,7 +92,7 @@ struct Layout {
     static constexpr uint32_t kNumBars = 9 + 2 * kStages;
     // then per stage the column mask of its query chunk in a shared tile
     static constexpr uint32_t kMaskS = kBars + kNumBars * 8 + 16;
-    static constexpr uint32_t kBytes = kMaskS + 16;
+    static constexpr uint32_t kBytes = kMaskS + 16;  // (scored: the chunk's first row above the mask's 4 bits)
     static constexpr uint32_t kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 232448, "shared memory per block");
     static_assert(kDQ % 128 == 0, "TMA source alignment");
@@ -103,7 +110,7 @@ __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t adesc, uint
 
 enum { kSiteKV = 11, kSiteQFull, kSiteQEmpty, kSiteS, kSiteDQFull = 16, kSiteDQEmpty, kSiteDone, kSiteToken };
 
-template <int D>
+template <int D, int kScore>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_bwd_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -112,8 +119,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const int *__restrict__ blk_off, const int *__restrict__ colT_ptr, const int *__restrict__ rowT,
                   const int *__restrict__ perm, const float *__restrict__ nlse_p, const float *__restrict__ delta,
                   float *__restrict__ dQacc, __nv_bfloat16 *__restrict__ dK, __nv_bfloat16 *__restrict__ dV,
-                  float scale, float scale_log2, int *__restrict__ status) {
+                  float scale, float scale_log2, int *__restrict__ status, ScoreArgs sc) {
     using L = Layout<D>;
+    constexpr bool kEnc = (kScore & kScored) != 0;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
@@ -129,12 +137,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool shared_tile = jblk2 >= 0;
     const int kvalid = min(128, bo[(shared_tile ? jblk2 : jblk) + 1] - k0);
     const size_t colid = (size_t)bh * g.nbmax + jblk;
-    const int u_begin = colT_ptr[colid], u_end = colT_ptr[colid + 1];
+    const int u_begin = colT_ptr[colid], u_end = kEnc ? sc.list_end[colid] : colT_ptr[colid + 1];
     // the second key block's column (empty unless the tile is shared)
-    const int u2_begin = shared_tile ? colT_ptr[colid + 1] : 0, u2_end = shared_tile ? colT_ptr[colid + 2] : 0;
+    const int u2_begin = shared_tile ? colT_ptr[colid + 1] : 0;
+    const int u2_end = shared_tile ? (kEnc ? sc.list_end[colid + 1] : colT_ptr[colid + 2]) : 0;
 
     // 64-row query chunks of the column(s)
-    const int nchunk = union_segments(rowT + u_begin, u_end - u_begin, rowT + u2_begin, u2_end - u2_begin, bo, lane);
+    const int nchunk = union_segments<kEnc>(rowT + u_begin, u_end - u_begin, rowT + u2_begin, u2_end - u2_begin, bo, lane);
 
     const uint32_t bar_kv = sbase + L::kBars;
     const uint32_t bar_qf = bar_kv + 8, bar_qe = bar_qf + 8 * kStages, bar_sf = bar_qe + 8 * kStages;
@@ -202,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(sbase + L::kV + hf * L::kKVHalf + rh * 8192, &tmV, bar_kv, hf * 64,
                                 rowbase + k0 + rh * 64);
                 }
-            SegWalk wk;
+            SegWalk<kEnc> wk;
             wk.init(u_begin, u_end, u2_begin, u2_end, rowT, bo);
             int issued = 0;
             for (int c = 0; c < nchunk; ++c) {
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t sVec = sbase + L::kVec + st * 512;
                 const uint32_t bar = bar_qf + 8 * st;
                 const int r = wk.r;
-                mask_s[st] = (uint32_t)wk.mask;  // published by the arrive below
+                mask_s[st] = (uint32_t)wk.mask | (kEnc ? (uint32_t)r << 4 : 0u);  // published by the arrive below
                 mbar_expect_tx(bar, 2 * 64 * D * 2 + 512);
                 for (int hf = 0; hf < L::kHalves; ++hf) {
                     tma_load_2d(sQ + hf * L::kQHalf, &tmQ, bar, hf * 64, rowbase + r);
@@ -242,6 +251,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = rowid < kvalid;
         const int half = shared_tile ? (quad >> 1) : 0;  // which key block's rows (warp-uniform)
         bool ok = true;
+        // scored: this key's position, visibility and document (no query has -2), the slope in log2 units
+        float pk = 0.f, vk = 0.f, slope2 = 0.f;
+        int dk = -2;
+        if constexpr (kEnc) {
+            if (live) {
+                pk = sc.pos[(size_t)b * g.N + k0 + rowid];
+                vk = sc.vis[(size_t)b * g.N + k0 + rowid];
+                dk = sc.doc[(size_t)b * g.N + k0 + rowid];
+            }
+            if (kScore & kBias) slope2 = sc.slopes[h] * 1.4426950408889634f;
+        }
         const bool issuer = ((warp - 2) & 7) == 0;  // the group's first warp issues its products
         constexpr uint32_t idST = idesc_bf16(128, 64, false);
         constexpr uint32_t idAcc = idesc_bf16(128, D, true);
@@ -276,7 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                            abort_flag));
             if (ok) {
                 tc_fence_after();
-                const bool act = live && ((mask_s[st] >> half) & 1u);
+                const uint32_t mw = mask_s[st];
+                const bool act = live && ((mw >> half) & 1u);
+                const bool part = kEnc && ((mw >> (2 + half)) & 1u);
+                const size_t qn = kEnc ? (size_t)b * g.N + (mw >> 4) : 0;  // the chunk's first query
                 const uint32_t dsrow = sbase + L::kDS + (c & 1) * 16384 + rowid * 128;
 #pragma unroll 1
                 for (int sub = 0; sub < 2; ++sub) {
@@ -286,33 +309,89 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld16(tST, sv);
                     tmem_ld16(tmem + kColDP + (c & 1) * 64 + 16 * cq + lane_off, dv);
                     const uint32_t vec = sbase + L::kVec + st * 512 + cq * 64;
-                    float4 N4[4], D4[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        N4[j] = lds_f4(vec + 16 * j);
-                        D4[j] = lds_f4(vec + 256 + 16 * j);
-                    }
-                    tmem_wait_ld();
                     uint32_t pd[16];
-                    if (act) {
-                        const uint64_t s2 = splat2(scale_log2);
+                    if constexpr (!kEnc) {
+                        float4 N4[4], D4[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int q = 4 * j;
-                            float x0, x1, x2, x3, d0, d1, d2, d3;
-                            fma2(__uint_as_float(sv[q]), __uint_as_float(sv[q + 1]), s2, pair2(N4[j].x, N4[j].y), x0, x1);
-                            fma2(__uint_as_float(sv[q + 2]), __uint_as_float(sv[q + 3]), s2, pair2(N4[j].z, N4[j].w), x2, x3);
-                            const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
-                            mul_sub2(p0, p1, __uint_as_float(dv[q]), __uint_as_float(dv[q + 1]), D4[j].x, D4[j].y, d0, d1);
-                            mul_sub2(p2, p3, __uint_as_float(dv[q + 2]), __uint_as_float(dv[q + 3]), D4[j].z, D4[j].w, d2, d3);
-                            pd[2 * j] = pack_bf16x2(p0, p1);
-                            pd[2 * j + 1] = pack_bf16x2(p2, p3);
-                            pd[8 + 2 * j] = pack_bf16x2(d0, d1);
-                            pd[8 + 2 * j + 1] = pack_bf16x2(d2, d3);
+                            N4[j] = lds_f4(vec + 16 * j);
+                            D4[j] = lds_f4(vec + 256 + 16 * j);
+                        }
+                        tmem_wait_ld();
+                        if (act) {
+                            const uint64_t s2 = splat2(scale_log2);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int q = 4 * j;
+                                float x0, x1, x2, x3, d0, d1, d2, d3;
+                                fma2(__uint_as_float(sv[q]), __uint_as_float(sv[q + 1]), s2, pair2(N4[j].x, N4[j].y), x0, x1);
+                                fma2(__uint_as_float(sv[q + 2]), __uint_as_float(sv[q + 3]), s2, pair2(N4[j].z, N4[j].w), x2, x3);
+                                const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+                                mul_sub2(p0, p1, __uint_as_float(dv[q]), __uint_as_float(dv[q + 1]), D4[j].x, D4[j].y, d0, d1);
+                                mul_sub2(p2, p3, __uint_as_float(dv[q + 2]), __uint_as_float(dv[q + 3]), D4[j].z, D4[j].w, d2, d3);
+                                pd[2 * j] = pack_bf16x2(p0, p1);
+                                pd[2 * j + 1] = pack_bf16x2(p2, p3);
+                                pd[8 + 2 * j] = pack_bf16x2(d0, d1);
+                                pd[8 + 2 * j + 1] = pack_bf16x2(d2, d3);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pd[e] = 0u;
                         }
                     } else {
+                        // the scored form of the same: x from cap tanh(S / cap) and the bias, P = 0 where
+                        // the key is hidden, dS times tanh's derivative 1 - tanh^2
+                        tmem_wait_ld();
+                        if (act) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pd[e] = 0u;
+                            for (int j = 0; j < 4; ++j) {
+                                const int q = 4 * j;
+                                const size_t qi = qn + 16 * cq + 4 * j;
+                                float4 pq = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if ((kScore & kBias) || part) pq = __ldg(reinterpret_cast<const float4 *>(sc.pos + qi));
+                                float x0 = __uint_as_float(sv[q]), x1 = __uint_as_float(sv[q + 1]);
+                                float x2 = __uint_as_float(sv[q + 2]), x3 = __uint_as_float(sv[q + 3]);
+                                float m4 = scale_log2;
+                                uint64_t t02 = 0, t13 = 0;
+                                if constexpr ((kScore & kCap) != 0) {
+                                    tanh4(x0, x1, x2, x3, sc.cap_in, t02, t13);
+                                    x0 = plo(t02), x1 = plo(t13), x2 = phi(t02), x3 = phi(t13);
+                                    m4 = sc.cap_out;
+                                }
+                                const float4 N = lds_f4(vec + 16 * j), dl = lds_f4(vec + 256 + 16 * j);
+                                if constexpr ((kScore & kBias) != 0) {
+                                    x0 = fmaf(x0, m4, fmaf(-slope2, fabsf(pq.x - pk), N.x));
+                                    x1 = fmaf(x1, m4, fmaf(-slope2, fabsf(pq.y - pk), N.y));
+                                    x2 = fmaf(x2, m4, fmaf(-slope2, fabsf(pq.z - pk), N.z));
+                                    x3 = fmaf(x3, m4, fmaf(-slope2, fabsf(pq.w - pk), N.w));
+                                } else {
+                                    x0 = fmaf(x0, m4, N.x), x1 = fmaf(x1, m4, N.y);
+                                    x2 = fmaf(x2, m4, N.z), x3 = fmaf(x3, m4, N.w);
+                                }
+                                float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+                                if (part) {
+                                    const int4 dq = __ldg(reinterpret_cast<const int4 *>(sc.doc + qi));
+                                    if (!(vk <= pq.x && dq.x == dk)) p0 = 0.f;
+                                    if (!(vk <= pq.y && dq.y == dk)) p1 = 0.f;
+                                    if (!(vk <= pq.z && dq.z == dk)) p2 = 0.f;
+                                    if (!(vk <= pq.w && dq.w == dk)) p3 = 0.f;
+                                }
+                                float d0, d1, d2, d3;
+                                mul_sub2(p0, p1, __uint_as_float(dv[q]), __uint_as_float(dv[q + 1]), dl.x, dl.y, d0, d1);
+                                mul_sub2(p2, p3, __uint_as_float(dv[q + 2]), __uint_as_float(dv[q + 3]), dl.z, dl.w, d2, d3);
+                                if constexpr ((kScore & kCap) != 0) {
+                                    d0 *= fmaf(-plo(t02), plo(t02), 1.f), d1 *= fmaf(-plo(t13), plo(t13), 1.f);
+                                    d2 *= fmaf(-phi(t02), phi(t02), 1.f), d3 *= fmaf(-phi(t13), phi(t13), 1.f);
+                                }
+                                pd[2 * j] = pack_bf16x2(p0, p1);
+                                pd[2 * j + 1] = pack_bf16x2(p2, p3);
+                                pd[8 + 2 * j] = pack_bf16x2(d0, d1);
+                                pd[8 + 2 * j + 1] = pack_bf16x2(d2, d3);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pd[e] = 0u;
+                        }
                     }
                     tmem_st16(tST, pd);
                     sts_u4(dsrow + (((2 * cq) ^ (rowid & 7)) << 4), pd[8], pd[9], pd[10], pd[11]);
@@ -385,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int d = quad * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const bool leader = (warp == 2 + kSoftmaxWarps && lane == 0);
-        SegWalk wk;
+        SegWalk<kEnc> wk;
         wk.init(u_begin, u_end, u2_begin, u2_end, rowT, bo);
         for (int c = 0; c < nchunk; ++c) {
             if (!__all_sync(0xffffffffu,
@@ -434,31 +513,58 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace bwdtc
 
-prism_status configure_attn_bwd_tc_kernels() {
-    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)bwdtc::Layout<64>::kAlloc));
-    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)bwdtc::Layout<128>::kAlloc));
+template <int D>
+static prism_status configure_bwd() {
+    constexpr int bytes = (int)bwdtc::Layout<D>::kAlloc;
+    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    PRISM_CUDA_OK(
+        cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    PRISM_CUDA_OK(
+        cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kCap | kBias>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
     return PRISM_OK;
+}
+
+prism_status configure_attn_bwd_tc_kernels() {
+    prism_status s = configure_bwd<64>();
+    return s == PRISM_OK ? configure_bwd<128>() : s;
 }
 
 // Runs the tensor-core key-stationary backward; the caller has zeroed dQacc
 // and written dOp and delta.
-template <int D>
+template <int D, int kScore>
 static prism_status bwd_tc_main(Plan &pl, void *dK, void *dV, cudaStream_t st) {
     const Geo &g = pl.g;
     const double scale = 1.0 / sqrt((double)D);
     TimerScope ts(pl, kTAttnBwd, st);
-    bwdtc::k_attn_bwd_tc<D><<<dim3(g.nbmax, g.batch * g.heads), bwdtc::kThreads, bwdtc::Layout<D>::kAlloc, st>>>(
-        pl.tmQ, pl.tmK, pl.tmV, pl.tmdO, pl.tmdQ, g, pl.nqt, pl.qt_row, pl.qt_blk, pl.blk_off, pl.colT_ptr, pl.rowT,
-        pl.perm, pl.nlse_p, pl.delta, pl.dQacc, static_cast<__nv_bfloat16 *>(dK), static_cast<__nv_bfloat16 *>(dV),
-        (float)scale, (float)(scale * 1.4426950408889634), pl.status);
+    bwdtc::k_attn_bwd_tc<D, kScore>
+        <<<dim3(g.nbmax, g.batch * g.heads), bwdtc::kThreads, bwdtc::Layout<D>::kAlloc, st>>>(
+            pl.tmQ, pl.tmK, pl.tmV, pl.tmdO, pl.tmdQ, g, pl.nqt, pl.qt_row, pl.qt_blk, pl.blk_off, pl.colT_ptr,
+            kScore ? pl.score.rowT : pl.rowT, pl.perm, pl.nlse_p, pl.delta, pl.dQacc, static_cast<__nv_bfloat16 *>(dK),
+            static_cast<__nv_bfloat16 *>(dV), (float)scale, (float)(scale * 1.4426950408889634), pl.status,
+            kScore ? score_args(pl, true) : ScoreArgs{});
     PRISM_CUDA_OK(cudaGetLastError());
     return PRISM_OK;
 }
 
 prism_status launch_attn_bwd_tc_main(Plan &pl, void *dK, void *dV, cudaStream_t st) {
-    return pl.g.D == 64 ? bwd_tc_main<64>(pl, dK, dV, st) : bwd_tc_main<128>(pl, dK, dV, st);
+    return pl.g.D == 64 ? bwd_tc_main<64, 0>(pl, dK, dV, st) : bwd_tc_main<128, 0>(pl, dK, dV, st);
+}
+
+template <int D>
+static prism_status bwd_scored(Plan &pl, void *dK, void *dV, cudaStream_t st) {
+    switch (score_flags(pl.score)) {
+        case kScored: return bwd_tc_main<D, kScored>(pl, dK, dV, st);
+        case kScored | kCap: return bwd_tc_main<D, kScored | kCap>(pl, dK, dV, st);
+        case kScored | kBias: return bwd_tc_main<D, kScored | kBias>(pl, dK, dV, st);
+        default: return bwd_tc_main<D, kScored | kCap | kBias>(pl, dK, dV, st);
+    }
+}
+
+prism_status launch_attn_bwd_tc_scored(Plan &pl, void *dK, void *dV, cudaStream_t st) {
+    return pl.g.D == 64 ? bwd_scored<64>(pl, dK, dV, st) : bwd_scored<128>(pl, dK, dV, st);
 }
 
 }  // namespace prism

@@ -40,6 +40,15 @@
 // log2 |B_j| of every key block in shared memory (one byte each, -1 for the
 // blocks of S_i); each softmax warp then turns a chunk's 128 entries into
 // float biases in its own buffer.  One online softmax covers both parts.
+//
+// Scored variants (kScore): the selection is the one without hidden block
+// pairs (score.cu); the score is cap tanh(s / cap) - slope_h |p_q - p_k|, and in
+// the pairs that are only partly visible a key counts where its document is the
+// query's and the query's position has reached its visibility.  The producer
+// brings a chunk's key positions, visibilities and documents (128 each) into
+// one of two slots beside the segment mask; the softmax rewrites its 128 scores
+// in registers before the row max.  Block pairs that are wholly visible, most
+// of them, skip the mask.
 #include <cuda.h>
 
 #include "tc_common.cuh"
@@ -75,12 +84,16 @@ struct Layout {
     static constexpr uint32_t kLg = kBias + 4 * 128 * 4;
     __host__ __device__ static uint32_t lg_stride(int nbmax) { return (nbmax + 15) & ~15u; }
     static uint32_t taylor_alloc(int nbmax) { return kLg + 2 * lg_stride(nbmax) + 1024; }
+    // Scored variants: position, visibility and document of a chunk's 128 keys, two slots
+    static constexpr uint32_t kMeta = (kBytes + 15) & ~15u;
+    static constexpr uint32_t kMetaSlot = 3 * 512;
+    static constexpr uint32_t kScoreAlloc = kMeta + 2 * kMetaSlot + 1024;
 };
 
 // Site codes recorded with a timeout.
 enum { kSiteQ = 1, kSiteK, kSiteV, kSiteKEmpty, kSiteVEmpty, kSiteS, kSiteP, kSiteO, kSiteMask };
 
-template <int D, bool kTaylor>
+template <int D, bool kTaylor, int kScore>
 __global__ void __launch_bounds__(kThreads, 2)
     k_attn_fwd_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKb,
@@ -89,8 +102,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                   const int *__restrict__ qt_row, const int *__restrict__ qt_blk, const int *__restrict__ blk_off,
                   const int *__restrict__ row_ptr, const int *__restrict__ col, const int *__restrict__ perm,
                   __nv_bfloat16 *__restrict__ O, float *__restrict__ lse_user, float *__restrict__ nlse_p,
-                  float scale_log2, int *__restrict__ status) {
+                  float scale_log2, int *__restrict__ status, ScoreArgs sc) {
     using L = Layout<D>;
+    constexpr bool kEnc = (kScore & kScored) != 0;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
@@ -106,12 +120,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool shared_tile = iblk2 >= 0;
     const int qvalid = min(128, bo[(shared_tile ? iblk2 : iblk) + 1] - q0);
     const size_t crow = (size_t)bh * g.nbmax + iblk;
-    const int c_begin = row_ptr[crow], c_end = row_ptr[crow + 1];
+    const int c_begin = row_ptr[crow], c_end = kEnc ? sc.list_end[crow] : row_ptr[crow + 1];
     // the second query block's selection (empty unless the tile is shared)
-    const int c2_begin = shared_tile ? row_ptr[crow + 1] : 0, c2_end = shared_tile ? row_ptr[crow + 2] : 0;
+    const int c2_begin = shared_tile ? row_ptr[crow + 1] : 0;
+    const int c2_end = shared_tile ? (kEnc ? sc.list_end[crow + 1] : row_ptr[crow + 2]) : 0;
 
     // number of 64-row key segments of the selection (every warp computes it)
-    const int nseg = union_segments(col + c_begin, c_end - c_begin, col + c2_begin, c2_end - c2_begin, bo, lane);
+    const int nseg = union_segments<kEnc>(col + c_begin, c_end - c_begin, col + c2_begin, c2_end - c2_begin, bo, lane);
     const int nchunk = (nseg + 1) >> 1;
     // Taylor variant: pooled chunks follow the selected ones
     const int nbb = kTaylor ? nbv[b] : 0;
@@ -179,28 +194,44 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int rh = 0; rh < 2; ++rh)
                     tma_load_2d(sbase + L::kQ + hf * L::kTileBytes + rh * 8192, &tmQ, bar_q, hf * 64,
                                 rowbase + q0 + rh * 64);
-            SegWalk wk;
+            SegWalk<kEnc> wk;
             wk.init(c_begin, c_end, c2_begin, c2_end, col, bo);
-            int kissued = 0, vissued = 0;
+            int kissued = 0, vissued = 0, missued = 0;
             for (int c = 0; c < nchunk_all; ++c) {
                 const bool pooled = kTaylor && c >= nchunk;
                 const int nsg = pooled ? min(2, nseg_t - 2 * (c - nchunk)) : min(2, nseg - 2 * c);
                 const uint32_t bytes = nsg * 64 * D * 2;
                 const CUtensorMap *mK = pooled ? &tmKb : &tmK, *mV = pooled ? &tmVb : &tmV;
                 int rows[2];
-                uint32_t segmask = 0;  // bits 2s, 2s+1: segment s in S_i, in S_{i+1}
+                uint32_t segmask = 0;  // bits 2s, 2s+1: segment s in S_i, in S_{i+1}; + 4: only partly visible
                 if (pooled) {  // rows of the pooled [batch*heads][nbmax][D] copies
                     for (int gsg = 0; gsg < nsg; ++gsg) rows[gsg] = bh * g.nbmax + 128 * (c - nchunk) + 64 * gsg;
                 } else {
                     for (int gsg = 0; gsg < nsg; ++gsg) {
                         rows[gsg] = rowbase + wk.r;
-                        segmask |= (uint32_t)wk.mask << (2 * gsg);
+                        segmask |= (uint32_t)(wk.mask & 3) << (2 * gsg);
+                        if (kEnc) segmask |= (uint32_t)(wk.mask >> 2) << (4 + 2 * gsg);
                         wk.advance(col, bo);
                     }
                 }
                 // K_c once S_{c-1} has consumed the K buffer
                 if (c > 0 && !mbar_wait(bar_ke, (c - 1) & 1, status, kSiteKEmpty, abort_flag)) break;
-                if (shared_tile && !pooled) {  // the softmax has read this slot for chunk c - 2
+                if constexpr (kEnc) {  // the softmax has read this slot for chunk c - 2
+                    mask_w[c & 1] = segmask;
+                    const uint32_t bar = bar_mk + 8 * (c & 1), slot = sbase + L::kMeta + (c & 1) * L::kMetaSlot;
+                    const bool part = segmask >> 4;
+                    const uint32_t per = ((kScore & kBias) ? 256 : 0) + (part ? 512 : 0);
+                    mbar_expect_tx(bar, per * nsg);
+                    for (int gsg = 0; gsg < nsg; ++gsg) {
+                        const size_t n0 = (size_t)b * g.N + (rows[gsg] - rowbase);
+                        if (kScore & kBias) bulk_load(slot + gsg * 256, sc.pos + n0, 256, bar);
+                        if (part) {
+                            bulk_load(slot + 512 + gsg * 256, sc.vis + n0, 256, bar);
+                            bulk_load(slot + 1024 + gsg * 256, sc.doc + n0, 256, bar);
+                        }
+                    }
+                    missued = c + 1;
+                } else if (shared_tile && !pooled) {  // the softmax has read this slot for chunk c - 2
                     mask_w[c & 1] = segmask;
                     mbar_arrive(bar_mk + 8 * (c & 1));
                 }
@@ -222,6 +253,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             // drain: every issued load must land before the CTA may exit
             if (kissued > 0) mbar_wait(bar_kf, (kissued - 1) & 1, status, kSiteK, abort_flag);
             if (vissued > 0) mbar_wait(bar_vf, (vissued - 1) & 1, status, kSiteV, abort_flag);
+            if (kEnc)
+                for (int c = max(0, missued - 2); c < missued; ++c)
+                    mbar_wait(bar_mk + 8 * (c & 1), (c >> 1) & 1, status, kSiteMask, abort_flag);
             mbar_wait(bar_q, 0, status, kSiteQ, abort_flag);
         }
     } else if (warp == 1) {
@@ -268,16 +302,30 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t bias_s = sbase + L::kBias + quad * 512;  // this warp's 128 column biases
         const int half = shared_tile ? (quad >> 1) : 0;        // which query block's rows (warp-uniform)
         const int8_t *lgh = lg + half * lgs;
+        // scored: this row's position, document (no key has -2) and slope in log2 units
+        float pq = 0.f, slope2 = 0.f;
+        int dq = -2;
+        if constexpr (kEnc) {
+            if (rowid < qvalid) {
+                pq = sc.pos[(size_t)b * g.N + q0 + rowid];
+                dq = sc.doc[(size_t)b * g.N + q0 + rowid];
+            }
+            if (kScore & kBias) slope2 = sc.slopes[h] * 1.4426950408889634f;
+        }
         for (int c = 0; c < nchunk_all; ++c) {
             const bool pooled = kTaylor && c >= nchunk;
             // segments of this chunk outside this half's selection get P = 0
-            bool live0 = true, live1 = true;
-            if (shared_tile && !pooled) {
+            bool live0 = true, live1 = true, part0 = false, part1 = false;
+            if (kEnc || (shared_tile && !pooled)) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar_mk + 8 * (c & 1), (c >> 1) & 1, status, kSiteMask, abort_flag));
                 if (!ok) break;
                 const uint32_t mw = mask_w[c & 1];
                 live0 = (mw >> half) & 1u;
                 live1 = (mw >> (2 + half)) & 1u;
+                if (kEnc) {
+                    part0 = (mw >> (4 + half)) & 1u;
+                    part1 = (mw >> (6 + half)) & 1u;
+                }
             }
             if (pooled) {  // biases of this chunk's pooled keys, before S lands
                 float *bias = reinterpret_cast<float *>(smem + L::kBias + quad * 512);
@@ -301,6 +349,50 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int q = 0; q < 4; ++q)
                 if (q < nq) tmem_ld32(tSr + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
             tmem_wait_ld();
+            // scored: S becomes cap tanh(S / cap) - slope |p_q - p_k| in log2 units
+            // in place (only the mask: S as it is), -inf where the key is hidden
+            if constexpr (kEnc) {
+                const uint32_t meta = sbase + L::kMeta + (c & 1) * L::kMetaSlot;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (q < nq && (q < 2 ? live0 : live1)) {
+                        if constexpr ((kScore & (kCap | kBias)) != 0) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                float *x = reinterpret_cast<float *>(&sr[32 * q + e]);
+                                float m4 = scale_log2, x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
+                                if constexpr ((kScore & kCap) != 0) {
+                                    uint64_t t02, t13;
+                                    tanh4(x0, x1, x2, x3, sc.cap_in, t02, t13);
+                                    x0 = plo(t02), x1 = plo(t13), x2 = phi(t02), x3 = phi(t13);
+                                    m4 = sc.cap_out;
+                                }
+                                if constexpr ((kScore & kBias) != 0) {
+                                    const float4 pk = lds_f4(meta + (32 * q + e) * 4);
+                                    x[0] = fmaf(x0, m4, -slope2 * fabsf(pq - pk.x));
+                                    x[1] = fmaf(x1, m4, -slope2 * fabsf(pq - pk.y));
+                                    x[2] = fmaf(x2, m4, -slope2 * fabsf(pq - pk.z));
+                                    x[3] = fmaf(x3, m4, -slope2 * fabsf(pq - pk.w));
+                                } else {
+                                    x[0] = x0 * m4, x[1] = x1 * m4, x[2] = x2 * m4, x[3] = x3 * m4;
+                                }
+                            }
+                        }
+                        if (q < 2 ? part0 : part1) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 vk = lds_f4(meta + 512 + (32 * q + e) * 4);
+                                const float4 dk = lds_f4(meta + 1024 + (32 * q + e) * 4);
+                                uint32_t *x = &sr[32 * q + e];
+                                const uint32_t ninf = 0xff800000u;
+                                if (!(vk.x <= pq && __float_as_int(dk.x) == dq)) x[0] = ninf;
+                                if (!(vk.y <= pq && __float_as_int(dk.y) == dq)) x[1] = ninf;
+                                if (!(vk.z <= pq && __float_as_int(dk.z) == dq)) x[2] = ninf;
+                                if (!(vk.w <= pq && __float_as_int(dk.w) == dq)) x[3] = ninf;
+                            }
+                        }
+                    }
+            }
             // pass 1: row max (three-input max, four independent chains).  Pooled
             // chunks first turn S into x = S*scale*log2e + bias in place.
             float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
@@ -345,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
             }
             const float mx = fmaxf(fmaxf(mxa, mxb), fmaxf(mxc, mxd));
-            const float mx2 = pooled ? mx : mx * scale_log2;
+            const bool scaled = pooled || (kScore & (kCap | kBias)) != 0;  // x is in log2 units already
+            const float mx2 = scaled ? mx : mx * scale_log2;
             const bool need = (c > 0) && (mx2 > m + kRescaleThreshold);
             if (c == 0) m = mx2;
             // TMEM loads / stores are warp-collective: the whole warp rescales when
@@ -353,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             // holds every earlier chunk: S_c was issued after P_{c-1} V_{c-1}.
             if (__any_sync(0xffffffffu, need)) {
                 const float mnew = fmaxf(m, mx2);
-                const float corr = ex2(m - mnew);
+                // (scored: a row that has seen no key yet has m = -inf, l = 0, O = 0)
+                const float corr = ex2(m - (kEnc && mnew == -INFINITY ? 0.f : mnew));
 #pragma unroll 1
                 for (int q = 0; q < D / 16; ++q) {
                     uint32_t orr[16];
@@ -370,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // (group q packs into columns [16q, 16q+16); all of S is in registers).
             // (scale, -m) and the running sum as packed fp32 pairs; a pooled
             // chunk's registers already hold the scaled, biased x.
-            const uint64_t s2 = splat2(pooled ? 1.0f : scale_log2), c2 = splat2(-m);
+            const uint64_t s2 = splat2(scaled ? 1.0f : scale_log2), c2 = splat2(kEnc && m == -INFINITY ? 0.f : -m);
             uint64_t acc2 = 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -406,8 +500,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         // epilogue: the last product P V must have landed
         if (ok && nchunk_all > 0)
             ok = __all_sync(0xffffffffu, mbar_wait(bar_o, (nchunk_all - 1) & 1, status, kSiteO, abort_flag));
-        if (ok && nchunk_all > 0) {
+        if (ok && (kEnc || nchunk_all > 0)) {
             tc_fence_after();
+            const bool empty = kEnc && l == 0.f;  // no key is visible: O = 0, log-sum-exp -inf
             const float inv = 1.f / l;
             const int n = q0 + rowid;
             const bool write = rowid < qvalid;
@@ -421,8 +516,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 uint4 pkt[4];
                 uint32_t *pw = reinterpret_cast<uint32_t *>(pkt);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 16; ++e) {
                     pw[e] = pack_bf16x2(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
+                    if (empty) pw[e] = 0u;
+                }
                 if (write) {
                     uint4 *d4 = reinterpret_cast<uint4 *>(dst + q * 32);
 #pragma unroll
@@ -430,8 +527,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             if (write) {
-                const float lse2 = m + __log2f(l);
-                if (!kTaylor) nlse_p[(size_t)bh * g.N + n] = -lse2;  // negated, log2 units: the backward's exp2 addend
+                const float lse2 = empty ? -INFINITY : m + __log2f(l);
+                // negated, log2 units: the backward's exp2 addend (an empty row's is -inf: P = 0)
+                if (!kTaylor) nlse_p[(size_t)bh * g.N + n] = empty ? -INFINITY : -lse2;
                 if (lse_user) lse_user[(size_t)bh * g.N + tok] = lse2 * 0.69314718055994531f;
             }
         }
@@ -530,15 +628,18 @@ prism_status make_tensor_maps(Plan &pl) {
     return s;
 }
 
-template <int D, bool kTaylor>
+template <int D, bool kTaylor, int kScore = 0>
 static prism_status fwd_tc_impl(Plan &pl, void *O, float *lse, cudaStream_t st) {
     const Geo &g = pl.g;
     const float scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
-    const uint32_t smem = kTaylor ? fwdtc::Layout<D>::taylor_alloc(g.nbmax) : fwdtc::Layout<D>::kAlloc;
+    const uint32_t smem = kTaylor  ? fwdtc::Layout<D>::taylor_alloc(g.nbmax)
+                          : kScore ? fwdtc::Layout<D>::kScoreAlloc
+                                   : fwdtc::Layout<D>::kAlloc;
     TimerScope ts(pl, kTaylor ? kTAttnFwdTaylor : kTAttnFwd, st);
-    fwdtc::k_attn_fwd_tc<D, kTaylor><<<dim3(g.nbmax, g.batch * g.heads), fwdtc::kThreads, smem, st>>>(
+    fwdtc::k_attn_fwd_tc<D, kTaylor, kScore><<<dim3(g.nbmax, g.batch * g.heads), fwdtc::kThreads, smem, st>>>(
         pl.tmQ, pl.tmK, pl.tmV, pl.tmKb, pl.tmVb, pl.nb, g, pl.nqt, pl.qt_row, pl.qt_blk, pl.blk_off, pl.row_ptr,
-        pl.col, pl.perm, static_cast<__nv_bfloat16 *>(O), lse, pl.nlse_p, scale_log2, pl.status);
+        kScore ? pl.score.col : pl.col, pl.perm, static_cast<__nv_bfloat16 *>(O), lse, pl.nlse_p, scale_log2, pl.status,
+        kScore ? score_args(pl, false) : ScoreArgs{});
     PRISM_CUDA_OK(cudaGetLastError());
     return PRISM_OK;
 }
@@ -546,20 +647,45 @@ static prism_status fwd_tc_impl(Plan &pl, void *O, float *lse, cudaStream_t st) 
 // Largest dynamic shared memory of a CTA on sm_100 (227 KB).
 constexpr int kMaxDynSmem = 232448;
 
-prism_status configure_attn_tc_kernels() {
-    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)fwdtc::Layout<64>::kAlloc));
-    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)fwdtc::Layout<128>::kAlloc));
-    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<64, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int D>
+static prism_status configure_fwd() {
+    using L = fwdtc::Layout<D>;
+    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<D, false, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)L::kAlloc));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<D, true, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kMaxDynSmem));
-    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMaxDynSmem));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<D, false, kScored>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kScoreAlloc));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<D, false, kScored | kCap>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kScoreAlloc));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<D, false, kScored | kBias>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kScoreAlloc));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(fwdtc::k_attn_fwd_tc<D, false, kScored | kCap | kBias>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kScoreAlloc));
     return PRISM_OK;
+}
+
+prism_status configure_attn_tc_kernels() {
+    prism_status s = configure_fwd<64>();
+    return s == PRISM_OK ? configure_fwd<128>() : s;
 }
 
 prism_status launch_attn_fwd_tc(Plan &pl, void *O, float *lse, cudaStream_t st) {
     return pl.g.D == 64 ? fwd_tc_impl<64, false>(pl, O, lse, st) : fwd_tc_impl<128, false>(pl, O, lse, st);
+}
+
+template <int D>
+static prism_status fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t st) {
+    switch (score_flags(pl.score)) {
+        case kScored: return fwd_tc_impl<D, false, kScored>(pl, O, lse, st);
+        case kScored | kCap: return fwd_tc_impl<D, false, kScored | kCap>(pl, O, lse, st);
+        case kScored | kBias: return fwd_tc_impl<D, false, kScored | kBias>(pl, O, lse, st);
+        default: return fwd_tc_impl<D, false, kScored | kCap | kBias>(pl, O, lse, st);
+    }
+}
+
+prism_status launch_attn_fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t st) {
+    return pl.g.D == 64 ? fwd_scored<64>(pl, O, lse, st) : fwd_scored<128>(pl, O, lse, st);
 }
 
 bool taylor_fits(const Geo &g) {

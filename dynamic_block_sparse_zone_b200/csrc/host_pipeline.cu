@@ -142,7 +142,7 @@ prism_status host_step(Plan &pl, const prism_host_io &io, cudaStream_t user, uns
     PRISM_CUDA_OK(cudaStreamWaitEvent(hp.comp, hp.in_ready[s], 0));
     if (t > (unsigned long long)kSets)
         PRISM_CUDA_OK(cudaStreamWaitEvent(hp.comp, hp.out_done[(t - 1 - kSets) % kRing], 0));
-    pl.have_fwd = false;
+    pl.have_fwd = 0;
     st = launch_plan(pl, hp.in[s][kQ], hp.in[s][kK], hp.in[s][kV], static_cast<const float *>(hp.in[s][kA]), hp.comp);
     if (st != PRISM_OK) return st;
     pl.built = true;
@@ -150,7 +150,7 @@ prism_status host_step(Plan &pl, const prism_host_io &io, cudaStream_t user, uns
     st = io.taylor ? launch_attn_fwd_taylor(pl, hp.out[s][kO], lse_dev, hp.comp)
                    : launch_attn_fwd_tc(pl, hp.out[s][kO], lse_dev, hp.comp);
     if (st != PRISM_OK) return st;
-    pl.have_fwd = true;
+    pl.have_fwd = 1;
     PRISM_CUDA_OK(cudaEventRecord(hp.fwd_done[s], hp.comp));
     if (bwd) {
         PRISM_CUDA_OK(cudaStreamWaitEvent(hp.comp, hp.dO_ready[s], 0));

@@ -216,6 +216,7 @@ TimerScope::~TimerScope() {
 
 static void release_buffers(Plan &pl) {
     release_host_pipe(pl);  // first: its streams may still use the plan's buffers
+    release_score(pl);
     Alloc a[64];
     const size_t n = plan_allocs(pl, a);
     for (size_t k = 0; k < n; ++k)
@@ -342,7 +343,7 @@ prism_status prism_plan_build(prism_plan *plan, const void *Q, const void *K, co
     if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "Q, K, V must be 16-byte aligned");
     if (plan->pl.g.Ctot != plan->pl.g.C && !plan->pl.p.hilbert_block)
         return fail(PRISM_ERR_STATE, "a head-sharded plan is built with build_stats, an exchange and build_finish");
-    plan->pl.have_fwd = false;
+    plan->pl.have_fwd = 0;
     s = launch_plan(plan->pl, Q, K, V, a_norm, static_cast<cudaStream_t>(stream));
     if (s == PRISM_OK) plan->pl.built = true;
     return s;
@@ -356,7 +357,7 @@ prism_status prism_plan_build_stats(prism_plan *plan, const void *V, const float
     if ((uintptr_t)V & 15) return fail(PRISM_ERR_INVALID_ARG, "V must be 16-byte aligned");
     if (plan->pl.p.hilbert_block)
         return fail(PRISM_ERR_STATE, "a Hilbert-order plan has no zone statistics: build it with prism_plan_build");
-    plan->pl.have_fwd = false;
+    plan->pl.have_fwd = 0;
     plan->pl.built = false;
     s = launch_plan_stats(plan->pl, V, a_norm, static_cast<cudaStream_t>(stream));
     plan->pl.have_stats = s == PRISM_OK;
@@ -385,7 +386,7 @@ prism_status prism_plan_build_finish(prism_plan *plan, const void *Q, const void
     const uintptr_t al = (uintptr_t)Q | (uintptr_t)K | (uintptr_t)V;
     if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "Q, K, V must be 16-byte aligned");
     if (!plan->pl.have_stats) return fail(PRISM_ERR_STATE, "prism_plan_build_finish needs prism_plan_build_stats first");
-    plan->pl.have_fwd = false;
+    plan->pl.have_fwd = 0;
     plan->pl.have_stats = false;
     s = launch_plan_finish(plan->pl, Q, K, V, static_cast<cudaStream_t>(stream));
     if (s == PRISM_OK) plan->pl.built = true;
@@ -416,7 +417,7 @@ prism_status prism_plan_build_with_zones(prism_plan *plan, const void *Q, const 
                         z % pl.g.M, z / pl.g.M, c, B);
     }
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    pl.have_fwd = false;
+    pl.have_fwd = 0;
     pl.built = false;
     pl.have_stats = false;
     PRISM_CUDA_OK(cudaMemcpyAsync(pl.zone_B, zone_B, nz * sizeof(int), cudaMemcpyHostToDevice, st));
@@ -434,7 +435,7 @@ prism_status prism_plan_update_qkv(prism_plan *plan, const void *Q, const void *
     if (!plan->pl.built) return fail(PRISM_ERR_STATE, "prism_plan_update_qkv needs a built plan");
     const uintptr_t al = (uintptr_t)Q | (uintptr_t)K | (uintptr_t)V;
     if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "Q, K, V must be 16-byte aligned");
-    plan->pl.have_fwd = false;
+    plan->pl.have_fwd = 0;
     return launch_regather(plan->pl, Q, K, V, static_cast<cudaStream_t>(stream));
 }
 
@@ -446,8 +447,50 @@ prism_status prism_attn_fwd(prism_plan *plan, void *O, float *lse, void *stream)
     if (!plan->pl.built) return fail(PRISM_ERR_STATE, "prism_attn_fwd needs a built plan");
     if ((uintptr_t)O & 15) return fail(PRISM_ERR_INVALID_ARG, "O must be 16-byte aligned");
     s = launch_attn_fwd_tc(plan->pl, O, lse, static_cast<cudaStream_t>(stream));
-    if (s == PRISM_OK) plan->pl.have_fwd = true;
+    if (s == PRISM_OK) plan->pl.have_fwd = 1;
     return s;
+}
+
+prism_status prism_plan_set_score(prism_plan *plan, const prism_score *score, void *stream) {
+    g_last_error.clear();
+    if (!plan || !score) return fail(PRISM_ERR_INVALID_ARG, "NULL argument to prism_plan_set_score");
+    if (!(score->cap == 0.f || (score->cap >= 1e-3f && score->cap <= 1e6f)))
+        return fail(PRISM_ERR_INVALID_ARG, "cap must be 0 (none) or in [1e-3, 1e6]");
+    if (score->prefix && !score->causal) return fail(PRISM_ERR_INVALID_ARG, "a prefix needs a causal mask");
+    const uintptr_t al = (uintptr_t)score->slopes | (uintptr_t)score->pos | (uintptr_t)score->doc | (uintptr_t)score->prefix;
+    if (al & 3) return fail(PRISM_ERR_INVALID_ARG, "slopes, pos, doc and prefix must be 4-byte aligned");
+    prism_status s = device_guard(plan->pl);
+    if (s != PRISM_OK) return s;
+    if (!plan->pl.built) return fail(PRISM_ERR_STATE, "prism_plan_set_score needs a built plan");
+    plan->pl.have_fwd = 0;
+    return set_score(plan->pl, *score, static_cast<cudaStream_t>(stream));
+}
+
+prism_status prism_attn_fwd_scored(prism_plan *plan, void *O, float *lse, void *stream) {
+    g_last_error.clear();
+    if (!plan || !O) return fail(PRISM_ERR_INVALID_ARG, "NULL argument to prism_attn_fwd_scored");
+    prism_status s = device_guard(plan->pl);
+    if (s != PRISM_OK) return s;
+    if (!plan->pl.built || !plan->pl.score.set)
+        return fail(PRISM_ERR_STATE, "prism_attn_fwd_scored needs a prism_plan_set_score after the last build");
+    if ((uintptr_t)O & 15) return fail(PRISM_ERR_INVALID_ARG, "O must be 16-byte aligned");
+    s = launch_attn_fwd_scored(plan->pl, O, lse, static_cast<cudaStream_t>(stream));
+    if (s == PRISM_OK) plan->pl.have_fwd = 2;
+    return s;
+}
+
+prism_status prism_attn_bwd_scored(prism_plan *plan, const void *O, const void *dO, void *dQ, void *dK, void *dV,
+                                   void *stream) {
+    g_last_error.clear();
+    if (!plan || !O || !dO || !dQ || !dK || !dV)
+        return fail(PRISM_ERR_INVALID_ARG, "NULL argument to prism_attn_bwd_scored");
+    prism_status s = device_guard(plan->pl);
+    if (s != PRISM_OK) return s;
+    if (plan->pl.have_fwd != 2 || !plan->pl.score.set)
+        return fail(PRISM_ERR_STATE, "prism_attn_bwd_scored needs a prism_attn_fwd_scored as the last forward");
+    const uintptr_t al = (uintptr_t)O | (uintptr_t)dO | (uintptr_t)dQ | (uintptr_t)dK | (uintptr_t)dV;
+    if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+    return launch_attn_bwd_scored(plan->pl, O, dO, dQ, dK, dV, static_cast<cudaStream_t>(stream));
 }
 
 prism_status prism_attn_fwd_taylor(prism_plan *plan, void *O, float *lse, void *stream) {
@@ -468,7 +511,7 @@ prism_status prism_attn_bwd(prism_plan *plan, const void *O, const void *dO, voi
     if (!plan || !O || !dO || !dQ || !dK || !dV) return fail(PRISM_ERR_INVALID_ARG, "NULL argument to prism_attn_bwd");
     prism_status s = device_guard(plan->pl);
     if (s != PRISM_OK) return s;
-    if (!plan->pl.have_fwd)
+    if (plan->pl.have_fwd != 1)
         return fail(PRISM_ERR_STATE, "prism_attn_bwd needs a prism_attn_fwd after the last build or update");
     const uintptr_t al = (uintptr_t)O | (uintptr_t)dO | (uintptr_t)dQ | (uintptr_t)dK | (uintptr_t)dV;
     if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "tensors must be 16-byte aligned");

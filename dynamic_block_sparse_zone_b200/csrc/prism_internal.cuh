@@ -37,6 +37,28 @@ struct Geo {
     int Ctot, chunk0, nchunk_tot;
 };
 
+// The scored attention of a plan (score.cu): the caller's scores and masks in
+// block-contiguous order, and the selection without the block pairs that the
+// mask hides.  Buffers are allocated by the first prism_plan_set_score.
+struct BlockRange {  // of a block's tokens that are not padding
+    float pmin, pmax;  // positions
+    float kmin, kmax;  // least position that sees each key
+    int dmin, dmax;    // documents
+    int tokens, pads;  // how many tokens, how many of padding
+};
+struct Score {
+    bool set;               // valid for the plan's current build
+    bool has_bias, has_doc;
+    float cap;              // 0: none
+    float *slopes;          // [heads]
+    float *pos;             // [batch][N] position of each token
+    float *vis;             // [batch][N] a key is visible to queries at positions >= this (+inf: padding)
+    int *doc;               // [batch][N] document, -1: padding
+    BlockRange *blk;        // [batch][nbmax]
+    int *row_end, *col;     // the CSR again, rows starting at row_ptr: 2 j + (partly visible), see list_block
+    int *colT_end, *rowT;   // and its transpose, columns starting at colT_ptr
+};
+
 // Everything a plan owns (device pointers unless noted).
 struct Plan {
     prism_params p;
@@ -44,7 +66,7 @@ struct Plan {
     int fixed_idx;          // table index of the fixed shape, -1 = dynamic
     int cap_stride;         // worst-case selected blocks per row
     int device;
-    bool have_fwd;
+    int have_fwd;           // the statistics of the last forward: 0 none, 1 sparse, 2 scored
     bool built;
     bool have_stats;        // zone statistics computed since the last finished build
     // zone statistics and decisions
@@ -88,6 +110,7 @@ struct Plan {
     int *host_nb;           // pinned host copy of nb
     TimerState *timers;     // NULL unless timing is on
     HostPipe *pipe;         // NULL until the first host-buffer step
+    Score score;            // buffers NULL until the first prism_plan_set_score
     // TMA descriptors of the permuted copies, viewed as [batch*heads*N][D] bf16
     CUtensorMap tmQ, tmK, tmV, tmdO;
     CUtensorMap tmKb, tmVb;  // the pooled bf16 copies, viewed as [batch*heads*nbmax][D]
@@ -127,6 +150,27 @@ prism_status make_tensor_maps(Plan &pl);
 prism_status launch_attn_bwd_tc_main(Plan &pl, void *dK, void *dV, cudaStream_t st);
 prism_status launch_attn_bwd(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
                              cudaStream_t st);
+
+prism_status launch_attn_fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t st);
+prism_status launch_attn_bwd_scored(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
+                                    cudaStream_t st);
+prism_status launch_attn_bwd_tc_scored(Plan &pl, void *dK, void *dV, cudaStream_t st);
+prism_status set_score(Plan &pl, const prism_score &s, cudaStream_t st);
+prism_status launch_zero_padding(Plan &pl, cudaStream_t st);  // padding tokens' rows of Qp, Kp, Vp
+void release_score(Plan &pl);
+
+// What the scored attention kernels read besides the plan.
+struct ScoreArgs {
+    const int *list_end;        // row_end (forward) or colT_end (backward)
+    const float *pos, *vis;
+    const int *doc;
+    const float *slopes;
+    float cap_in;               // 1 / (sqrt(D) cap)
+    float cap_out;              // cap log2(e)
+};
+ScoreArgs score_args(const Plan &pl, bool backward);
+constexpr int kScored = 1, kCap = 2, kBias = 4;  // template flags of those kernels
+inline int score_flags(const Score &s) { return kScored | (s.cap > 0.f ? kCap : 0) | (s.has_bias ? kBias : 0); }
 
 prism_status launch_audio_norms(const void *h, float *a, long long rows, int C, cudaStream_t st);
 

@@ -1,0 +1,226 @@
+// score.cu -- the scores and masks of a plan's scored attention: the caller's
+// per-token positions, documents and visibility in block-contiguous order, and
+// the plan's selection without the block pairs that the mask hides.
+//
+// A pair of blocks is hidden when no query of the one may see a key of the
+// other (their documents do not meet, or every key lies behind every query),
+// whole when every query sees every key, and partly visible otherwise.  The
+// decision reads only each block's ranges, so it can call a pair partly visible
+// that is hidden or whole; the attention kernels then find out token by token.
+// Hidden pairs, most of a selection over packed clips, cost nothing after this.
+#include "prism_internal.cuh"
+
+namespace prism {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__global__ void __launch_bounds__(kThreads) k_score_tokens(Geo g, const int *__restrict__ perm,
+                                                           const float *__restrict__ pos, const int *__restrict__ doc,
+                                                           bool causal, const float *__restrict__ prefix,
+                                                           const float *__restrict__ slopes,
+                                                           float *__restrict__ pos_p, float *__restrict__ vis_p,
+                                                           int *__restrict__ doc_p, float *__restrict__ slopes_p) {
+    const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+    if (slopes && i < (size_t)g.heads) slopes_p[i] = slopes[i];
+    if (i >= (size_t)g.batch * g.N) return;
+    const int b = (int)(i / g.N), tok = perm[i];
+    const size_t src = (size_t)b * g.N + tok;
+    const float p = pos ? pos[src] : (float)(tok / (g.H * g.W));
+    const int d = doc ? doc[src] : 0;
+    pos_p[i] = p;
+    doc_p[i] = d < 0 ? -1 : d;
+    vis_p[i] = d < 0 ? INFINITY : !causal || (prefix && p < prefix[b]) ? -INFINITY : p;
+}
+
+// One warp per block.
+__global__ void __launch_bounds__(kThreads) k_score_blocks(Geo g, const int *__restrict__ nb, const int *__restrict__ blk_off,
+                                                           const float *__restrict__ pos, const float *__restrict__ vis,
+                                                           const int *__restrict__ doc, BlockRange *__restrict__ out) {
+    const int b = blockIdx.y, j = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (j >= nb[b]) return;
+    const int *bo = blk_off + (size_t)b * (g.nbmax + 1);
+    BlockRange r{INFINITY, -INFINITY, INFINITY, -INFINITY, 0x7fffffff, -1, 0, 0};
+    for (int n = bo[j] + lane; n < bo[j + 1]; n += 32) {
+        const size_t i = (size_t)b * g.N + n;
+        if (doc[i] < 0) {
+            ++r.pads;
+            continue;
+        }
+        ++r.tokens;
+        r.pmin = fminf(r.pmin, pos[i]);
+        r.pmax = fmaxf(r.pmax, pos[i]);
+        r.kmin = fminf(r.kmin, vis[i]);
+        r.kmax = fmaxf(r.kmax, vis[i]);
+        r.dmin = min(r.dmin, doc[i]);
+        r.dmax = max(r.dmax, doc[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        r.pmin = fminf(r.pmin, __shfl_xor_sync(0xffffffffu, r.pmin, o));
+        r.pmax = fmaxf(r.pmax, __shfl_xor_sync(0xffffffffu, r.pmax, o));
+        r.kmin = fminf(r.kmin, __shfl_xor_sync(0xffffffffu, r.kmin, o));
+        r.kmax = fmaxf(r.kmax, __shfl_xor_sync(0xffffffffu, r.kmax, o));
+        r.dmin = min(r.dmin, __shfl_xor_sync(0xffffffffu, r.dmin, o));
+        r.dmax = max(r.dmax, __shfl_xor_sync(0xffffffffu, r.dmax, o));
+        r.tokens += __shfl_xor_sync(0xffffffffu, r.tokens, o);
+        r.pads += __shfl_xor_sync(0xffffffffu, r.pads, o);
+    }
+    if (lane == 0) out[(size_t)b * g.nbmax + j] = r;
+}
+
+// 0 hidden, 1 whole, 2 partly visible
+__device__ __forceinline__ int pair_class(const BlockRange &q, const BlockRange &k) {
+    if (q.tokens == 0 || k.tokens == 0 || q.dmax < k.dmin || k.dmax < q.dmin || k.kmin > q.pmax) return 0;
+    const bool one = q.dmin == q.dmax && k.dmin == k.dmax && q.dmin == k.dmin;
+    return one && q.pads == 0 && k.pads == 0 && k.kmax <= q.pmin ? 1 : 2;
+}
+
+// One warp per list: the entries that are not hidden, in order, at the list's
+// own place; a list's end is written beside.  kCols: the list of a key block
+// holds query blocks.
+template <bool kCols>
+__global__ void __launch_bounds__(kThreads) k_score_filter(Geo g, const int *__restrict__ ptr, const int *__restrict__ list,
+                                                           const BlockRange *__restrict__ blk, int *__restrict__ end,
+                                                           int *__restrict__ out) {
+    const size_t lists = (size_t)g.batch * g.heads * g.nbmax;
+    const int lane = threadIdx.x & 31;
+    for (size_t r = (size_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < lists;
+         r += (size_t)gridDim.x * (kThreads / 32)) {
+        const int p0 = ptr[r], p1 = ptr[r + 1];
+        const BlockRange *bb = blk + r / g.nbmax / g.heads * g.nbmax;
+        int w = p0;
+        if (p0 < p1) {
+            const BlockRange own = bb[r % g.nbmax];
+            for (int u0 = p0; u0 < p1; u0 += 32) {
+                const int u = u0 + lane;
+                const int j = u < p1 ? list[u] : 0;
+                const int c = u < p1 ? (kCols ? pair_class(bb[j], own) : pair_class(own, bb[j])) : 0;
+                const unsigned kept = __ballot_sync(0xffffffffu, c != 0);
+                if (c) out[w + __popc(kept & ((1u << lane) - 1))] = 2 * j + (c == 2);
+                w += __popc(kept);
+            }
+        }
+        if (lane == 0) end[r] = w;
+    }
+}
+
+// Rows of padding tokens become zero: what they hold (infinities, NaN) would
+// reach other rows through products with P = 0.
+__global__ void __launch_bounds__(kThreads) k_zero_padding(Geo g, const int *__restrict__ doc, __nv_bfloat16 *__restrict__ Qp,
+                                                           __nv_bfloat16 *__restrict__ Kp, __nv_bfloat16 *__restrict__ Vp) {
+    const int b = blockIdx.y, n = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (n >= g.N || doc[(size_t)b * g.N + n] >= 0) return;
+    const int per = g.D / 8;
+    for (int i = lane; i < g.heads * per; i += 32) {
+        const size_t at = (((size_t)b * g.heads + i / per) * g.N + n) * g.D + i % per * 8;
+        *reinterpret_cast<uint4 *>(Qp + at) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(Kp + at) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(Vp + at) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+struct Buf {
+    void **p;
+    size_t bytes;
+};
+int buffers(Plan &pl, Buf *out) {
+    const Geo &g = pl.g;
+    Score &s = pl.score;
+    const size_t lists = (size_t)g.batch * g.heads * g.nbmax, nnz = lists * (size_t)pl.cap_stride;
+    const size_t tokens = (size_t)g.batch * g.N;
+    int n = 0;
+    out[n++] = {(void **)&s.slopes, (size_t)g.heads * sizeof(float)};
+    out[n++] = {(void **)&s.pos, tokens * sizeof(float)};
+    out[n++] = {(void **)&s.vis, tokens * sizeof(float)};
+    out[n++] = {(void **)&s.doc, tokens * sizeof(int)};
+    out[n++] = {(void **)&s.blk, (size_t)g.batch * g.nbmax * sizeof(BlockRange)};
+    out[n++] = {(void **)&s.row_end, lists * sizeof(int)};
+    out[n++] = {(void **)&s.colT_end, lists * sizeof(int)};
+    out[n++] = {(void **)&s.col, nnz * sizeof(int)};
+    out[n++] = {(void **)&s.rowT, nnz * sizeof(int)};
+    return n;
+}
+
+}  // namespace
+
+void release_score(Plan &pl) {
+    Buf b[16];
+    const int n = buffers(pl, b);
+    for (int k = 0; k < n; ++k)
+        if (*b[k].p) {
+            cudaFree(*b[k].p);
+            *b[k].p = nullptr;
+        }
+    pl.score.set = false;
+}
+
+prism_status launch_zero_padding(Plan &pl, cudaStream_t st) {
+    const Geo &g = pl.g;
+    k_zero_padding<<<dim3((g.N + kThreads / 32 - 1) / (kThreads / 32), g.batch), kThreads, 0, st>>>(g, pl.score.doc, pl.Qp,
+                                                                                                  pl.Kp, pl.Vp);
+    PRISM_CUDA_OK(cudaGetLastError());
+    return PRISM_OK;
+}
+
+prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
+    const Geo &g = pl.g;
+    Score &s = pl.score;
+    s.set = false;
+    if (!s.rowT) {
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        PRISM_CUDA_OK(cudaStreamIsCapturing(st, &cap));
+        if (cap != cudaStreamCaptureStatusNone)
+            return fail(PRISM_ERR_STATE, "a plan's first prism_plan_set_score allocates: make it before the capture");
+        Buf b[16];
+        const int n = buffers(pl, b);
+        for (int k = 0; k < n; ++k) {
+            const cudaError_t e = cudaMalloc(b[k].p, b[k].bytes);
+            if (e != cudaSuccess) {
+                *b[k].p = nullptr;
+                cudaGetLastError();  // the failed allocation is reported here, not by a later call
+                release_score(pl);
+                return fail_cuda(e, "cudaMalloc", __FILE__, __LINE__);
+            }
+        }
+    }
+    s.cap = in.cap;
+    s.has_bias = in.slopes != nullptr;
+    s.has_doc = in.doc != nullptr;
+    size_t n = (size_t)g.batch * g.N;
+    if ((size_t)g.heads > n) n = g.heads;
+    k_score_tokens<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(
+        g, pl.perm, in.pos, in.doc, in.causal != 0, in.prefix, in.slopes, s.pos, s.vis, s.doc, s.slopes);
+    PRISM_CUDA_OK(cudaGetLastError());
+    k_score_blocks<<<dim3((g.nbmax + kThreads / 32 - 1) / (kThreads / 32), g.batch), kThreads, 0, st>>>(
+        g, pl.nb, pl.blk_off, s.pos, s.vis, s.doc, s.blk);
+    PRISM_CUDA_OK(cudaGetLastError());
+    k_score_filter<false><<<1184, kThreads, 0, st>>>(g, pl.row_ptr, pl.col, s.blk, s.row_end, s.col);
+    PRISM_CUDA_OK(cudaGetLastError());
+    k_score_filter<true><<<1184, kThreads, 0, st>>>(g, pl.colT_ptr, pl.rowT, s.blk, s.colT_end, s.rowT);
+    PRISM_CUDA_OK(cudaGetLastError());
+    if (s.has_doc) {
+        const prism_status z = launch_zero_padding(pl, st);
+        if (z != PRISM_OK) return z;
+    }
+    s.set = true;
+    return PRISM_OK;
+}
+
+ScoreArgs score_args(const Plan &pl, bool backward) {
+    const Score &s = pl.score;
+    ScoreArgs a{};
+    a.list_end = backward ? s.colT_end : s.row_end;
+    a.pos = s.pos;
+    a.vis = s.vis;
+    a.doc = s.doc;
+    a.slopes = s.slopes;
+    if (s.cap > 0.f) {
+        a.cap_in = (float)(1.0 / (sqrt((double)pl.g.D) * (double)s.cap));
+        a.cap_out = (float)((double)s.cap * 1.4426950408889634);
+    }
+    return a;
+}
+
+}  // namespace prism

@@ -240,6 +240,54 @@ PRISM_API prism_status prism_attn_fwd_taylor(prism_plan *plan, void *O, float *l
 PRISM_API prism_status prism_attn_bwd(prism_plan *plan, const void *O, const void *dO, void *dQ, void *dK,
                             void *dV, void *stream);
 
+/* Scores and masks for the plan's attention, over the same selected blocks
+ * (the method has none: they serve packed and causal training of the layer).
+ * With s = q.k / sqrt(head_dim) of a query q and a key k in a selected block
+ * pair, the scored attention's logit is
+ *   cap tanh(s / cap) - slopes[h] |pos_q - pos_k|
+ * (s itself without a cap, no second term without slopes), and the pair counts
+ * only where doc_q = doc_k >= 0 and, when causal, pos_k <= pos_q or pos_k <
+ * prefix of the sample.  The selection itself does not look at any of it.
+ *   cap     0 (none) or in [1e-3, 1e6]
+ *   slopes  device fp32 [heads] (this plan's heads), finite; NULL: no bias
+ *   pos     device fp32 [batch][N] in raster order, finite; NULL: the token's
+ *           frame t.  Packed clips restart their positions.
+ *   doc     device int [batch][N]: the clip a token belongs to; negative:
+ *           padding, which sees nothing and is seen by nothing.  NULL: one clip.
+ *   causal  nonzero: a query sees keys at its own position and before
+ *   prefix  device fp32 [batch]; keys at positions below it are visible to
+ *           every query of their clip; NULL: none (needs causal)
+ * prism_plan_set_score copies what it is given (the arrays may be freed once
+ * the work on `stream` is done), removes the hidden block pairs from its own
+ * copy of the selection, and zeroes the rows of padding tokens in the plan's
+ * copies of Q, K and V (as do later prism_plan_update_qkv calls), so that what
+ * padding holds reaches nothing; values of visible tokens must be finite.  It
+ * belongs to the plan's current build: every build drops it.  The first call on
+ * a plan allocates (about 8 bytes per selectable block pair and 12 per token;
+ * PRISM_ERR_STATE while `stream` is being captured); it forgets the last
+ * forward.  PRISM_ERR_STATE before a build.                                 */
+typedef struct prism_score {
+    float cap;
+    const float *slopes, *pos;
+    const int *doc;
+    int causal;
+    const float *prefix;
+} prism_score;
+PRISM_API prism_status prism_plan_set_score(prism_plan *plan, const prism_score *score, void *stream);
+
+/* The forward with the scores of the last prism_plan_set_score: arguments,
+ * layouts and errors as prism_attn_fwd.  A query that sees no key (padding, or
+ * a row whose selected blocks are all hidden) gets O = 0 and lse = -inf.  The
+ * logits, their softmax and the log-sum-exp are fp32.                       */
+PRISM_API prism_status prism_attn_fwd_scored(prism_plan *plan, void *O, float *lse, void *stream);
+
+/* Its gradient with respect to Q, K and V: as prism_attn_bwd, with the factor
+ * 1 - tanh^2(s / cap) on dS.  Tokens that see or are seen by nothing get zero
+ * gradients, whatever O and dO hold for padding.  PRISM_ERR_STATE unless the
+ * plan's last forward was prism_attn_fwd_scored.                            */
+PRISM_API prism_status prism_attn_bwd_scored(prism_plan *plan, const void *O, const void *dO, void *dQ, void *dK,
+                                             void *dV, void *stream);
+
 /* Audio guidance for the plan: a[b][t][h][w] = || h^[b][n][:] ||_2, the L2
  * norm over `channels` of the audio-to-video cross-attention output of video
  * token n = (t*H + h)*W + w [Prism guide, Method section 1, the sentence
