@@ -342,6 +342,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // the scored form of the same: x from cap tanh(S / cap) and the bias, P = 0 where
                         // the key is hidden, dS times tanh's derivative 1 - tanh^2
                         tmem_wait_ld();
+                        bool small = true;
+                        if constexpr ((kScore & kCap) != 0) {  // (rows that are not active do not matter)
+                            float ma = 0.f, mb = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                ma = fmax3_abs(ma, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                                mb = fmax3_abs(mb, __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]));
+                            }
+                            small = __all_sync(0xffffffffu, !act || fmaxf(ma, mb) <= sc.cap_one);
+                        }
                         if (act) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -352,21 +362,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 float x0 = __uint_as_float(sv[q]), x1 = __uint_as_float(sv[q + 1]);
                                 float x2 = __uint_as_float(sv[q + 2]), x3 = __uint_as_float(sv[q + 3]);
                                 float m4 = scale_log2;
-                                uint64_t t02 = 0, t13 = 0;
+                                uint64_t g01 = 0, g23 = 0;  // 1 - tanh^2
+                                float4 N = lds_f4(vec + 16 * j);
+                                const float4 dl = lds_f4(vec + 256 + 16 * j);
                                 if constexpr ((kScore & kCap) != 0) {
-                                    tanh4(x0, x1, x2, x3, sc.cap_in, t02, t13);
-                                    x0 = plo(t02), x1 = plo(t13), x2 = phi(t02), x3 = phi(t13);
-                                    m4 = sc.cap_out;
+                                    if (small) {
+                                        const uint64_t ku = splat2(sc.cap_u), one = splat2(1.f), neg = splat2(-1.f);
+                                        const uint64_t t01 = tanh_small2(x0, x1, ku), t23 = tanh_small2(x2, x3, ku);
+                                        g01 = pfma(pmul(t01, t01), neg, one), g23 = pfma(pmul(t23, t23), neg, one);
+                                        x0 = plo(t01), x1 = phi(t01), x2 = plo(t23), x3 = phi(t23);
+                                        m4 = sc.cap_out;
+                                    } else {
+                                        uint64_t q02, q13;
+                                        logistic4(x0, x1, x2, x3, sc.cap_in, q02, q13);
+                                        x0 = plo(q02), x1 = plo(q13), x2 = phi(q02), x3 = phi(q13);
+                                        const uint64_t q01 = pair2(x0, x1), q23 = pair2(x2, x3);
+                                        const uint64_t four = splat2(4.f), m4q = splat2(-4.f);
+                                        g01 = pmul(q01, pfma(q01, m4q, four)), g23 = pmul(q23, pfma(q23, m4q, four));
+                                        m4 = -2.f * sc.cap_out;
+                                        N.x += sc.cap_out, N.y += sc.cap_out, N.z += sc.cap_out, N.w += sc.cap_out;
+                                    }
                                 }
-                                const float4 N = lds_f4(vec + 16 * j), dl = lds_f4(vec + 256 + 16 * j);
                                 if constexpr ((kScore & kBias) != 0) {
                                     x0 = fmaf(x0, m4, fmaf(-slope2, fabsf(pq.x - pk), N.x));
                                     x1 = fmaf(x1, m4, fmaf(-slope2, fabsf(pq.y - pk), N.y));
                                     x2 = fmaf(x2, m4, fmaf(-slope2, fabsf(pq.z - pk), N.z));
                                     x3 = fmaf(x3, m4, fmaf(-slope2, fabsf(pq.w - pk), N.w));
                                 } else {
-                                    x0 = fmaf(x0, m4, N.x), x1 = fmaf(x1, m4, N.y);
-                                    x2 = fmaf(x2, m4, N.z), x3 = fmaf(x3, m4, N.w);
+                                    fma2(x0, x1, splat2(m4), pair2(N.x, N.y), x0, x1);
+                                    fma2(x2, x3, splat2(m4), pair2(N.z, N.w), x2, x3);
                                 }
                                 float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
                                 if (part) {
@@ -380,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mul_sub2(p0, p1, __uint_as_float(dv[q]), __uint_as_float(dv[q + 1]), dl.x, dl.y, d0, d1);
                                 mul_sub2(p2, p3, __uint_as_float(dv[q + 2]), __uint_as_float(dv[q + 3]), dl.z, dl.w, d2, d3);
                                 if constexpr ((kScore & kCap) != 0) {
-                                    d0 *= fmaf(-plo(t02), plo(t02), 1.f), d1 *= fmaf(-plo(t13), plo(t13), 1.f);
-                                    d2 *= fmaf(-phi(t02), phi(t02), 1.f), d3 *= fmaf(-phi(t13), phi(t13), 1.f);
+                                    const uint64_t y01 = pmul(pair2(d0, d1), g01), y23 = pmul(pair2(d2, d3), g23);
+                                    d0 = plo(y01), d1 = phi(y01), d2 = plo(y23), d3 = phi(y23);
                                 }
                                 pd[2 * j] = pack_bf16x2(p0, p1);
                                 pd[2 * j + 1] = pack_bf16x2(p2, p3);

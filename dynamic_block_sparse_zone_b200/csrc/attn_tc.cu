@@ -46,9 +46,12 @@
 // the pairs that are only partly visible a key counts where its document is the
 // query's and the query's position has reached its visibility.  The producer
 // brings a chunk's key positions, visibilities and documents (128 each) into
-// one of two slots beside the segment mask; the softmax rewrites its 128 scores
-// in registers before the row max.  Block pairs that are wholly visible, most
-// of them, skip the mask.
+// one of two slots beside the segment mask; wholly visible pairs, most of
+// them, skip the mask.  What the score needs makes the softmax the longest
+// stage, so it has eight warps (two threads per row, 64 keys each) instead of
+// four: with four, capped scores issued 0.32 instructions per cycle and
+// scheduler, held by latency.  P of the second 64 keys then lies over its own
+// scores, TMEM columns [64, 96).
 #include <cuda.h>
 
 #include "tc_common.cuh"
@@ -59,9 +62,10 @@ using namespace tc;
 
 namespace fwdtc {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 192, kScoredThreads = 320;
 constexpr uint32_t kTmemCols = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kScoredThreshold = 24.0f;  // P and the sums are floating point: 2^24 costs them no digits
 
 template <int D>
 struct Layout {
@@ -87,14 +91,16 @@ struct Layout {
     // Scored variants: position, visibility and document of a chunk's 128 keys, two slots
     static constexpr uint32_t kMeta = (kBytes + 15) & ~15u;
     static constexpr uint32_t kMetaSlot = 3 * 512;
-    static constexpr uint32_t kScoreAlloc = kMeta + 2 * kMetaSlot + 1024;
+    // what the two threads of a row tell each other, and the quadrants' failure flags
+    static constexpr uint32_t kExch = kMeta + 2 * kMetaSlot;
+    static constexpr uint32_t kScoreAlloc = kExch + 2 * 512 + 16 + 1024;
 };
 
 // Site codes recorded with a timeout.
 enum { kSiteQ = 1, kSiteK, kSiteV, kSiteKEmpty, kSiteVEmpty, kSiteS, kSiteP, kSiteO, kSiteMask };
 
 template <int D, bool kTaylor, int kScore>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
     k_attn_fwd_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKb,
                   const __grid_constant__ CUtensorMap tmVb, const int *__restrict__ nbv, Geo g,
@@ -165,6 +171,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(bar_mk, 1);
             mbar_init(bar_mk + 8, 1);
             *abort_flag = 0;
+            if (kEnc)
+                for (int k = 0; k < 4; ++k) reinterpret_cast<volatile int *>(smem + L::kExch + 1024)[k] = 0;
             mbar_fence_init();
             prefetch_map(&tmQ);
             prefetch_map(&tmK);
@@ -287,9 +295,220 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mma_ts4<8, 16, 24, 128, 256, 384>(tO, tS, bV, idPV, c > 0);
                 if (!__all_sync(0xffffffffu, mbar_wait(bar_p2, c & 1, status, kSiteP, abort_flag))) break;
                 tc_fence_after();
-                if (full) mma_ts4<8, 16, 24, 128, 256, 384>(tO, tS + 32, bV + 512, idPV, 1u);
+                if (full) mma_ts4<8, 16, 24, 128, 256, 384>(tO, tS + (kEnc ? 64 : 32), bV + 512, idPV, 1u);
                 mma_commit(bar_ve);
                 mma_commit(bar_o);
+            }
+        }
+    } else if constexpr (kEnc) {
+        // ------------------------------------------------------------ scored softmax
+        // Two threads per row, one for each 64-key segment of the chunk (warps
+        // 2..5 the first, 6..9 the second).  They share the row's reference m:
+        // one barrier with an OR per chunk tells the two warps of a quadrant
+        // whether any of their rows' maxima has outgrown it, which is rare.
+        const int quad = warp & 3, seg = (warp - 2) >> 2;
+        const int rowid = quad * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        const int half = shared_tile ? (quad >> 1) : 0;  // which query block's rows (warp-uniform)
+        volatile float *exch = reinterpret_cast<volatile float *>(smem + L::kExch);  // [seg][row]
+        volatile int *failed = reinterpret_cast<volatile int *>(smem + L::kExch + 1024) + quad;
+        // this row's position, document (no key has -2) and slope in log2 units
+        float pq = 0.f, slope2 = 0.f;
+        int dq = -2;
+        if (rowid < qvalid) {
+            pq = sc.pos[(size_t)b * g.N + q0 + rowid];
+            dq = sc.doc[(size_t)b * g.N + q0 + rowid];
+        }
+        if (kScore & kBias) slope2 = sc.slopes[h] * 1.4426950408889634f;
+        constexpr bool kScaled = (kScore & (kCap | kBias)) != 0;  // x is put in log2 units before the maximum
+        const uint32_t tSr = tS + lane_off + seg * 64;
+        for (int c = 0; c < nchunk_all; ++c) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_mk + 8 * (c & 1), (c >> 1) & 1, status, kSiteMask, abort_flag));
+            const uint32_t mw = mask_w[c & 1];
+            const bool live = ok && ((mw >> (2 * seg + half)) & 1u);
+            const bool part = (mw >> (4 + 2 * seg + half)) & 1u;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_s, c & 1, status, kSiteS, abort_flag));
+            tc_fence_after();
+            uint32_t sr[64];
+            float mx = -INFINITY;
+            if (live && ok) {
+                tmem_ld32(tSr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+                tmem_ld32(tSr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+                tmem_wait_ld();
+                const uint32_t meta = sbase + L::kMeta + (c & 1) * L::kMetaSlot + seg * 256;
+                bool small = true;
+                if constexpr ((kScore & kCap) != 0) {
+                    float ma = 0.f, mb = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        const float *x = reinterpret_cast<const float *>(&sr[e]);
+                        ma = fmax3_abs(ma, x[0], x[1]);
+                        mb = fmax3_abs(mb, x[2], x[3]);
+                    }
+                    small = __all_sync(0xffffffffu, fmaxf(ma, mb) <= sc.cap_one);
+                    if (!small) {  // q of every score in place
+#pragma unroll
+                        for (int e = 0; e < 64; e += 4) {
+                            float *x = reinterpret_cast<float *>(&sr[e]);
+                            uint64_t q02, q13;
+                            logistic4(x[0], x[1], x[2], x[3], sc.cap_in, q02, q13);
+                            x[0] = plo(q02), x[1] = plo(q13), x[2] = phi(q02), x[3] = phi(q13);
+                        }
+                    } else {  // tanh in place
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) {
+                            float *x = reinterpret_cast<float *>(&sr[e]);
+                            const uint64_t t = tanh_small2(x[0], x[1], splat2(sc.cap_u));
+                            x[0] = plo(t), x[1] = phi(t);
+                        }
+                    }
+                }
+                if constexpr (kScaled) {  // the score in log2 units: what is in place times k2, plus a
+                    const float k = !(kScore & kCap) ? scale_log2 : small ? sc.cap_out : -2.f * sc.cap_out;
+                    const float a = !(kScore & kCap) || small ? 0.f : sc.cap_out;
+                    const uint64_t k2 = splat2(k);
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        float *x = reinterpret_cast<float *>(&sr[e]);
+                        uint64_t a01 = splat2(a), a23 = splat2(a);
+                        if constexpr ((kScore & kBias) != 0) {
+                            const float4 pk = lds_f4(meta + e * 4);
+                            a01 = pair2(fmaf(-slope2, fabsf(pq - pk.x), a), fmaf(-slope2, fabsf(pq - pk.y), a));
+                            a23 = pair2(fmaf(-slope2, fabsf(pq - pk.z), a), fmaf(-slope2, fabsf(pq - pk.w), a));
+                        }
+                        const uint64_t y01 = pfma(pair2(x[0], x[1]), k2, a01), y23 = pfma(pair2(x[2], x[3]), k2, a23);
+                        x[0] = plo(y01), x[1] = phi(y01), x[2] = plo(y23), x[3] = phi(y23);
+                    }
+                }
+                if (part) {
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        const float4 vk = lds_f4(meta + 512 + e * 4);
+                        const float4 dk = lds_f4(meta + 1024 + e * 4);
+                        const uint32_t ninf = 0xff800000u;
+                        if (!(vk.x <= pq && __float_as_int(dk.x) == dq)) sr[e] = ninf;
+                        if (!(vk.y <= pq && __float_as_int(dk.y) == dq)) sr[e + 1] = ninf;
+                        if (!(vk.z <= pq && __float_as_int(dk.z) == dq)) sr[e + 2] = ninf;
+                        if (!(vk.w <= pq && __float_as_int(dk.w) == dq)) sr[e + 3] = ninf;
+                    }
+                }
+                float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 64; e += 8) {
+                    const float *v = reinterpret_cast<const float *>(&sr[e]);
+                    mxa = fmax3(mxa, v[0], v[1]);
+                    mxb = fmax3(mxb, v[2], v[3]);
+                    mxc = fmax3(mxc, v[4], v[5]);
+                    mxd = fmax3(mxd, v[6], v[7]);
+                }
+                mx = fmaxf(fmaxf(mxa, mxb), fmaxf(mxc, mxd));
+                if (!kScaled) mx *= scale_log2;
+            }
+            // one barrier per chunk on every path: a warp whose wait failed meets its
+            // partner here and they leave together
+            if (!ok && lane == 0) *failed = 1;
+            if (named_bar_or(1 + quad, 64, !ok || mx > m + kScoredThreshold)) {
+                if (*failed) {
+                    ok = false;
+                    break;
+                }
+                exch[seg * 128 + rowid] = mx;
+                named_bar_sync(1 + quad, 64);
+                const float both = fmaxf(mx, exch[(seg ^ 1) * 128 + rowid]);
+                // the same answer in both threads; a row that has seen no key has m = -inf, l = 0, O = 0
+                const float mnew = both > m + kScoredThreshold ? both : m;
+                const float corr = ex2(m - (mnew == -INFINITY ? 0.f : mnew));
+                if (c > 0) {  // each thread one half of O's columns
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t orr[16];
+                        tmem_ld16(tO + lane_off + seg * (D / 2) + q * 16, orr);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            orr[e] = __float_as_uint(__uint_as_float(orr[e]) * (mnew == m ? 1.f : corr));
+                        tmem_st16(tO + lane_off + seg * (D / 2) + q * 16, orr);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                if (mnew != m) {
+                    l *= corr;
+                    m = mnew;
+                }
+                named_bar_sync(1 + quad, 64);  // O is whole again before either publishes its P
+                tc_fence_after();
+            }
+            // P = exp2(x - m), bf16 pairs over the segment's own scores
+            if (live) {
+                const uint64_t s2 = splat2(kScaled ? 1.0f : scale_log2), c2 = splat2(m == -INFINITY ? 0.f : -m);
+                uint64_t acc2 = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float x0, x1;
+                        fma2(__uint_as_float(sr[16 * q + 2 * e]), __uint_as_float(sr[16 * q + 2 * e + 1]), s2, c2, x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        add2(acc2, p0, p1);
+                        pk[e] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st8(tSr + 8 * q, pk);
+                }
+                l += sum2(acc2);
+            } else if (seg == 0 || chunk_full(c)) {
+                uint32_t z[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[e] = 0u;
+                tmem_st16(tSr, z);
+                tmem_st16(tSr + 16, z);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(seg == 0 ? bar_p : bar_p2);
+        }
+        // epilogue: the row's sum, then each thread one half of O's columns
+        if (ok) {
+            exch[seg * 128 + rowid] = l;
+            named_bar_sync(1 + quad, 64);
+            l = exch[rowid] + exch[128 + rowid];
+            if (nchunk_all > 0)  // the last product P V must have landed
+                ok = __all_sync(0xffffffffu, mbar_wait(bar_o, (nchunk_all - 1) & 1, status, kSiteO, abort_flag));
+        }
+        if (ok) {
+            tc_fence_after();
+            const bool empty = l == 0.f;  // no key is visible: O = 0, log-sum-exp -inf
+            const float inv = 1.f / l;
+            const int n = q0 + rowid;
+            const bool write = rowid < qvalid;
+            const int tok = write ? perm[(size_t)b * g.N + n] : 0;
+            __nv_bfloat16 *dst = O + (((size_t)b * g.N + tok) * g.heads + h) * D + seg * (D / 2);
+#pragma unroll 1
+            for (int q = 0; q < D / 64; ++q) {
+                uint32_t orr[32];
+                tmem_ld32(tO + lane_off + seg * (D / 2) + q * 32, orr);
+                tmem_wait_ld();
+                uint4 pkt[4];
+                uint32_t *pw = reinterpret_cast<uint32_t *>(pkt);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    pw[e] = pack_bf16x2(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
+                    if (empty) pw[e] = 0u;
+                }
+                if (write) {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(dst + q * 32);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d4[e] = pkt[e];
+                }
+            }
+            if (write && seg == 0) {
+                const float lse2 = empty ? -INFINITY : m + __log2f(l);
+                // negated: the backward's exp2 addend; an empty row's is -inf (P = 0)
+                nlse_p[(size_t)bh * g.N + n] = empty ? -INFINITY : -lse2;
+                if (lse_user) lse_user[(size_t)bh * g.N + tok] = lse2 * 0.69314718055994531f;
             }
         }
     } else {
@@ -302,30 +521,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t bias_s = sbase + L::kBias + quad * 512;  // this warp's 128 column biases
         const int half = shared_tile ? (quad >> 1) : 0;        // which query block's rows (warp-uniform)
         const int8_t *lgh = lg + half * lgs;
-        // scored: this row's position, document (no key has -2) and slope in log2 units
-        float pq = 0.f, slope2 = 0.f;
-        int dq = -2;
-        if constexpr (kEnc) {
-            if (rowid < qvalid) {
-                pq = sc.pos[(size_t)b * g.N + q0 + rowid];
-                dq = sc.doc[(size_t)b * g.N + q0 + rowid];
-            }
-            if (kScore & kBias) slope2 = sc.slopes[h] * 1.4426950408889634f;
-        }
         for (int c = 0; c < nchunk_all; ++c) {
             const bool pooled = kTaylor && c >= nchunk;
             // segments of this chunk outside this half's selection get P = 0
-            bool live0 = true, live1 = true, part0 = false, part1 = false;
-            if (kEnc || (shared_tile && !pooled)) {
+            bool live0 = true, live1 = true;
+            if (shared_tile && !pooled) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar_mk + 8 * (c & 1), (c >> 1) & 1, status, kSiteMask, abort_flag));
                 if (!ok) break;
                 const uint32_t mw = mask_w[c & 1];
                 live0 = (mw >> half) & 1u;
                 live1 = (mw >> (2 + half)) & 1u;
-                if (kEnc) {
-                    part0 = (mw >> (4 + half)) & 1u;
-                    part1 = (mw >> (6 + half)) & 1u;
-                }
             }
             if (pooled) {  // biases of this chunk's pooled keys, before S lands
                 float *bias = reinterpret_cast<float *>(smem + L::kBias + quad * 512);
@@ -349,50 +554,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int q = 0; q < 4; ++q)
                 if (q < nq) tmem_ld32(tSr + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
             tmem_wait_ld();
-            // scored: S becomes cap tanh(S / cap) - slope |p_q - p_k| in log2 units
-            // in place (only the mask: S as it is), -inf where the key is hidden
-            if constexpr (kEnc) {
-                const uint32_t meta = sbase + L::kMeta + (c & 1) * L::kMetaSlot;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (q < nq && (q < 2 ? live0 : live1)) {
-                        if constexpr ((kScore & (kCap | kBias)) != 0) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                float *x = reinterpret_cast<float *>(&sr[32 * q + e]);
-                                float m4 = scale_log2, x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
-                                if constexpr ((kScore & kCap) != 0) {
-                                    uint64_t t02, t13;
-                                    tanh4(x0, x1, x2, x3, sc.cap_in, t02, t13);
-                                    x0 = plo(t02), x1 = plo(t13), x2 = phi(t02), x3 = phi(t13);
-                                    m4 = sc.cap_out;
-                                }
-                                if constexpr ((kScore & kBias) != 0) {
-                                    const float4 pk = lds_f4(meta + (32 * q + e) * 4);
-                                    x[0] = fmaf(x0, m4, -slope2 * fabsf(pq - pk.x));
-                                    x[1] = fmaf(x1, m4, -slope2 * fabsf(pq - pk.y));
-                                    x[2] = fmaf(x2, m4, -slope2 * fabsf(pq - pk.z));
-                                    x[3] = fmaf(x3, m4, -slope2 * fabsf(pq - pk.w));
-                                } else {
-                                    x[0] = x0 * m4, x[1] = x1 * m4, x[2] = x2 * m4, x[3] = x3 * m4;
-                                }
-                            }
-                        }
-                        if (q < 2 ? part0 : part1) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 vk = lds_f4(meta + 512 + (32 * q + e) * 4);
-                                const float4 dk = lds_f4(meta + 1024 + (32 * q + e) * 4);
-                                uint32_t *x = &sr[32 * q + e];
-                                const uint32_t ninf = 0xff800000u;
-                                if (!(vk.x <= pq && __float_as_int(dk.x) == dq)) x[0] = ninf;
-                                if (!(vk.y <= pq && __float_as_int(dk.y) == dq)) x[1] = ninf;
-                                if (!(vk.z <= pq && __float_as_int(dk.z) == dq)) x[2] = ninf;
-                                if (!(vk.w <= pq && __float_as_int(dk.w) == dq)) x[3] = ninf;
-                            }
-                        }
-                    }
-            }
             // pass 1: row max (three-input max, four independent chains).  Pooled
             // chunks first turn S into x = S*scale*log2e + bias in place.
             float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
@@ -437,8 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
             }
             const float mx = fmaxf(fmaxf(mxa, mxb), fmaxf(mxc, mxd));
-            const bool scaled = pooled || (kScore & (kCap | kBias)) != 0;  // x is in log2 units already
-            const float mx2 = scaled ? mx : mx * scale_log2;
+            const float mx2 = pooled ? mx : mx * scale_log2;
             const bool need = (c > 0) && (mx2 > m + kRescaleThreshold);
             if (c == 0) m = mx2;
             // TMEM loads / stores are warp-collective: the whole warp rescales when
@@ -446,8 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // holds every earlier chunk: S_c was issued after P_{c-1} V_{c-1}.
             if (__any_sync(0xffffffffu, need)) {
                 const float mnew = fmaxf(m, mx2);
-                // (scored: a row that has seen no key yet has m = -inf, l = 0, O = 0)
-                const float corr = ex2(m - (kEnc && mnew == -INFINITY ? 0.f : mnew));
+                const float corr = ex2(m - mnew);
 #pragma unroll 1
                 for (int q = 0; q < D / 16; ++q) {
                     uint32_t orr[16];
@@ -464,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // (group q packs into columns [16q, 16q+16); all of S is in registers).
             // (scale, -m) and the running sum as packed fp32 pairs; a pooled
             // chunk's registers already hold the scaled, biased x.
-            const uint64_t s2 = splat2(scaled ? 1.0f : scale_log2), c2 = splat2(kEnc && m == -INFINITY ? 0.f : -m);
+            const uint64_t s2 = splat2(pooled ? 1.0f : scale_log2), c2 = splat2(-m);
             uint64_t acc2 = 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -500,9 +659,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         // epilogue: the last product P V must have landed
         if (ok && nchunk_all > 0)
             ok = __all_sync(0xffffffffu, mbar_wait(bar_o, (nchunk_all - 1) & 1, status, kSiteO, abort_flag));
-        if (ok && (kEnc || nchunk_all > 0)) {
+        if (ok && nchunk_all > 0) {
             tc_fence_after();
-            const bool empty = kEnc && l == 0.f;  // no key is visible: O = 0, log-sum-exp -inf
             const float inv = 1.f / l;
             const int n = q0 + rowid;
             const bool write = rowid < qvalid;
@@ -516,10 +674,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 uint4 pkt[4];
                 uint32_t *pw = reinterpret_cast<uint32_t *>(pkt);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 16; ++e)
                     pw[e] = pack_bf16x2(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
-                    if (empty) pw[e] = 0u;
-                }
                 if (write) {
                     uint4 *d4 = reinterpret_cast<uint4 *>(dst + q * 32);
 #pragma unroll
@@ -527,9 +683,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             if (write) {
-                const float lse2 = empty ? -INFINITY : m + __log2f(l);
-                // negated, log2 units: the backward's exp2 addend (an empty row's is -inf: P = 0)
-                if (!kTaylor) nlse_p[(size_t)bh * g.N + n] = empty ? -INFINITY : -lse2;
+                const float lse2 = m + __log2f(l);
+                if (!kTaylor) nlse_p[(size_t)bh * g.N + n] = -lse2;  // negated, log2 units: the backward's exp2 addend
                 if (lse_user) lse_user[(size_t)bh * g.N + tok] = lse2 * 0.69314718055994531f;
             }
         }
@@ -636,7 +791,8 @@ static prism_status fwd_tc_impl(Plan &pl, void *O, float *lse, cudaStream_t st) 
                           : kScore ? fwdtc::Layout<D>::kScoreAlloc
                                    : fwdtc::Layout<D>::kAlloc;
     TimerScope ts(pl, kTaylor ? kTAttnFwdTaylor : kTAttnFwd, st);
-    fwdtc::k_attn_fwd_tc<D, kTaylor, kScore><<<dim3(g.nbmax, g.batch * g.heads), fwdtc::kThreads, smem, st>>>(
+    fwdtc::k_attn_fwd_tc<D, kTaylor, kScore><<<dim3(g.nbmax, g.batch * g.heads),
+                                                kScore ? fwdtc::kScoredThreads : fwdtc::kThreads, smem, st>>>(
         pl.tmQ, pl.tmK, pl.tmV, pl.tmKb, pl.tmVb, pl.nb, g, pl.nqt, pl.qt_row, pl.qt_blk, pl.blk_off, pl.row_ptr,
         kScore ? pl.score.col : pl.col, pl.perm, static_cast<__nv_bfloat16 *>(O), lse, pl.nlse_p, scale_log2, pl.status,
         kScore ? score_args(pl, false) : ScoreArgs{});

@@ -165,7 +165,9 @@ struct ScoreArgs {
     const float *pos, *vis;
     const int *doc;
     const float *slopes;
-    float cap_in;               // 1 / (sqrt(D) cap)
+    float cap_u;                // 1 / (sqrt(D) cap)
+    float cap_one;              // sqrt(D) cap: unscaled scores up to here have |u| <= 1
+    float cap_in;               // 2 log2(e) / (sqrt(D) cap)
     float cap_out;              // cap log2(e)
 };
 ScoreArgs score_args(const Plan &pl, bool backward);

@@ -217,7 +217,9 @@ ScoreArgs score_args(const Plan &pl, bool backward) {
     a.doc = s.doc;
     a.slopes = s.slopes;
     if (s.cap > 0.f) {
-        a.cap_in = (float)(1.0 / (sqrt((double)pl.g.D) * (double)s.cap));
+        a.cap_one = (float)(sqrt((double)pl.g.D) * (double)s.cap);
+        a.cap_u = (float)(1.0 / (sqrt((double)pl.g.D) * (double)s.cap));
+        a.cap_in = (float)(2.0 * 1.4426950408889634 / (sqrt((double)pl.g.D) * (double)s.cap));
         a.cap_out = (float)((double)s.cap * 1.4426950408889634);
     }
     return a;

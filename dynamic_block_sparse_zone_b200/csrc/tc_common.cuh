@@ -169,6 +169,16 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(nthreads) : "memory");
 }
+// the same barrier, and whether any of its threads has p set
+__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(id), "r"(nthreads), "r"((uint32_t)p)
+        : "memory");
+    return r != 0;
+}
 // shared-memory accesses by 32-bit shared-window address
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     float4 v;
@@ -219,6 +229,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
                  :
                  : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n"
+                 :
+                 : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
@@ -381,6 +398,11 @@ __device__ __forceinline__ uint64_t pmul(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ uint64_t padd(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ float plo(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float phi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 __device__ __forceinline__ float rcp(float x) {
@@ -388,37 +410,47 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
-// tanh of k x0 .. k x3 (as pairs): u P(u^2) / Q(u^2) with P and Q of degree 4,
-// fitted to tanh on [0, 9] for the least largest error (absolute error below
-// 4e-7 in fp32, checked on a grid), u held within +-9 where tanh is within
-// 4e-8 of +-1.  The special-function unit already gives one exp2 per score, so
-// the quotient takes one reciprocal for the four scores (Q lies in [1, 416], so
-// the product of four is far from overflow) and the rest runs as packed fp32.
-__device__ __forceinline__ void tanh4(float x0, float x1, float x2, float x3, float k, uint64_t &t02, uint64_t &t13) {
-    const uint64_t k2 = splat2(k);
-    const uint64_t a = pmul(pair2(x0, x2), k2), b = pmul(pair2(x1, x3), k2);
-    const uint64_t u = pair2(fminf(fmaxf(plo(a), -9.f), 9.f), fminf(fmaxf(phi(a), -9.f), 9.f));
-    const uint64_t v = pair2(fminf(fmaxf(plo(b), -9.f), 9.f), fminf(fmaxf(phi(b), -9.f), 9.f));
-    const uint64_t wu = pmul(u, u), wv = pmul(v, v);
-    const uint64_t p4 = splat2(1.31836876e-08f), p3 = splat2(2.04714787e-05f), p2 = splat2(3.48656274e-03f),
-                   p1 = splat2(1.33731826e-01f), p0 = splat2(9.99999907e-01f);
-    const uint64_t q4 = splat2(7.70245336e-07f), q3 = splat2(3.27135234e-04f), q2 = splat2(2.58419093e-02f),
-                   q1 = splat2(4.67064795e-01f), q0 = splat2(1.0f);
-    const uint64_t pu = pmul(u, pfma(pfma(pfma(pfma(p4, wu, p3), wu, p2), wu, p1), wu, p0));
-    const uint64_t pv = pmul(v, pfma(pfma(pfma(pfma(p4, wv, p3), wv, p2), wv, p1), wv, p0));
-    const uint64_t qu = pfma(pfma(pfma(pfma(q4, wu, q3), wu, q2), wu, q1), wu, q0);
-    const uint64_t qv = pfma(pfma(pfma(pfma(q4, wv, q3), wv, q2), wv, q1), wv, q0);
-    const uint64_t m = pmul(qu, qv);  // (q0 q1, q2 q3)
-    const uint64_t r = pmul(splat2(rcp(plo(m) * phi(m))), pair2(phi(m), plo(m)));  // (1 / q0 q1, 1 / q2 q3)
-    t02 = pmul(pu, pmul(r, qv));
-    t13 = pmul(pv, pmul(r, qu));
-}
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
+
+// tanh u for capped scores, u = s / cap, in two forms; a warp takes the first
+// where all of its scores have |u| <= 1 (caps are set well above the usual
+// score).  Both are off by at most a few 2^-24 of the largest score in hand.
+//
+// |u| <= 1: u P(u^2), P of degree 6 fitted to tanh(u) / u for the least largest
+// relative error (5e-8; 1.6e-7 with fp32's rounding, checked on a grid).  (0, 1)
+// and (2, 3) of four scores per call; no special-function unit.
+__device__ __forceinline__ uint64_t tanh_small2(float x0, float x1, uint64_t k) {
+    const uint64_t u = pmul(pair2(x0, x1), k), w = pmul(u, u);
+    uint64_t p = pfma(splat2(1.0410445977e-3f), w, splat2(-6.2034507282e-3f));
+    p = pfma(p, w, splat2(2.0290071145e-2f));
+    p = pfma(p, w, splat2(-5.3457085043e-2f));
+    p = pfma(p, w, splat2(1.3325205445e-1f));
+    p = pfma(p, w, splat2(-3.3332839608e-1f));
+    p = pfma(p, w, splat2(9.9999994040e-1f));
+    return pmul(u, p);
+}
+// any u: q_i = 1 / (1 + exp(2 u_i)) of four scores (2 u_i log2(e) = k2 x_i), as the
+// pairs (0, 2) and (1, 3): tanh u = 1 - 2 q, 1 - tanh^2 u = 4 q (1 - q), absolute
+// error of tanh about 2e-7.  The four reciprocals are one of the product
+// (exponents are held below 30, so it stays under 2^121; tanh is 1 to fp32
+// beyond 10.4).  5 instructions and 1.25 special-function results per score; a
+// quotient of polynomials on [0, 9] took 9 instructions.
+__device__ __forceinline__ void logistic4(float x0, float x1, float x2, float x3, float k2, uint64_t &q02, uint64_t &q13) {
+    const float e0 = ex2(fminf(x0 * k2, 30.f)), e1 = ex2(fminf(x1 * k2, 30.f));
+    const float e2 = ex2(fminf(x2 * k2, 30.f)), e3 = ex2(fminf(x3 * k2, 30.f));
+    const uint64_t one = splat2(1.f);
+    const uint64_t a = padd(pair2(e0, e2), one), b = padd(pair2(e1, e3), one);
+    const uint64_t m = pmul(a, b);                                           // (a0 b1, a2 b3)
+    const uint64_t r = pmul(splat2(rcp(plo(m) * phi(m))), pair2(phi(m), plo(m)));  // their reciprocals
+    q02 = pmul(r, b);
+    q13 = pmul(r, a);
+}
+// max(m, |a|, |b|)
+__device__ __forceinline__ float fmax3_abs(float m, float a, float b) { return fmax3(m, fabsf(a), fabsf(b)); }
 
 }  // namespace tc
 }  // namespace prism
