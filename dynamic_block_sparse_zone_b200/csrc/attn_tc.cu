@@ -331,78 +331,85 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
             const bool part = (mw >> (4 + 2 * seg + half)) & 1u;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_s, c & 1, status, kSiteS, abort_flag));
             tc_fence_after();
-            uint32_t sr[64];
+            // pass 1, 32 scores at a time (few enough live values for the arithmetic to
+            // interleave): the logit in log2 units back to TMEM, and its maximum
             float mx = -INFINITY;
             if (live && ok) {
-                tmem_ld32(tSr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-                tmem_ld32(tSr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-                tmem_wait_ld();
-                const uint32_t meta = sbase + L::kMeta + (c & 1) * L::kMetaSlot + seg * 256;
-                bool small = true;
-                if constexpr ((kScore & kCap) != 0) {
-                    float ma = 0.f, mb = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        const float *x = reinterpret_cast<const float *>(&sr[e]);
-                        ma = fmax3_abs(ma, x[0], x[1]);
-                        mb = fmax3_abs(mb, x[2], x[3]);
-                    }
-                    small = __all_sync(0xffffffffu, fmaxf(ma, mb) <= sc.cap_one);
-                    if (!small) {  // q of every score in place
-#pragma unroll
-                        for (int e = 0; e < 64; e += 4) {
-                            float *x = reinterpret_cast<float *>(&sr[e]);
-                            uint64_t q02, q13;
-                            logistic4(x[0], x[1], x[2], x[3], sc.cap_in, q02, q13);
-                            x[0] = plo(q02), x[1] = plo(q13), x[2] = phi(q02), x[3] = phi(q13);
-                        }
-                    } else {  // tanh in place
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            float *x = reinterpret_cast<float *>(&sr[e]);
-                            const uint64_t t = tanh_small2(x[0], x[1], splat2(sc.cap_u));
-                            x[0] = plo(t), x[1] = phi(t);
-                        }
-                    }
-                }
-                if constexpr (kScaled) {  // the score in log2 units: what is in place times k2, plus a
-                    const float k = !(kScore & kCap) ? scale_log2 : small ? sc.cap_out : -2.f * sc.cap_out;
-                    const float a = !(kScore & kCap) || small ? 0.f : sc.cap_out;
-                    const uint64_t k2 = splat2(k);
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        float *x = reinterpret_cast<float *>(&sr[e]);
-                        uint64_t a01 = splat2(a), a23 = splat2(a);
-                        if constexpr ((kScore & kBias) != 0) {
-                            const float4 pk = lds_f4(meta + e * 4);
-                            a01 = pair2(fmaf(-slope2, fabsf(pq - pk.x), a), fmaf(-slope2, fabsf(pq - pk.y), a));
-                            a23 = pair2(fmaf(-slope2, fabsf(pq - pk.z), a), fmaf(-slope2, fabsf(pq - pk.w), a));
-                        }
-                        const uint64_t y01 = pfma(pair2(x[0], x[1]), k2, a01), y23 = pfma(pair2(x[2], x[3]), k2, a23);
-                        x[0] = plo(y01), x[1] = phi(y01), x[2] = plo(y23), x[3] = phi(y23);
-                    }
-                }
-                if (part) {
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        const float4 vk = lds_f4(meta + 512 + e * 4);
-                        const float4 dk = lds_f4(meta + 1024 + e * 4);
-                        const uint32_t ninf = 0xff800000u;
-                        if (!(vk.x <= pq && __float_as_int(dk.x) == dq)) sr[e] = ninf;
-                        if (!(vk.y <= pq && __float_as_int(dk.y) == dq)) sr[e + 1] = ninf;
-                        if (!(vk.z <= pq && __float_as_int(dk.z) == dq)) sr[e + 2] = ninf;
-                        if (!(vk.w <= pq && __float_as_int(dk.w) == dq)) sr[e + 3] = ninf;
-                    }
-                }
                 float mxa = -INFINITY, mxb = -INFINITY, mxc = -INFINITY, mxd = -INFINITY;
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t sr[32];
+                    tmem_ld32(tSr + 32 * q, sr);
+                    const uint32_t meta = sbase + L::kMeta + (c & 1) * L::kMetaSlot + seg * 256 + q * 128;
+                    tmem_wait_ld();
+                    float k = scale_log2, a = 0.f;  // the logit is what is in place times k, plus a and the bias
+                    if constexpr ((kScore & kCap) != 0) {
+                        float ma = 0.f, mb = 0.f;
 #pragma unroll
-                for (int e = 0; e < 64; e += 8) {
-                    const float *v = reinterpret_cast<const float *>(&sr[e]);
-                    mxa = fmax3(mxa, v[0], v[1]);
-                    mxb = fmax3(mxb, v[2], v[3]);
-                    mxc = fmax3(mxc, v[4], v[5]);
-                    mxd = fmax3(mxd, v[6], v[7]);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float *x = reinterpret_cast<const float *>(&sr[e]);
+                            ma = fmax3_abs(ma, x[0], x[1]);
+                            mb = fmax3_abs(mb, x[2], x[3]);
+                        }
+                        if (__all_sync(0xffffffffu, fmaxf(ma, mb) <= sc.cap_one)) {  // tanh in place
+                            const uint64_t ku = splat2(sc.cap_u);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float *x = reinterpret_cast<float *>(&sr[e]);
+                                const uint64_t t = tanh_small2(x[0], x[1], ku);
+                                x[0] = plo(t), x[1] = phi(t);
+                            }
+                            k = sc.cap_out;
+                        } else {  // q of every score in place
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                float *x = reinterpret_cast<float *>(&sr[e]);
+                                uint64_t q02, q13;
+                                logistic4(x[0], x[1], x[2], x[3], sc.cap_in, q02, q13);
+                                x[0] = plo(q02), x[1] = plo(q13), x[2] = phi(q02), x[3] = phi(q13);
+                            }
+                            k = -2.f * sc.cap_out;
+                            a = sc.cap_out;
+                        }
+                    }
+                    if constexpr (kScaled) {
+                        const uint64_t k2 = splat2(k);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            float *x = reinterpret_cast<float *>(&sr[e]);
+                            uint64_t a01 = splat2(a), a23 = splat2(a);
+                            if constexpr ((kScore & kBias) != 0) {
+                                const float4 pk = lds_f4(meta + e * 4);
+                                a01 = pair2(fmaf(-slope2, fabsf(pq - pk.x), a), fmaf(-slope2, fabsf(pq - pk.y), a));
+                                a23 = pair2(fmaf(-slope2, fabsf(pq - pk.z), a), fmaf(-slope2, fabsf(pq - pk.w), a));
+                            }
+                            const uint64_t y01 = pfma(pair2(x[0], x[1]), k2, a01), y23 = pfma(pair2(x[2], x[3]), k2, a23);
+                            x[0] = plo(y01), x[1] = phi(y01), x[2] = plo(y23), x[3] = phi(y23);
+                        }
+                    }
+                    if (part) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 vk = lds_f4(meta + 512 + e * 4);
+                            const float4 dk = lds_f4(meta + 1024 + e * 4);
+                            const uint32_t ninf = 0xff800000u;
+                            if (!(vk.x <= pq && __float_as_int(dk.x) == dq)) sr[e] = ninf;
+                            if (!(vk.y <= pq && __float_as_int(dk.y) == dq)) sr[e + 1] = ninf;
+                            if (!(vk.z <= pq && __float_as_int(dk.z) == dq)) sr[e + 2] = ninf;
+                            if (!(vk.w <= pq && __float_as_int(dk.w) == dq)) sr[e + 3] = ninf;
+                        }
+                    }
+                    if (kScaled || part) tmem_st32(tSr + 32 * q, sr);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        const float *v = reinterpret_cast<const float *>(&sr[e]);
+                        mxa = fmax3(mxa, v[0], v[1]);
+                        mxb = fmax3(mxb, v[2], v[3]);
+                        mxc = fmax3(mxc, v[4], v[5]);
+                        mxd = fmax3(mxd, v[6], v[7]);
+                    }
                 }
+                if (kScaled || part) tmem_wait_st();
                 mx = fmaxf(fmaxf(mxa, mxb), fmaxf(mxc, mxd));
                 if (!kScaled) mx *= scale_log2;
             }
@@ -441,22 +448,27 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
                 named_bar_sync(1 + quad, 64);  // O is whole again before either publishes its P
                 tc_fence_after();
             }
-            // P = exp2(x - m), bf16 pairs over the segment's own scores
+            // pass 2: P = exp2(x - m), bf16 pairs over the segment's own scores (the
+            // second 32 scores' P lies over the first 32's, read by then)
             if (live) {
                 const uint64_t s2 = splat2(kScaled ? 1.0f : scale_log2), c2 = splat2(m == -INFINITY ? 0.f : -m);
                 uint64_t acc2 = 0;
+                uint32_t sr[2][32];
+                tmem_ld32(tSr, sr[0]);
+                tmem_ld32(tSr + 32, sr[1]);
+                tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t pk[8];
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 16; ++e) {
                         float x0, x1;
-                        fma2(__uint_as_float(sr[16 * q + 2 * e]), __uint_as_float(sr[16 * q + 2 * e + 1]), s2, c2, x0, x1);
+                        fma2(__uint_as_float(sr[q][2 * e]), __uint_as_float(sr[q][2 * e + 1]), s2, c2, x0, x1);
                         const float p0 = ex2(x0), p1 = ex2(x1);
                         add2(acc2, p0, p1);
                         pk[e] = pack_bf16x2(p0, p1);
                     }
-                    tmem_st8(tSr + 8 * q, pk);
+                    tmem_st16(tSr + 16 * q, pk);
                 }
                 l += sum2(acc2);
             } else if (seg == 0 || chunk_full(c)) {
