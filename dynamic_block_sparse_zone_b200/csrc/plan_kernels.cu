@@ -428,10 +428,21 @@ __global__ void __launch_bounds__(1024) k_zone_decide(Geo g, const double *__res
 
 // ---------------------------------------------------------------------------
 // K3: block-contiguous, head-major copies of Q, K, V and the fp64 block means
-// of Q and K.  One CTA per (block, slice of kPPThreads x 8 channels); a thread
-// owns 8 channels of one head and walks the block's tokens.
+// of Q and K.  One CTA per (block, slice of kPPThreads x 2 channels); a thread
+// owns 2 channels of one head (a warp moves whole 128-byte lines) and walks the
+// block's tokens in order, kPPRows at a time so that their loads are in flight
+// together.  That walk is the latency of the whole kernel on small grids: with
+// 8 channels per thread and the loads of four rows behind one another's stores,
+// 16x32x32 tokens of 1024 channels took 166 us (now 55), 24x96x160 of 2048
+// 1690 us (now 1540, 0.91 of the copy bandwidth).
 // ---------------------------------------------------------------------------
 constexpr int kPPThreads = 128;
+constexpr int kPPRows = 16;  // blocks are multiples of 64 tokens
+__device__ __forceinline__ uint32_t ld_stream2(const __nv_bfloat16 *p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 struct BlockGeom {
     int off, B, t0, h0, w0, bT, bH, bW, eH, eW;  // edges bT x bH x bW; bH = 2^eH, bW = 2^eW
 };
@@ -465,7 +476,7 @@ __device__ __forceinline__ int block_token(const Geo &g, const BlockGeom &bg, in
 // kPerm: the blocks are runs of an existing permutation (Hilbert-order plans),
 // which is read instead of derived from the zone shapes and written.
 template <bool kPerm>
-__global__ void __launch_bounds__(kPPThreads, 5) k_permute_pool(const __nv_bfloat16 *__restrict__ Q,
+__global__ void __launch_bounds__(kPPThreads, 4) k_permute_pool(const __nv_bfloat16 *__restrict__ Q,
                                                       const __nv_bfloat16 *__restrict__ K,
                                                       const __nv_bfloat16 *__restrict__ V, Geo g,
                                                       const int *__restrict__ nb, const int *__restrict__ blk_off,
@@ -473,7 +484,7 @@ __global__ void __launch_bounds__(kPPThreads, 5) k_permute_pool(const __nv_bfloa
                                                       __nv_bfloat16 *__restrict__ Qp, __nv_bfloat16 *__restrict__ Kp,
                                                       __nv_bfloat16 *__restrict__ Vp, double *__restrict__ Qbar,
                                                       double *__restrict__ Kbar) {
-    const int nslice = (g.C / 8 + kPPThreads - 1) / kPPThreads;
+    const int nslice = (g.C / 2 + kPPThreads - 1) / kPPThreads;
     const int j = blockIdx.x / nslice, slice = blockIdx.x % nslice, b = blockIdx.y;
     if (j >= nb[b]) return;
     BlockGeom bg;
@@ -488,44 +499,40 @@ __global__ void __launch_bounds__(kPPThreads, 5) k_permute_pool(const __nv_bfloa
                 perm[(size_t)b * g.N + bg.off + r] = block_token(g, bg, r);
     }
     const int *pb = perm + (size_t)b * g.N + bg.off;
-    const int G = g.C / 8;
     const double inv = 1.0 / (double)bg.B;  // B is a power of two: exact
-    const int grp = slice * kPPThreads + threadIdx.x;
-    if (grp < G) {
-        const int hd = (grp * 8) / g.D, d0 = (grp * 8) % g.D;
+    const int c = 2 * (slice * kPPThreads + threadIdx.x);
+    if (c < g.C) {
+        const int hd = c / g.D, d0 = c % g.D;
         const size_t bh = (size_t)b * g.heads + hd;
-        double sq[8], sk[8];
+        double sq[2] = {0.0, 0.0}, sk[2] = {0.0, 0.0};
+        const size_t src0 = (size_t)b * g.N * g.C + c, dst0 = (bh * g.N + bg.off) * g.D + d0;
+#pragma unroll 1
+        for (int r0 = 0; r0 < bg.B; r0 += kPPRows) {
+            uint32_t q[kPPRows], k[kPPRows], v[kPPRows];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sq[k] = sk[k] = 0.0;
-        const __nv_bfloat16 *srcQ = Q + (size_t)b * g.N * g.C + grp * 8;
-        const __nv_bfloat16 *srcK = K + (size_t)b * g.N * g.C + grp * 8;
-        const __nv_bfloat16 *srcV = V + (size_t)b * g.N * g.C + grp * 8;
-        const size_t dst0 = (bh * g.N + bg.off) * g.D + d0;
-#pragma unroll 4
-        for (int r = 0; r < bg.B; ++r) {
-            const size_t tok = kPerm ? (size_t)pb[r] : (size_t)block_token(g, bg, r);
-            const uint4 q = ld_stream(srcQ + tok * g.C);
-            const uint4 k = ld_stream(srcK + tok * g.C);
-            const uint4 v = ld_stream(srcV + tok * g.C);
-            *reinterpret_cast<uint4 *>(Qp + dst0 + (size_t)r * g.D) = q;
-            *reinterpret_cast<uint4 *>(Kp + dst0 + (size_t)r * g.D) = k;
-            *reinterpret_cast<uint4 *>(Vp + dst0 + (size_t)r * g.D) = v;
-            float xq[8], xk[8];
-            bf16x8_to_float(q, xq);
-            bf16x8_to_float(k, xk);
+            for (int i = 0; i < kPPRows; ++i) {
+                const size_t tok = kPerm ? (size_t)pb[r0 + i] : (size_t)block_token(g, bg, r0 + i);
+                q[i] = ld_stream2(Q + src0 + tok * g.C);
+                k[i] = ld_stream2(K + src0 + tok * g.C);
+                v[i] = ld_stream2(V + src0 + tok * g.C);
+            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sq[e] = __dadd_rn(sq[e], (double)xq[e]);
-                sk[e] = __dadd_rn(sk[e], (double)xk[e]);
+            for (int i = 0; i < kPPRows; ++i) {
+                const size_t dst = dst0 + (size_t)(r0 + i) * g.D;
+                *reinterpret_cast<uint32_t *>(Qp + dst) = q[i];
+                *reinterpret_cast<uint32_t *>(Kp + dst) = k[i];
+                *reinterpret_cast<uint32_t *>(Vp + dst) = v[i];
+                sq[0] = __dadd_rn(sq[0], (double)__uint_as_float(q[i] << 16));
+                sq[1] = __dadd_rn(sq[1], (double)__uint_as_float(q[i] & 0xffff0000u));
+                sk[0] = __dadd_rn(sk[0], (double)__uint_as_float(k[i] << 16));
+                sk[1] = __dadd_rn(sk[1], (double)__uint_as_float(k[i] & 0xffff0000u));
             }
         }
-        double *oq = Qbar + (bh * g.nbmax + j) * g.D + d0;
-        double *ok = Kbar + (bh * g.nbmax + j) * g.D + d0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            oq[e] = sq[e] * inv;
-            ok[e] = sk[e] * inv;
-        }
+        double *oq = Qbar + (bh * g.nbmax + j) * g.D + d0, *ok = Kbar + (bh * g.nbmax + j) * g.D + d0;
+        oq[0] = sq[0] * inv;
+        oq[1] = sq[1] * inv;
+        ok[0] = sk[0] * inv;
+        ok[1] = sk[1] * inv;
     }
 }
 
@@ -1050,12 +1057,13 @@ static void launch_permute_pool(Plan &pl, const __nv_bfloat16 *Q, const __nv_bfl
                                 cudaStream_t st) {
     const Geo &g = pl.g;
     TimerScope ts(pl, kTPermutePool, st);
+    const dim3 grid((g.C / 2 + kPPThreads - 1) / kPPThreads * g.nbmax, g.batch);
     if (pl.p.hilbert_block)
-        k_permute_pool<true><<<dim3((g.C / 8 + kPPThreads - 1) / kPPThreads * g.nbmax, g.batch), kPPThreads, 0, st>>>(
-            Q, K, V, g, pl.nb, pl.blk_off, pl.zone_shape, pl.perm, pl.Qp, pl.Kp, pl.Vp, pl.Qbar, pl.Kbar);
+        k_permute_pool<true><<<grid, kPPThreads, 0, st>>>(Q, K, V, g, pl.nb, pl.blk_off, pl.zone_shape, pl.perm, pl.Qp,
+                                                          pl.Kp, pl.Vp, pl.Qbar, pl.Kbar);
     else
-        k_permute_pool<false><<<dim3((g.C / 8 + kPPThreads - 1) / kPPThreads * g.nbmax, g.batch), kPPThreads, 0, st>>>(
-            Q, K, V, g, pl.nb, pl.blk_off, pl.zone_shape, pl.perm, pl.Qp, pl.Kp, pl.Vp, pl.Qbar, pl.Kbar);
+        k_permute_pool<false><<<grid, kPPThreads, 0, st>>>(Q, K, V, g, pl.nb, pl.blk_off, pl.zone_shape, pl.perm, pl.Qp,
+                                                           pl.Kp, pl.Vp, pl.Qbar, pl.Kbar);
 }
 
 // The block-contiguous copies and pooled means, then scores, selection and
