@@ -32,7 +32,8 @@ EXPORTED = ("prism_plan_create", "prism_plan_bytes", "prism_plan_build", "prism_
             "prism_plan_build_finish", "prism_attn_fwd_taylor", "prism_plan_build_with_zones",
             "prism_ckpt_bytes", "prism_ckpt_pack", "prism_ckpt_unpack", "prism_layer_norm_fwd",
             "prism_layer_norm_bwd_workspace", "prism_layer_norm_bwd",
-            "prism_plan_set_score", "prism_attn_fwd_scored", "prism_attn_bwd_scored")
+            "prism_plan_set_score", "prism_attn_fwd_scored", "prism_attn_bwd_scored",
+            "prism_attn_ckpt_save", "prism_plan_update_qkv_ckpt", "prism_attn_bwd_ckpt")
 NUM_TIMERS = 12
 
 
@@ -71,6 +72,10 @@ class prism_rows(ctypes.Structure):
 
 class prism_ckpt(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int)]
+
+
+class prism_attn_ckpt(ctypes.Structure):
+    _fields_ = [(n, prism_ckpt) for n in ("Q", "K", "V", "O")] + [("lse", ctypes.c_void_p)]
 
 
 class prism_score(ctypes.Structure):
@@ -129,8 +134,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.prism_plan_set_score.argtypes = [V, ctypes.POINTER(prism_score), P]
     lib.prism_attn_fwd_scored.argtypes = [V, P, P, P]
     lib.prism_attn_bwd_scored.argtypes = [V, P, P, P, P, P, P]
-    for name in ("prism_ckpt_bytes", "prism_ckpt_pack", "prism_ckpt_unpack", "prism_layer_norm_fwd",
-                 "prism_layer_norm_bwd", "prism_plan_set_score", "prism_attn_fwd_scored", "prism_attn_bwd_scored"):
+    A = ctypes.POINTER(prism_attn_ckpt)
+    lib.prism_attn_ckpt_save.argtypes = [V, P, P, P, P, A, P]
+    lib.prism_plan_update_qkv_ckpt.argtypes = [V, A, P]
+    lib.prism_attn_bwd_ckpt.argtypes = [V, A, P, P, P, P, ctypes.c_int, P]
+    for name in ("prism_attn_ckpt_save", "prism_plan_update_qkv_ckpt", "prism_attn_bwd_ckpt",
+                 "prism_ckpt_bytes", "prism_ckpt_pack", "prism_ckpt_unpack", "prism_layer_norm_fwd",
+                 "prism_layer_norm_bwd", "prism_plan_set_score", "prism_attn_fwd_scored", "prism_attn_bwd_scored",
+            "prism_attn_ckpt_save", "prism_plan_update_qkv_ckpt", "prism_attn_bwd_ckpt"):
         getattr(lib, name).restype = ctypes.c_int
     lib.prism_plan_destroy.argtypes = [V]
     lib.prism_plan_destroy.restype = None
@@ -357,6 +368,38 @@ class PrismPlan:
         fn = load_library().prism_attn_bwd_scored if scored else load_library().prism_attn_bwd
         _check(fn(self._h, _ptr(O), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV), _stream()))
         return dQ, dK, dV
+
+    # -- 8-bit checkpoints between the passes ------------------------------------
+    def save(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor, lse: torch.Tensor,
+             fmt: str = "int8") -> "AttnCheckpoint":
+        """Q, K, V and O of a forward in 8 bits, with its lse (kept as it is): what bwd_ckpt takes."""
+        p = self.params
+        for t, n in ((Q, "Q"), (K, "K"), (V, "V"), (O, "O")):
+            _need(t, n, torch.bfloat16, self._qkv_shape())
+        _need(lse, "lse", torch.float32, (p.batch, p.heads, p.N))
+        kept = [_new_ckpt(t, p.batch * p.N, p.heads * p.head_dim, fmt) for t in (Q, K, V, O)]
+        out = AttnCheckpoint(*kept, lse)
+        c = out.to_c(p)
+        _check(load_library().prism_attn_ckpt_save(self._h, _ptr(Q), _ptr(K), _ptr(V), _ptr(O), ctypes.byref(c), _stream()))
+        return out
+
+    def update_qkv_ckpt(self, ckpt: "AttnCheckpoint"):
+        """update_qkv with the values that the checkpoint's 8-bit Q, K, V stand for."""
+        c = ckpt.to_c(self.params)
+        _check(load_library().prism_plan_update_qkv_ckpt(self._h, ctypes.byref(c), _stream()))
+        return self
+
+    def bwd_ckpt(self, ckpt: "AttnCheckpoint", dO: torch.Tensor, dQ=None, dK=None, dV=None, scored: bool = False):
+        """Gradients from a checkpoint of the forward (prism_attn_bwd_ckpt)."""
+        shp = self._qkv_shape()
+        _need(dO, "dO", torch.bfloat16, shp)
+        grads = [torch.empty(shp, dtype=torch.bfloat16, device="cuda") if t is None else t for t in (dQ, dK, dV)]
+        for t, n in zip(grads, ("dQ", "dK", "dV")):
+            _need(t, n, torch.bfloat16, shp)
+        c = ckpt.to_c(self.params)
+        _check(load_library().prism_attn_bwd_ckpt(self._h, ctypes.byref(c), _ptr(dO), *(_ptr(t) for t in grads),
+                                                  int(bool(scored)), _stream()))
+        return tuple(grads)
 
     # -- steps from host memory (pipelined across calls) ---------------------
     def step_host(self, Q, K, V, a_norm, O, lse=None, dO=None, dQ=None, dK=None, dV=None, taylor=False) -> int:
@@ -612,7 +655,7 @@ def _weights_dtype(x, *ws):
 @dataclass
 class Checkpoint:
     """Values kept in 8 bits: a code per value and a scale per 32 channels of a row.
-    shape and dtype are the tensor's it was made from."""
+    shape and dtype are the tensor's it was made from (its last axes make up a row)."""
     codes: torch.Tensor    # uint8 [rows, channels]
     scales: torch.Tensor   # uint8 [rows, ceil(channels / 32)]
     format: str            # "int8" or "e4m3"
@@ -633,9 +676,30 @@ class Checkpoint:
             _need(t, n, torch.uint8, sh)
         if self.format not in _FORMATS:
             raise ValueError(f"checkpoint format {self.format!r} is not one of {sorted(_FORMATS)}")
-        if C != self.shape[-1] or rows != math.prod(self.shape[:-1]) or self.scales.device != self.device:
+        if rows * C != math.prod(self.shape) or C % max(self.shape[-1], 1) or self.scales.device != self.device:
             raise ValueError("codes, scales and shape do not belong together")
         return prism_ckpt(self.codes.data_ptr(), self.scales.data_ptr(), _FORMATS[self.format])
+
+
+@dataclass
+class AttnCheckpoint:
+    """What an attention layer keeps in 8 bits between its passes (PrismPlan.save)."""
+    Q: Checkpoint
+    K: Checkpoint
+    V: Checkpoint
+    O: Checkpoint
+    lse: torch.Tensor
+
+    @property
+    def nbytes(self) -> int:
+        return sum(k.nbytes for k in (self.Q, self.K, self.V, self.O)) + self.lse.nbytes
+
+    def to_c(self, p: Params) -> prism_attn_ckpt:
+        parts = (self.Q, self.K, self.V, self.O)
+        if any(tuple(k.codes.shape) != (p.batch * p.N, p.heads * p.head_dim) for k in parts):
+            raise ValueError("the checkpoint belongs to a plan of other sizes")
+        _need(self.lse, "lse", torch.float32, (p.batch, p.heads, p.N))
+        return prism_attn_ckpt(*(k.to_c() for k in parts), self.lse.data_ptr())
 
 
 def _new_ckpt(x: torch.Tensor, rows: int, channels: int, fmt: str) -> Checkpoint:
@@ -663,7 +727,7 @@ def prism_ckpt_unpack(ckpt: Checkpoint, out: Optional[torch.Tensor] = None) -> t
         out = torch.empty(ckpt.shape, dtype=ckpt.dtype, device=ckpt.device)
     elif tuple(out.shape) != ckpt.shape:
         raise ValueError(f"out must have shape {ckpt.shape}")
-    r, n, C = _rows(out, "out", ckpt.device)
+    r, n, C = _rows(out if ckpt.codes.shape[1] == ckpt.shape[-1] else out.view(ckpt.codes.shape), "out", ckpt.device)
     with _on(ckpt.device):
         _check(load_library().prism_ckpt_unpack(ctypes.byref(c), ctypes.byref(r), _DTYPES[out.dtype], n, C, _stream()))
     return out
@@ -706,8 +770,8 @@ def prism_layer_norm_bwd(dy: torch.Tensor, x, gamma: Optional[torch.Tensor], mea
         if t.device != dy.device:
             raise ValueError(f"{name} must be on {dy.device}")
     if isinstance(x, Checkpoint):
-        if x.device != dy.device:
-            raise ValueError(f"the checkpoint must be on {dy.device}")
+        if x.device != dy.device or tuple(x.codes.shape) != (n, C):
+            raise ValueError(f"the checkpoint must hold {n} rows of {C} channels on {dy.device}")
         rx, c = None, ctypes.byref(x.to_c())
     else:
         rx, c = ctypes.byref(_rows(x, "x", dy.device, dy.dtype)[0]), None

@@ -1,11 +1,11 @@
 // attn_bwd_aux.cu -- the memory-bound steps around the tensor-core backward:
-//   k_attn_bwd_pre   Delta_q = rowsum(dO_q * O_q) from the forward's bf16 O and
+//   k_attn_bwd_pre   Delta_q = rowsum(dO_q * O_q) from the forward's bf16 O (or its 8-bit form) and
 //                    the block-contiguous, head-major copy of dO
 //   k_dq_finalize    fp32 dQ accumulator (block-contiguous) -> bf16 dQ in the
 //                    caller's raster layout
 // and the launcher of the whole backward [Prism guide, Method section 3; the
 // standard softmax-attention gradient through the selected block pairs].
-#include "prism_internal.cuh"
+#include "rows.cuh"
 
 namespace prism {
 
@@ -18,8 +18,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // backward, part 1: Delta = rowsum(dO * O) and the permuted copy of dO
 // ---------------------------------------------------------------------------
 // (doc, scored attention: a padding token's row counts as dO = 0, whatever it holds.)
-template <int D>
-__global__ void __launch_bounds__(256) k_attn_bwd_pre(Geo g, const __nv_bfloat16 *__restrict__ O,
+// kO8: O is a checkpoint's codes, with their scales and format.
+template <int D, bool kO8>
+__global__ void __launch_bounds__(256) k_attn_bwd_pre(Geo g, const void *__restrict__ Ov,
+                                                      const uint8_t *__restrict__ Os, int fmt,
                                                       const __nv_bfloat16 *__restrict__ dO,
                                                       const int *__restrict__ perm, const int *__restrict__ doc,
                                                       __nv_bfloat16 *__restrict__ dOp, float *__restrict__ delta) {
@@ -32,8 +34,19 @@ __global__ void __launch_bounds__(256) k_attn_bwd_pre(Geo g, const __nv_bfloat16
         const int n = blockIdx.x * kTile + nl;
         const int tok = perm[(size_t)b * g.N + n];
         const size_t src = ((size_t)b * g.N + tok) * g.C + grp * 8;
-        uint4 ov = *reinterpret_cast<const uint4 *>(O + src);
         uint4 dv = *reinterpret_cast<const uint4 *>(dO + src);
+        uint4 ov;
+        if constexpr (kO8) {
+            rows::Codes<8> c;
+            c.load(static_cast<const uint8_t *>(Ov) + src, 0, 8);
+            const uint32_t sb = Os[((size_t)b * g.N + tok) * (g.C / rows::kGroup) + grp / (rows::kGroup / 8)];
+            rows::f2 x[4];
+            c.decode<__nv_bfloat16>(sb, fmt, x);
+            ov.x = rows::narrow<__nv_bfloat16>(x[0]), ov.y = rows::narrow<__nv_bfloat16>(x[1]);
+            ov.z = rows::narrow<__nv_bfloat16>(x[2]), ov.w = rows::narrow<__nv_bfloat16>(x[3]);
+        } else {
+            ov = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(Ov) + src);
+        }
         if (doc && doc[(size_t)b * g.N + n] < 0) ov = dv = make_uint4(0, 0, 0, 0);
         const int hd = grp * 8 / D, d0 = grp * 8 % D;
         const size_t bh = (size_t)b * g.heads + hd;
@@ -78,17 +91,22 @@ __global__ void __launch_bounds__(256) k_dq_finalize(Geo g, const float *__restr
 // ---------------------------------------------------------------------------
 // launcher
 // ---------------------------------------------------------------------------
+// O: bf16, or (o8) its checkpoint
 template <int D>
-static prism_status bwd_impl(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV, bool scored,
-                             cudaStream_t st) {
+static prism_status bwd_impl(Plan &pl, const void *O, const prism_ckpt *o8, const void *dO, void *dQ, void *dK, void *dV,
+                             bool scored, cudaStream_t st) {
     const Geo &g = pl.g;
     PRISM_CUDA_OK(cudaMemsetAsync(pl.dQacc, 0, (size_t)g.batch * g.heads * g.N * D * sizeof(float), st));
     {
         TimerScope ts(pl, kTBwdPre, st);
-        k_attn_bwd_pre<D><<<dim3(g.nbmax, g.batch), 256, 0, st>>>(g, static_cast<const __nv_bfloat16 *>(O),
-                                                                 static_cast<const __nv_bfloat16 *>(dO), pl.perm,
-                                                                 scored && pl.score.has_doc ? pl.score.doc : nullptr,
-                                                                 pl.dOp, pl.delta);
+        const int *doc = scored && pl.score.has_doc ? pl.score.doc : nullptr;
+        const auto *dOb = static_cast<const __nv_bfloat16 *>(dO);
+        if (o8)
+            k_attn_bwd_pre<D, true><<<dim3(g.nbmax, g.batch), 256, 0, st>>>(
+                g, o8->codes, static_cast<const uint8_t *>(o8->scales), o8->format, dOb, pl.perm, doc, pl.dOp, pl.delta);
+        else
+            k_attn_bwd_pre<D, false>
+                <<<dim3(g.nbmax, g.batch), 256, 0, st>>>(g, O, nullptr, 0, dOb, pl.perm, doc, pl.dOp, pl.delta);
         PRISM_CUDA_OK(cudaGetLastError());
     }
     prism_status s = scored ? launch_attn_bwd_tc_scored(pl, dK, dV, st) : launch_attn_bwd_tc_main(pl, dK, dV, st);
@@ -100,16 +118,16 @@ static prism_status bwd_impl(Plan &pl, const void *O, const void *dO, void *dQ, 
     return PRISM_OK;
 }
 
-prism_status launch_attn_bwd(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
+prism_status launch_attn_bwd(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV, bool scored,
                              cudaStream_t st) {
-    return pl.g.D == 64 ? bwd_impl<64>(pl, O, dO, dQ, dK, dV, false, st)
-                        : bwd_impl<128>(pl, O, dO, dQ, dK, dV, false, st);
+    return pl.g.D == 64 ? bwd_impl<64>(pl, O, nullptr, dO, dQ, dK, dV, scored, st)
+                        : bwd_impl<128>(pl, O, nullptr, dO, dQ, dK, dV, scored, st);
 }
 
-prism_status launch_attn_bwd_scored(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
-                                    cudaStream_t st) {
-    return pl.g.D == 64 ? bwd_impl<64>(pl, O, dO, dQ, dK, dV, true, st)
-                        : bwd_impl<128>(pl, O, dO, dQ, dK, dV, true, st);
+prism_status launch_attn_bwd_o8(Plan &pl, const prism_ckpt &O, const void *dO, void *dQ, void *dK, void *dV, bool scored,
+                                cudaStream_t st) {
+    return pl.g.D == 64 ? bwd_impl<64>(pl, nullptr, &O, dO, dQ, dK, dV, scored, st)
+                        : bwd_impl<128>(pl, nullptr, &O, dO, dQ, dK, dV, scored, st);
 }
 
 }  // namespace prism

@@ -1,0 +1,120 @@
+// attn_ckpt.cu -- the attention's side of 8-bit checkpoints: Q, K and V from
+// codes straight into the plan's block-contiguous bf16 copies (a code times its
+// power of two is a bf16 value, so nothing is rounded again), and the forward's
+// log-sum-exp into the order in which the backward reads it.
+//
+// HBM-bound: 1 + 1/32 bytes read and 2 written per value.  A thread owns four
+// channels and walks a block's tokens, eight at a time, as the bf16 gather does;
+// the eight threads of a scale group share its scale byte's cache line.
+#include "rows.cuh"
+
+namespace prism {
+
+using namespace rows;
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRows = 8;
+
+struct Codes8 {
+    const uint8_t *codes, *scales;
+    int fmt;
+};
+
+__global__ void __launch_bounds__(kThreads, 4) k_permute_pool_ckpt(Codes8 Q, Codes8 K, Codes8 V, Geo g,
+                                                                   const int *__restrict__ nb,
+                                                                   const int *__restrict__ blk_off,
+                                                                   const int *__restrict__ perm,
+                                                                   __nv_bfloat16 *__restrict__ Qp,
+                                                                   __nv_bfloat16 *__restrict__ Kp,
+                                                                   __nv_bfloat16 *__restrict__ Vp,
+                                                                   double *__restrict__ Qbar, double *__restrict__ Kbar) {
+    const int nslice = (g.C / 4 + kThreads - 1) / kThreads;
+    const int j = blockIdx.x / nslice, slice = blockIdx.x % nslice, b = blockIdx.y;
+    if (j >= nb[b]) return;
+    const int *bo = blk_off + (size_t)b * (g.nbmax + 1);
+    const int off = bo[j], B = bo[j + 1] - off, ng = g.C / kGroup;
+    const int *pb = perm + (size_t)b * g.N + off;
+    const int c = 4 * (slice * kThreads + threadIdx.x);
+    if (c >= g.C) return;
+    const int hd = c / g.D, d0 = c % g.D;
+    const size_t bh = (size_t)b * g.heads + hd, dst0 = (bh * g.N + off) * g.D + d0;
+    double sq[4] = {0.0, 0.0, 0.0, 0.0}, sk[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 1
+    for (int r0 = 0; r0 < B; r0 += kRows) {
+        Codes<4> q[kRows], k[kRows], v[kRows];
+        uint32_t qs[kRows], ks[kRows], vs[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const size_t row = (size_t)b * g.N + pb[r0 + i], at = row * g.C + c, sat = row * ng + c / kGroup;
+            q[i].w[0] = __ldg(reinterpret_cast<const uint32_t *>(Q.codes + at));
+            k[i].w[0] = __ldg(reinterpret_cast<const uint32_t *>(K.codes + at));
+            v[i].w[0] = __ldg(reinterpret_cast<const uint32_t *>(V.codes + at));
+            qs[i] = __ldg(Q.scales + sat);
+            ks[i] = __ldg(K.scales + sat);
+            vs[i] = __ldg(V.scales + sat);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const size_t dst = dst0 + (size_t)(r0 + i) * g.D;
+            f2 x[2];
+            q[i].decode<__nv_bfloat16>(qs[i], Q.fmt, x);
+            *reinterpret_cast<uint2 *>(Qp + dst) = make_uint2(narrow<__nv_bfloat16>(x[0]), narrow<__nv_bfloat16>(x[1]));
+            sq[0] += (double)low(x[0]), sq[1] += (double)high(x[0]);
+            sq[2] += (double)low(x[1]), sq[3] += (double)high(x[1]);
+            k[i].decode<__nv_bfloat16>(ks[i], K.fmt, x);
+            *reinterpret_cast<uint2 *>(Kp + dst) = make_uint2(narrow<__nv_bfloat16>(x[0]), narrow<__nv_bfloat16>(x[1]));
+            sk[0] += (double)low(x[0]), sk[1] += (double)high(x[0]);
+            sk[2] += (double)low(x[1]), sk[3] += (double)high(x[1]);
+            v[i].decode<__nv_bfloat16>(vs[i], V.fmt, x);
+            *reinterpret_cast<uint2 *>(Vp + dst) = make_uint2(narrow<__nv_bfloat16>(x[0]), narrow<__nv_bfloat16>(x[1]));
+        }
+    }
+    const double inv = 1.0 / (double)B;
+    double *oq = Qbar + (bh * g.nbmax + j) * g.D + d0, *ok = Kbar + (bh * g.nbmax + j) * g.D + d0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        oq[e] = sq[e] * inv;
+        ok[e] = sk[e] * inv;
+    }
+}
+
+// nlse_p = -log2(e) lse in block-contiguous order; a row without a key keeps -inf (P = 0).
+__global__ void __launch_bounds__(256) k_restore_lse(Geo g, const int *__restrict__ perm, const float *__restrict__ lse,
+                                                     float *__restrict__ nlse_p) {
+    const int n = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y, b = bh / g.heads;
+    if (n >= g.N) return;
+    const float v = lse[(size_t)bh * g.N + perm[(size_t)b * g.N + n]];
+    nlse_p[(size_t)bh * g.N + n] = v == -INFINITY ? v : -v * 1.4426950408889634f;
+}
+
+Codes8 codes_of(const prism_ckpt &k) {
+    return Codes8{static_cast<const uint8_t *>(k.codes), static_cast<const uint8_t *>(k.scales), k.format};
+}
+
+}  // namespace
+
+prism_status launch_regather_ckpt(Plan &pl, const prism_attn_ckpt &c, cudaStream_t st) {
+    const Geo &g = pl.g;
+    {
+        TimerScope ts(pl, kTPermutePool, st);
+        k_permute_pool_ckpt<<<dim3((g.C / 4 + kThreads - 1) / kThreads * g.nbmax, g.batch), kThreads, 0, st>>>(
+            codes_of(c.Q), codes_of(c.K), codes_of(c.V), g, pl.nb, pl.blk_off, pl.perm, pl.Qp, pl.Kp, pl.Vp, pl.Qbar,
+            pl.Kbar);
+    }
+    PRISM_CUDA_OK(cudaGetLastError());
+    return pl.score.set && pl.score.has_doc ? launch_zero_padding(pl, st) : PRISM_OK;
+}
+
+prism_status launch_attn_bwd_ckpt(Plan &pl, const prism_attn_ckpt &c, const void *dO, void *dQ, void *dK, void *dV,
+                                  bool scored, cudaStream_t st) {
+    prism_status s = launch_regather_ckpt(pl, c, st);
+    if (s != PRISM_OK) return s;
+    const Geo &g = pl.g;
+    k_restore_lse<<<dim3((g.N + 255) / 256, g.batch * g.heads), 256, 0, st>>>(g, pl.perm, c.lse, pl.nlse_p);
+    PRISM_CUDA_OK(cudaGetLastError());
+    return launch_attn_bwd_o8(pl, c.O, dO, dQ, dK, dV, scored, st);
+}
+
+}  // namespace prism

@@ -51,8 +51,15 @@ __device__ __forceinline__ long long items(const CkptArgs &a, long long &per_row
     return a.lanes == 32 ? a.nrows * per_row : (a.nrows + rows_per_item - 1) / rows_per_item;
 }
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptArgs a) {
+// Tensors of one shape packed by one launch, one grid row each.
+template <int N>
+struct CkptBatch {
+    CkptArgs a[N];
+};
+
+template <typename T, int VEC, int N>
+__global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptBatch<N> batch) {
+    const CkptArgs &a = batch.a[N == 1 ? 0 : blockIdx.y];
     constexpr int VP = VEC / 2, kPer = kGroup / VEC;
     long long per_row;
     const long long n = items(a, per_row), ng = (a.C + kGroup - 1) / kGroup;
@@ -113,8 +120,9 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_unpack(CkptArgs a) {
     }
 }
 
-template <typename T, int VEC, bool kPack>
-prism_status run(CkptArgs a, bool dense, cudaStream_t st) {
+// How a's rows are laid over lanes, and the CTAs that takes.
+template <int VEC>
+int lay_out(CkptArgs &a, bool dense) {
     if (dense && a.C % kGroup == 0) {
         a.C *= a.nrows;
         a.nrows = 1;
@@ -125,8 +133,13 @@ prism_status run(CkptArgs a, bool dense, cudaStream_t st) {
     const long long per = (long long)kU * (32 / a.lanes);
     const long long n = a.lanes == 32 ? a.nrows * ((a.nvec + 32 * kU - 1) / (32 * kU)) : (a.nrows + per - 1) / per;
     const long long ctas = (n + kThreads / 32 - 1) / (kThreads / 32), most = 148 * 16;
-    const int grid = (int)(ctas < most ? ctas : most);
-    if constexpr (kPack) k_ckpt_pack<T, VEC><<<grid, kThreads, 0, st>>>(a);
+    return (int)(ctas < most ? ctas : most);
+}
+
+template <typename T, int VEC, bool kPack>
+prism_status run(CkptArgs a, bool dense, cudaStream_t st) {
+    const int grid = lay_out<VEC>(a, dense);
+    if constexpr (kPack) k_ckpt_pack<T, VEC, 1><<<grid, kThreads, 0, st>>>(CkptBatch<1>{{a}});
     else k_ckpt_unpack<T, VEC><<<grid, kThreads, 0, st>>>(a);
     PRISM_CUDA_OK(cudaGetLastError());
     return PRISM_OK;
@@ -153,6 +166,20 @@ prism_status run_any(const RowPtr &x, int dtype, long long nrows, int C, const p
 }
 
 }  // namespace
+
+prism_status launch_ckpt_pack4(const void *const (&x)[4], const prism_ckpt *const (&k)[4], long long nrows, int C,
+                               cudaStream_t st) {
+    CkptBatch<4> b;
+    int grid = 0;
+    for (int i = 0; i < 4; ++i) {
+        b.a[i] = CkptArgs{RowPtr{(char *)x[i], C * 2ll, 0, 0}, static_cast<uint8_t *>(k[i]->codes),
+                          static_cast<uint8_t *>(k[i]->scales), k[i]->format, nrows, 0, C, 0};
+        grid = lay_out<8>(b.a[i], true);
+    }
+    k_ckpt_pack<__nv_bfloat16, 8, 4><<<dim3(grid, 4), kThreads, 0, st>>>(b);
+    PRISM_CUDA_OK(cudaGetLastError());
+    return PRISM_OK;
+}
 
 prism_status launch_ckpt_pack(const RowPtr &x, int dtype, long long nrows, int C, const prism_ckpt &k, cudaStream_t st) {
     return run_any<true>(x, dtype, nrows, C, k, st);

@@ -155,7 +155,7 @@ prism_status host_step(Plan &pl, const prism_host_io &io, cudaStream_t user, uns
     if (bwd) {
         PRISM_CUDA_OK(cudaStreamWaitEvent(hp.comp, hp.dO_ready[s], 0));
         st = launch_attn_bwd(pl, hp.out[s][kO], hp.in[s][kdO], hp.out[s][kdQ], hp.out[s][kdK], hp.out[s][kdV],
-                             hp.comp);
+                             false, hp.comp);
         if (st != PRISM_OK) return st;
     }
     PRISM_CUDA_OK(cudaEventRecord(hp.comp_done[s], hp.comp));

@@ -11,7 +11,7 @@
 #include <utility>
 #include <vector>
 
-#include "prism_internal.cuh"
+#include "rows.cuh"
 
 namespace prism {
 
@@ -490,7 +490,7 @@ prism_status prism_attn_bwd_scored(prism_plan *plan, const void *O, const void *
         return fail(PRISM_ERR_STATE, "prism_attn_bwd_scored needs a prism_attn_fwd_scored as the last forward");
     const uintptr_t al = (uintptr_t)O | (uintptr_t)dO | (uintptr_t)dQ | (uintptr_t)dK | (uintptr_t)dV;
     if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
-    return launch_attn_bwd_scored(plan->pl, O, dO, dQ, dK, dV, static_cast<cudaStream_t>(stream));
+    return launch_attn_bwd(plan->pl, O, dO, dQ, dK, dV, true, static_cast<cudaStream_t>(stream));
 }
 
 prism_status prism_attn_fwd_taylor(prism_plan *plan, void *O, float *lse, void *stream) {
@@ -515,7 +515,61 @@ prism_status prism_attn_bwd(prism_plan *plan, const void *O, const void *dO, voi
         return fail(PRISM_ERR_STATE, "prism_attn_bwd needs a prism_attn_fwd after the last build or update");
     const uintptr_t al = (uintptr_t)O | (uintptr_t)dO | (uintptr_t)dQ | (uintptr_t)dK | (uintptr_t)dV;
     if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
-    return launch_attn_bwd(plan->pl, O, dO, dQ, dK, dV, static_cast<cudaStream_t>(stream));
+    return launch_attn_bwd(plan->pl, O, dO, dQ, dK, dV, false, static_cast<cudaStream_t>(stream));
+}
+
+// The parts of an attention checkpoint that a call reads or writes.
+static prism_status check_attn_ckpt(const Plan &pl, const prism_attn_ckpt &c, bool with_o) {
+    const prism_ckpt *parts[4] = {&c.Q, &c.K, &c.V, &c.O};
+    static const char *const names[4] = {"Q", "K", "V", "O"};
+    for (int i = 0; i < (with_o ? 4 : 3); ++i) {
+        if (!parts[i]->codes || !parts[i]->scales) return fail(PRISM_ERR_INVALID_ARG, "checkpoint of %s is NULL", names[i]);
+        if (((uintptr_t)parts[i]->codes | (uintptr_t)parts[i]->scales) & 15)
+            return fail(PRISM_ERR_INVALID_ARG, "checkpoint of %s must be 16-byte aligned", names[i]);
+        if (parts[i]->format != PRISM_CKPT_INT8 && parts[i]->format != PRISM_CKPT_E4M3)
+            return fail(PRISM_ERR_INVALID_ARG, "checkpoint of %s: format %d is not int8 or e4m3", names[i], parts[i]->format);
+    }
+    return device_guard(pl);
+}
+
+prism_status prism_attn_ckpt_save(prism_plan *plan, const void *Q, const void *K, const void *V, const void *O,
+                                  const prism_attn_ckpt *out, void *stream) {
+    g_last_error.clear();
+    if (!plan || !Q || !K || !V || !O || !out) return fail(PRISM_ERR_INVALID_ARG, "NULL argument to prism_attn_ckpt_save");
+    const uintptr_t al = (uintptr_t)Q | (uintptr_t)K | (uintptr_t)V | (uintptr_t)O;
+    if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+    prism_status s = check_attn_ckpt(plan->pl, *out, true);
+    if (s != PRISM_OK) return s;
+    const void *const x[4] = {Q, K, V, O};
+    const prism_ckpt *const k[4] = {&out->Q, &out->K, &out->V, &out->O};
+    return launch_ckpt_pack4(x, k, (long long)plan->pl.g.batch * plan->pl.g.N, plan->pl.g.C, static_cast<cudaStream_t>(stream));
+}
+
+prism_status prism_plan_update_qkv_ckpt(prism_plan *plan, const prism_attn_ckpt *ckpt, void *stream) {
+    g_last_error.clear();
+    if (!plan || !ckpt) return fail(PRISM_ERR_INVALID_ARG, "NULL argument to prism_plan_update_qkv_ckpt");
+    prism_status s = check_attn_ckpt(plan->pl, *ckpt, false);
+    if (s != PRISM_OK) return s;
+    if (!plan->pl.built) return fail(PRISM_ERR_STATE, "prism_plan_update_qkv_ckpt needs a built plan");
+    plan->pl.have_fwd = 0;
+    return launch_regather_ckpt(plan->pl, *ckpt, static_cast<cudaStream_t>(stream));
+}
+
+prism_status prism_attn_bwd_ckpt(prism_plan *plan, const prism_attn_ckpt *ckpt, const void *dO, void *dQ, void *dK,
+                                 void *dV, int scored, void *stream) {
+    g_last_error.clear();
+    if (!plan || !ckpt || !dO || !dQ || !dK || !dV)
+        return fail(PRISM_ERR_INVALID_ARG, "NULL argument to prism_attn_bwd_ckpt");
+    if (!ckpt->lse || ((uintptr_t)ckpt->lse & 3)) return fail(PRISM_ERR_INVALID_ARG, "the checkpoint's lse is NULL or misaligned");
+    const uintptr_t al = (uintptr_t)dO | (uintptr_t)dQ | (uintptr_t)dK | (uintptr_t)dV;
+    if (al & 15) return fail(PRISM_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+    prism_status s = check_attn_ckpt(plan->pl, *ckpt, true);
+    if (s != PRISM_OK) return s;
+    if (!plan->pl.built) return fail(PRISM_ERR_STATE, "prism_attn_bwd_ckpt needs a built plan");
+    if (scored && !plan->pl.score.set)
+        return fail(PRISM_ERR_STATE, "a scored prism_attn_bwd_ckpt needs a prism_plan_set_score after the last build");
+    plan->pl.have_fwd = 0;
+    return launch_attn_bwd_ckpt(plan->pl, *ckpt, dO, dQ, dK, dV, scored != 0, static_cast<cudaStream_t>(stream));
 }
 
 prism_status prism_audio_norms(const void *h, float *a, int batch, int T, int H, int W, int channels, void *stream) {

@@ -148,12 +148,16 @@ bool taylor_fits(const Geo &g);  // the Taylor forward's shared memory fits one 
 prism_status launch_regather(Plan &pl, const void *Q, const void *K, const void *V, cudaStream_t st);
 prism_status make_tensor_maps(Plan &pl);
 prism_status launch_attn_bwd_tc_main(Plan &pl, void *dK, void *dV, cudaStream_t st);
-prism_status launch_attn_bwd(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
+prism_status launch_attn_bwd(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV, bool scored,
                              cudaStream_t st);
+prism_status launch_attn_bwd_o8(Plan &pl, const prism_ckpt &O, const void *dO, void *dQ, void *dK, void *dV, bool scored,
+                                cudaStream_t st);
+// From a checkpoint of Q, K, V (and O, lse): attn_ckpt.cu.
+prism_status launch_regather_ckpt(Plan &pl, const prism_attn_ckpt &c, cudaStream_t st);
+prism_status launch_attn_bwd_ckpt(Plan &pl, const prism_attn_ckpt &c, const void *dO, void *dQ, void *dK, void *dV,
+                                  bool scored, cudaStream_t st);
 
 prism_status launch_attn_fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t st);
-prism_status launch_attn_bwd_scored(Plan &pl, const void *O, const void *dO, void *dQ, void *dK, void *dV,
-                                    cudaStream_t st);
 prism_status launch_attn_bwd_tc_scored(Plan &pl, void *dK, void *dV, cudaStream_t st);
 prism_status set_score(Plan &pl, const prism_score &s, cudaStream_t st);
 prism_status launch_zero_padding(Plan &pl, cudaStream_t st);  // padding tokens' rows of Qp, Kp, Vp

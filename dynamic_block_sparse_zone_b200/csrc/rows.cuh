@@ -345,6 +345,9 @@ prism_status launch_norm_bwd(const rows::NormBwd &a, int dtype, cudaStream_t st)
 size_t norm_bwd_workspace(long long nrows, int C);
 prism_status launch_ckpt_pack(const rows::RowPtr &x, int dtype, long long nrows, int C, const prism_ckpt &k,
                               cudaStream_t st);
+// four dense, 16-byte aligned bf16 tensors of whole scale groups
+prism_status launch_ckpt_pack4(const void *const (&x)[4], const prism_ckpt *const (&k)[4], long long nrows, int C,
+                               cudaStream_t st);
 prism_status launch_ckpt_unpack(const prism_ckpt &k, const rows::RowPtr &y, int dtype, long long nrows, int C,
                                 cudaStream_t st);
 

@@ -348,6 +348,35 @@ PRISM_API prism_status prism_ckpt_pack(const prism_rows *x, int dtype, long long
 PRISM_API prism_status prism_ckpt_unpack(const prism_ckpt *in, const prism_rows *y, int dtype, long long rows,
                                          int channels, void *stream);
 
+/* The attention's inputs and output kept in 8 bits between the passes (half the
+ * bytes of bf16, and no plan has to hold a layer's Q, K and V): checkpoints of
+ * Q, K, V and O as [batch * N][heads * head_dim] rows of the user layout, each
+ * in its own format, and the forward's lse (fp32 [batch][heads][N], the
+ * caller's, read when the backward runs).
+ *   prism_attn_ckpt_save: codes and scales of the four tensors (device, bf16,
+ *     16-byte aligned), one launch; out->lse is not touched.
+ *   prism_plan_update_qkv_ckpt: as prism_plan_update_qkv, with the values that
+ *     the codes of Q, K and V stand for (exact in bf16).  Reads Q, K, V only.
+ *   prism_attn_bwd_ckpt: brings Q, K and V into the plan in the same way, takes
+ *     P = exp(logit - lse) with the logits of the 8-bit Q and K and the saved
+ *     lse, Delta = rowsum(dO * O) with the 8-bit O, and otherwise computes
+ *     prism_attn_bwd (scored = 0) or prism_attn_bwd_scored (1, under the plan's
+ *     current scores).  P's rows then sum to 1 only up to the 8-bit error;
+ *     prism_plan_update_qkv_ckpt, a forward and prism_attn_bwd instead give the
+ *     exact gradient at the 8-bit point, for the price of the forward.
+ * The plan's selection has to be the forward's.  Afterwards the plan holds the
+ * checkpoint's Q, K, V, and a backward needs a new forward.  Errors:
+ * PRISM_ERR_STATE before a build, or scored without scores.                 */
+typedef struct prism_attn_ckpt {
+    prism_ckpt Q, K, V, O;
+    const float *lse;
+} prism_attn_ckpt;
+PRISM_API prism_status prism_attn_ckpt_save(prism_plan *plan, const void *Q, const void *K, const void *V, const void *O,
+                                            const prism_attn_ckpt *out, void *stream);
+PRISM_API prism_status prism_plan_update_qkv_ckpt(prism_plan *plan, const prism_attn_ckpt *ckpt, void *stream);
+PRISM_API prism_status prism_attn_bwd_ckpt(prism_plan *plan, const prism_attn_ckpt *ckpt, const void *dO, void *dQ,
+                                           void *dK, void *dV, int scored, void *stream);
+
 /* Layer norm over the channels of each row: y = (x - mean) rstd gamma + beta
  * with mean = sum x / C, rstd = (sum (x - mean)^2 / C + eps)^(-1/2).  x and y
  * have type dtype; gamma and beta [channels] have type weight_dtype (fp32, or
