@@ -51,7 +51,11 @@
 // stage, so it has eight warps (two threads per row, 64 keys each) instead of
 // four: with four, capped scores issued 0.32 instructions per cycle and
 // scheduler, held by latency.  P of the second 64 keys then lies over its own
-// scores, TMEM columns [64, 96).
+// scores, TMEM columns [64, 128).  P goes to the tensor cores as hi + lo, two
+// bf16 numbers and two products with V: an 8-bit O is kept for the backward, and
+// a P of 8 bits moves O by about half a step of bf16, enough for every tenth
+// 8-bit code to fall on the other side and Delta with it (dQ off by up to
+// 0.012 in relative norm, 0.003 so).
 #include <cuda.h>
 
 #include "tc_common.cuh"
@@ -293,9 +297,11 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
                 // k-step kk (16 keys): P columns 8 kk, V rows 2048 B (128 descriptor units) further
                 const uint64_t bV = sdesc(sbase + L::kV, L::kTileBytes, 1024);
                 mma_ts4<8, 16, 24, 128, 256, 384>(tO, tS, bV, idPV, c > 0);
+                if (kEnc) mma_ts4<8, 16, 24, 128, 256, 384>(tO, tS + 32, bV, idPV, 1u);  // P's low part
                 if (!__all_sync(0xffffffffu, mbar_wait(bar_p2, c & 1, status, kSiteP, abort_flag))) break;
                 tc_fence_after();
                 if (full) mma_ts4<8, 16, 24, 128, 256, 384>(tO, tS + (kEnc ? 64 : 32), bV + 512, idPV, 1u);
+                if (kEnc && full) mma_ts4<8, 16, 24, 128, 256, 384>(tO, tS + 96, bV + 512, idPV, 1u);
                 mma_commit(bar_ve);
                 mma_commit(bar_o);
             }
@@ -448,8 +454,9 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
                 named_bar_sync(1 + quad, 64);  // O is whole again before either publishes its P
                 tc_fence_after();
             }
-            // pass 2: P = exp2(x - m), bf16 pairs over the segment's own scores (the
-            // second 32 scores' P lies over the first 32's, read by then)
+            // pass 2: P = exp2(x - m) as two bf16 numbers, over the segment's own scores
+            // (all of them are in registers by then): hi, P's upper 16 bits, in
+            // columns [0, 32), and lo, the rest, in [32, 64)
             if (live) {
                 const uint64_t s2 = splat2(kScaled ? 1.0f : scale_log2), c2 = splat2(m == -INFINITY ? 0.f : -m);
                 uint64_t acc2 = 0;
@@ -459,24 +466,28 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
                 tmem_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    uint32_t pk[16];
+                    uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float x0, x1;
                         fma2(__uint_as_float(sr[q][2 * e]), __uint_as_float(sr[q][2 * e + 1]), s2, c2, x0, x1);
                         const float p0 = ex2(x0), p1 = ex2(x1);
                         add2(acc2, p0, p1);
-                        pk[e] = pack_bf16x2(p0, p1);
+                        const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+                        hi[e] = __byte_perm(u0, u1, 0x7632);
+                        const uint64_t d = psub(pair2(p0, p1), (uint64_t)(u0 & 0xffff0000u) | (uint64_t)(u1 & 0xffff0000u) << 32);
+                        lo[e] = pack_bf16x2(plo(d), phi(d));
                     }
-                    tmem_st16(tSr + 16 * q, pk);
+                    tmem_st16(tSr + 16 * q, hi);
+                    tmem_st16(tSr + 32 + 16 * q, lo);
                 }
                 l += sum2(acc2);
             } else if (seg == 0 || chunk_full(c)) {
-                uint32_t z[16];
+                uint32_t z[32];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) z[e] = 0u;
-                tmem_st16(tSr, z);
-                tmem_st16(tSr + 16, z);
+                for (int e = 0; e < 32; ++e) z[e] = 0u;
+                tmem_st32(tSr, z);
+                tmem_st32(tSr + 32, z);
             }
             tmem_wait_st();
             tc_fence_before();
