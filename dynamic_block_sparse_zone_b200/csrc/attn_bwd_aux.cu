@@ -18,12 +18,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // backward, part 1: Delta = rowsum(dO * O) and the permuted copy of dO
 // ---------------------------------------------------------------------------
 // (doc, scored attention: a padding token's row counts as dO = 0, whatever it holds.)
-// kO8: O is a checkpoint's codes, with their scales and format.
+// kO8: O is a checkpoint's codes, with their scales and format.  Olo, if not
+// NULL (scored attention), is what the bf16 O leaves of the forward's fp32 O: in
+// rows with few visible keys dP and Delta nearly cancel, and O's rounding would
+// be the largest error of dS.
 template <int D, bool kO8>
 __global__ void __launch_bounds__(256) k_attn_bwd_pre(Geo g, const void *__restrict__ Ov,
                                                       const uint8_t *__restrict__ Os, int fmt,
                                                       const __nv_bfloat16 *__restrict__ dO,
                                                       const int *__restrict__ perm, const int *__restrict__ doc,
+                                                      const __nv_bfloat16 *__restrict__ Olo,
                                                       __nv_bfloat16 *__restrict__ dOp, float *__restrict__ delta) {
     constexpr int L = D / 8;  // lanes per (token, head)
     const int b = blockIdx.y;
@@ -57,6 +61,15 @@ __global__ void __launch_bounds__(256) k_attn_bwd_pre(Geo g, const void *__restr
         for (int k = 0; k < 4; ++k) {
             acc += __uint_as_float(ow[k] << 16) * __uint_as_float(dw[k] << 16);
             acc += __uint_as_float(ow[k] & 0xffff0000u) * __uint_as_float(dw[k] & 0xffff0000u);
+        }
+        if (Olo) {
+            const uint4 lv = *reinterpret_cast<const uint4 *>(Olo + (bh * g.N + n) * D + d0);
+            const uint32_t lw[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc += __uint_as_float(lw[k] << 16) * __uint_as_float(dw[k] << 16);
+                acc += __uint_as_float(lw[k] & 0xffff0000u) * __uint_as_float(dw[k] & 0xffff0000u);
+            }
         }
 #pragma unroll
         for (int o2 = L / 2; o2 > 0; o2 >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o2, L);
@@ -103,10 +116,12 @@ static prism_status bwd_impl(Plan &pl, const void *O, const prism_ckpt *o8, cons
         const auto *dOb = static_cast<const __nv_bfloat16 *>(dO);
         if (o8)
             k_attn_bwd_pre<D, true><<<dim3(g.nbmax, g.batch), 256, 0, st>>>(
-                g, o8->codes, static_cast<const uint8_t *>(o8->scales), o8->format, dOb, pl.perm, doc, pl.dOp, pl.delta);
+                g, o8->codes, static_cast<const uint8_t *>(o8->scales), o8->format, dOb, pl.perm, doc, nullptr, pl.dOp,
+                pl.delta);
         else
             k_attn_bwd_pre<D, false>
-                <<<dim3(g.nbmax, g.batch), 256, 0, st>>>(g, O, nullptr, 0, dOb, pl.perm, doc, pl.dOp, pl.delta);
+                <<<dim3(g.nbmax, g.batch), 256, 0, st>>>(g, O, nullptr, 0, dOb, pl.perm, doc,
+                                                         scored ? pl.score.Olo : nullptr, pl.dOp, pl.delta);
         PRISM_CUDA_OK(cudaGetLastError());
     }
     prism_status s = scored ? launch_attn_bwd_tc_scored(pl, dK, dV, st) : launch_attn_bwd_tc_main(pl, dK, dV, st);

@@ -514,17 +514,23 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
                 uint32_t orr[32];
                 tmem_ld32(tO + lane_off + seg * (D / 2) + q * 32, orr);
                 tmem_wait_ld();
-                uint4 pkt[4];
-                uint32_t *pw = reinterpret_cast<uint32_t *>(pkt);
+                uint4 pkt[4], low[4];
+                uint32_t *pw = reinterpret_cast<uint32_t *>(pkt), *lw = reinterpret_cast<uint32_t *>(low);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    pw[e] = pack_bf16x2(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
-                    if (empty) pw[e] = 0u;
+                    const float o0 = empty ? 0.f : __uint_as_float(orr[2 * e]) * inv;
+                    const float o1 = empty ? 0.f : __uint_as_float(orr[2 * e + 1]) * inv;
+                    pw[e] = pack_bf16x2(o0, o1);
+                    lw[e] = pack_bf16x2(o0 - __uint_as_float(pw[e] << 16), o1 - __uint_as_float(pw[e] & 0xffff0000u));
                 }
                 if (write) {
                     uint4 *d4 = reinterpret_cast<uint4 *>(dst + q * 32);
+                    uint4 *l4 = reinterpret_cast<uint4 *>(sc.Olo + ((size_t)bh * g.N + n) * D + seg * (D / 2) + q * 32);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d4[e] = pkt[e];
+                    for (int e = 0; e < 4; ++e) {
+                        d4[e] = pkt[e];
+                        l4[e] = low[e];
+                    }
                 }
             }
             if (write && seg == 0) {

@@ -55,6 +55,7 @@ struct Score {
     float *vis;             // [batch][N] a key is visible to queries at positions >= this (+inf: padding)
     int *doc;               // [batch][N] document, -1: padding
     BlockRange *blk;        // [batch][nbmax]
+    __nv_bfloat16 *Olo;     // [batch*heads][N][D] what the last scored forward's bf16 O leaves of its fp32 O
     int *row_end, *col;     // the CSR again, rows starting at row_ptr: 2 j + (partly visible), see list_block
     int *colT_end, *rowT;   // and its transpose, columns starting at colT_ptr
 };
@@ -169,6 +170,7 @@ struct ScoreArgs {
     const float *pos, *vis;
     const int *doc;
     const float *slopes;
+    __nv_bfloat16 *Olo;         // written by the forward
     float cap_u;                // 1 / (sqrt(D) cap)
     float cap_one;              // sqrt(D) cap: unscaled scores up to here have |u| <= 1
     float cap_in;               // 2 log2(e) / (sqrt(D) cap)

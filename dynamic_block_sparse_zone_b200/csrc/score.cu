@@ -138,6 +138,7 @@ int buffers(Plan &pl, Buf *out) {
     out[n++] = {(void **)&s.blk, (size_t)g.batch * g.nbmax * sizeof(BlockRange)};
     out[n++] = {(void **)&s.row_end, lists * sizeof(int)};
     out[n++] = {(void **)&s.colT_end, lists * sizeof(int)};
+    out[n++] = {(void **)&s.Olo, (size_t)g.heads * tokens * g.D * 2};
     out[n++] = {(void **)&s.col, nnz * sizeof(int)};
     out[n++] = {(void **)&s.rowT, nnz * sizeof(int)};
     return n;
@@ -216,6 +217,7 @@ ScoreArgs score_args(const Plan &pl, bool backward) {
     a.vis = s.vis;
     a.doc = s.doc;
     a.slopes = s.slopes;
+    a.Olo = s.Olo;
     if (s.cap > 0.f) {
         a.cap_one = (float)(sqrt((double)pl.g.D) * (double)s.cap);
         a.cap_u = (float)(1.0 / (sqrt((double)pl.g.D) * (double)s.cap));

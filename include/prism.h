@@ -263,7 +263,7 @@ PRISM_API prism_status prism_attn_bwd(prism_plan *plan, const void *O, const voi
  * copies of Q, K and V (as do later prism_plan_update_qkv calls), so that what
  * padding holds reaches nothing; values of visible tokens must be finite.  It
  * belongs to the plan's current build: every build drops it.  The first call on
- * a plan allocates (about 8 bytes per selectable block pair and 12 per token;
+ * a plan allocates (about 8 bytes per selectable block pair, 12 per token and 2 per value of O;
  * PRISM_ERR_STATE while `stream` is being captured); it forgets the last
  * forward.  PRISM_ERR_STATE before a build.                                 */
 typedef struct prism_score {
@@ -282,7 +282,8 @@ PRISM_API prism_status prism_plan_set_score(prism_plan *plan, const prism_score 
 PRISM_API prism_status prism_attn_fwd_scored(prism_plan *plan, void *O, float *lse, void *stream);
 
 /* Its gradient with respect to Q, K and V: as prism_attn_bwd, with the factor
- * 1 - tanh^2(s / cap) on dS.  Tokens that see or are seen by nothing get zero
+ * 1 - tanh^2(s / cap) on dS and with Delta from O before its rounding (the plan
+ * keeps the difference: O has to be the last scored forward's).  Tokens that see or are seen by nothing get zero
  * gradients, whatever O and dO hold for padding.  PRISM_ERR_STATE unless the
  * plan's last forward was prism_attn_fwd_scored.                            */
 PRISM_API prism_status prism_attn_bwd_scored(prism_plan *plan, const void *O, const void *dO, void *dQ, void *dK,
