@@ -165,7 +165,10 @@ def _check(status: int):
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the current device's current stream without the lookups of torch.cuda.current_stream (about 10 us)
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -603,9 +606,12 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _FORMATS = {"int8": 0, "e4m3": 1}
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on(device):
     """Makes `device` current for the calls that launch on the current device."""
-    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+    return _HERE_ALREADY if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _rows(t: torch.Tensor, name: str, device=None, dtype=None):
@@ -615,20 +621,23 @@ def _rows(t: torch.Tensor, name: str, device=None, dtype=None):
         raise ValueError(f"{name} must be a bf16, fp16 or fp32 CUDA tensor with a channel axis")
     if (device is not None and t.device != device) or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
-    C = t.shape[-1]
+    shape = t.shape
+    C = shape[-1]
+    if C > 0 and t.is_contiguous():
+        return prism_rows(t.data_ptr(), C, 0, 0), t.numel() // C, C
     if C < 1 or (C > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name}: channels must be consecutive elements of the last axis")
     levels = []  # innermost first: [count, stride]
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
             continue
         if levels and st == levels[-1][0] * levels[-1][1]:
             levels[-1][0] *= n
         else:
             levels.append([n, st])
-    count = math.prod(t.shape[:-1])
+    count = math.prod(shape[:-1])
     if count and (len(levels) > 2 or any(st < C for _, st in levels)):
-        raise ValueError(f"{name}: rows of shape {tuple(t.shape)} with strides {t.stride()} are not evenly spaced")
+        raise ValueError(f"{name}: rows of shape {tuple(shape)} with strides {t.stride()} are not evenly spaced")
     if not count or not levels:
         return prism_rows(t.data_ptr(), C, 0, 0), count, C
     if len(levels) == 1:
@@ -636,20 +645,23 @@ def _rows(t: torch.Tensor, name: str, device=None, dtype=None):
     return prism_rows(t.data_ptr(), levels[0][1], levels[1][1], levels[0][0]), count, C
 
 
-def _weight(t, name, x, channels):
-    if t is None:
-        return None
-    if (not t.is_cuda or t.device != x.device or t.dtype not in (x.dtype, torch.float32)
-            or tuple(t.shape) != (channels,) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous [{channels}] tensor on {x.device}, fp32 or {x.dtype}")
-    return t
+def _weights(x, channels, **weights):
+    """Checks gamma and beta against x; their common dtype (fp32 without any)."""
+    kind = None
+    for name, t in weights.items():
+        if t is None:
+            continue
+        if (not t.is_cuda or t.dtype not in (x.dtype, torch.float32) or t.device != x.device
+                or t.shape != (channels,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous [{channels}] tensor on {x.device}, fp32 or {x.dtype}")
+        if kind is not None and t.dtype != kind:
+            raise ValueError("the weights must have one dtype")
+        kind = t.dtype
+    return kind or torch.float32
 
 
-def _weights_dtype(x, *ws):
-    kinds = {w.dtype for w in ws if w is not None}
-    if len(kinds) > 1:
-        raise ValueError("the weights must have one dtype")
-    return kinds.pop() if kinds else torch.float32
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 @dataclass
@@ -703,11 +715,14 @@ class AttnCheckpoint:
 
 
 def _new_ckpt(x: torch.Tensor, rows: int, channels: int, fmt: str) -> Checkpoint:
-    if fmt not in _FORMATS:
+    code = _FORMATS.get(fmt)
+    if code is None:
         raise ValueError(f"checkpoint format {fmt!r} is not one of {sorted(_FORMATS)}")
-    return Checkpoint(torch.empty((rows, channels), dtype=torch.uint8, device=x.device),
-                      torch.empty((rows, (channels + 31) // 32), dtype=torch.uint8, device=x.device),
-                      fmt, tuple(x.shape), x.dtype)
+    codes = torch.empty((rows, channels), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((rows, (channels + 31) // 32), dtype=torch.uint8, device=x.device)
+    out = Checkpoint(codes, scales, fmt, tuple(x.shape), x.dtype)
+    out._c = prism_ckpt(codes.data_ptr(), scales.data_ptr(), code)
+    return out
 
 
 def prism_ckpt_pack(x: torch.Tensor, fmt: str = "int8") -> Checkpoint:
@@ -715,8 +730,7 @@ def prism_ckpt_pack(x: torch.Tensor, fmt: str = "int8") -> Checkpoint:
     r, n, C = _rows(x, "x")
     out = _new_ckpt(x, n, C, fmt)
     with _on(x.device):
-        _check(load_library().prism_ckpt_pack(ctypes.byref(r), _DTYPES[x.dtype], n, C, ctypes.byref(out.to_c()),
-                                              _stream()))
+        _check(load_library().prism_ckpt_pack(r, _DTYPES[x.dtype], n, C, out._c, _stream()))
     return out
 
 
@@ -729,7 +743,7 @@ def prism_ckpt_unpack(ckpt: Checkpoint, out: Optional[torch.Tensor] = None) -> t
         raise ValueError(f"out must have shape {ckpt.shape}")
     r, n, C = _rows(out if ckpt.codes.shape[1] == ckpt.shape[-1] else out.view(ckpt.codes.shape), "out", ckpt.device)
     with _on(ckpt.device):
-        _check(load_library().prism_ckpt_unpack(ctypes.byref(c), ctypes.byref(r), _DTYPES[out.dtype], n, C, _stream()))
+        _check(load_library().prism_ckpt_unpack(c, r, _DTYPES[out.dtype], n, C, _stream()))
     return out
 
 
@@ -739,20 +753,20 @@ def prism_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, 
     shape.  With ckpt = "int8" or "e4m3" also x in 8 bits, written in the same pass:
     (y, mean, rstd, Checkpoint) -- what prism_layer_norm_bwd can take in x's place."""
     rx, n, C = _rows(x, "x")
-    gamma, beta = _weight(gamma, "gamma", x, C), _weight(beta, "beta", x, C)
+    wdt = _weights(x, C, gamma=gamma, beta=beta)
+    dev, shape = x.device, x.shape
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif tuple(y.shape) != tuple(x.shape):
+        y = torch.empty(shape, dtype=x.dtype, device=dev)
+    elif y.shape != shape:
         raise ValueError("y must have x's shape")
-    ry, _, _ = _rows(y, "y", x.device, x.dtype)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    ry, _, _ = _rows(y, "y", dev, x.dtype)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
     kept = _new_ckpt(x, n, C, ckpt) if ckpt is not None else None
-    c = ctypes.byref(kept.to_c()) if kept is not None else None
-    with _on(x.device):
+    with _on(dev):
         _check(load_library().prism_layer_norm_fwd(
-            ctypes.byref(rx), _ptr(gamma), _ptr(beta), ctypes.byref(ry), _ptr(mean), _ptr(rstd), c, n, C, float(eps),
-            _DTYPES[x.dtype], _DTYPES[_weights_dtype(x, gamma, beta)], _stream()))
+            rx, _addr(gamma), _addr(beta), ry, mean.data_ptr(), rstd.data_ptr(), kept and kept._c, n, C, eps,
+            _DTYPES[x.dtype], _DTYPES[wdt], _stream()))
     return (y, mean, rstd) if kept is None else (y, mean, rstd, kept)
 
 
@@ -762,37 +776,37 @@ def prism_layer_norm_bwd(dy: torch.Tensor, x, gamma: Optional[torch.Tensor], mea
     Checkpoint.  dgamma and dbeta have gamma's dtype (fp32 without a gamma); with
     weight_grads = False only dx is computed, and they are None."""
     rdy, n, C = _rows(dy, "dy")
-    gamma = _weight(gamma, "gamma", dy, C)
-    if tuple(x.shape) != tuple(dy.shape):
-        raise ValueError(f"x {tuple(x.shape)} must have dy's shape {tuple(dy.shape)}")
+    wdt = _weights(dy, C, gamma=gamma)
+    dev, shape = dy.device, dy.shape
+    if tuple(x.shape) != shape:
+        raise ValueError(f"x {tuple(x.shape)} must have dy's shape {tuple(shape)}")
     for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _need(t, name, torch.float32, dy.shape[:-1])
-        if t.device != dy.device:
-            raise ValueError(f"{name} must be on {dy.device}")
+        if not t.is_cuda or t.dtype != torch.float32 or t.shape != shape[:-1] or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {tuple(shape[:-1])} on {dev}")
+    rx = c = None
     if isinstance(x, Checkpoint):
-        if x.device != dy.device or tuple(x.codes.shape) != (n, C):
-            raise ValueError(f"the checkpoint must hold {n} rows of {C} channels on {dy.device}")
-        rx, c = None, ctypes.byref(x.to_c())
+        if x.device != dev or tuple(x.codes.shape) != (n, C):
+            raise ValueError(f"the checkpoint must hold {n} rows of {C} channels on {dev}")
+        c = x.to_c()
     else:
-        rx, c = ctypes.byref(_rows(x, "x", dy.device, dy.dtype)[0]), None
+        rx = _rows(x, "x", dev, dy.dtype)[0]
     if dx is None:
-        dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-    elif tuple(dx.shape) != tuple(dy.shape):
+        dx = torch.empty(shape, dtype=dy.dtype, device=dev)
+    elif dx.shape != shape:
         raise ValueError("dx must have dy's shape")
-    rdx, _, _ = _rows(dx, "dx", dy.device, dy.dtype)
-    wdt = _weights_dtype(dy, gamma)
+    rdx, _, _ = _rows(dx, "dx", dev, dy.dtype)
     lib = load_library()
     dgamma = dbeta = work = None
     nbytes = 0
     if weight_grads:
-        dgamma = torch.empty(C, dtype=wdt, device=dy.device)
-        dbeta = torch.empty(C, dtype=wdt, device=dy.device)
+        dgamma = torch.empty(C, dtype=wdt, device=dev)
+        dbeta = torch.empty_like(dgamma)
         nbytes = lib.prism_layer_norm_bwd_workspace(n, C)
-        work = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
-    with _on(dy.device):
-        _check(lib.prism_layer_norm_bwd(rx, c, ctypes.byref(rdy), _ptr(gamma), _ptr(mean), _ptr(rstd),
-                                        ctypes.byref(rdx), _ptr(dgamma), _ptr(dbeta), _ptr(work), nbytes, n, C,
-                                        _DTYPES[dy.dtype], _DTYPES[wdt], _stream()))
+        work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with _on(dev):
+        _check(lib.prism_layer_norm_bwd(rx, c, rdy, _addr(gamma), mean.data_ptr(), rstd.data_ptr(), rdx, _addr(dgamma),
+                                        _addr(dbeta), _addr(work), nbytes, n, C, _DTYPES[dy.dtype], _DTYPES[wdt],
+                                        _stream()))
     return dx, dgamma, dbeta
 
 
