@@ -119,8 +119,15 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
 
-    const int tile = blockIdx.x, bh = blockIdx.y, b = bh / g.heads, h = bh % g.heads;
-    if (tile >= nqt[b]) return;
+    int tile = blockIdx.x, bh = blockIdx.y;
+    if constexpr (kEnc) {  // long tiles first
+        const int t = sc.order[blockIdx.y * gridDim.x + blockIdx.x];
+        if (t < 0) return;
+        bh = t / g.nbmax;
+        tile = t - bh * g.nbmax;
+    }
+    const int b = bh / g.heads, h = bh % g.heads;
+    if (!kEnc && tile >= nqt[b]) return;
     if (*reinterpret_cast<volatile int *>(status) != 0) return;  // an earlier CTA timed out: fail fast
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int *bo = blk_off + (size_t)b * (g.nbmax + 1);

@@ -58,6 +58,9 @@ struct Score {
     __nv_bfloat16 *Olo;     // [batch*heads][N][D] what the last scored forward's bf16 O leaves of its fp32 O
     int *row_end, *col;     // the CSR again, rows starting at row_ptr: 2 j + (partly visible), see list_block
     int *colT_end, *rowT;   // and its transpose, columns starting at colT_ptr
+    int *order;             // [2][batch*heads*nbmax] sample*head * nbmax + tile in launch order, the forward's query
+                            // tiles and the backward's key tiles; -1: none
+    int *work;              // [2][batch*heads*nbmax] 64-row segments of each tile
 };
 
 // Everything a plan owns (device pointers unless noted).
@@ -167,6 +170,7 @@ void release_score(Plan &pl);
 // What the scored attention kernels read besides the plan.
 struct ScoreArgs {
     const int *list_end;        // row_end (forward) or colT_end (backward)
+    const int *order;           // tile of each CTA
     const float *pos, *vis;
     const int *doc;
     const float *slopes;

@@ -8,7 +8,7 @@
 // decision reads only each block's ranges, so it can call a pair partly visible
 // that is hidden or whole; the attention kernels then find out token by token.
 // Hidden pairs, most of a selection over packed clips, cost nothing after this.
-#include "prism_internal.cuh"
+#include "tc_common.cuh"
 
 namespace prism {
 
@@ -106,6 +106,72 @@ __global__ void __launch_bounds__(kThreads) k_score_filter(Geo g, const int *__r
     }
 }
 
+// Segments that each tile streams (one warp per tile; y: forward, backward).
+__global__ void __launch_bounds__(kThreads) k_score_work(Geo g, const int *__restrict__ nqt, const int *__restrict__ qt_blk,
+                                                         const int *__restrict__ blk_off, const int *__restrict__ row_ptr,
+                                                         const int *__restrict__ row_end, const int *__restrict__ col,
+                                                         const int *__restrict__ colT_ptr, const int *__restrict__ colT_end,
+                                                         const int *__restrict__ rowT, int *__restrict__ work) {
+    const size_t tiles = (size_t)g.batch * g.heads * g.nbmax;
+    const size_t t = (size_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (t >= tiles) return;
+    const int lane = threadIdx.x & 31, tile = (int)(t % g.nbmax), b = (int)(t / g.nbmax / g.heads);
+    int n = -1;
+    if (tile < nqt[b]) {
+        const bool back = blockIdx.y;
+        const int *ptr = back ? colT_ptr : row_ptr, *end = back ? colT_end : row_end, *list = back ? rowT : col;
+        int j1, j2;
+        tc::tile_blocks(qt_blk[(size_t)b * g.nbmax + tile], j1, j2);
+        const size_t l = t - tile + j1;
+        const int a0 = ptr[l], a1 = end[l], b0 = j2 >= 0 ? ptr[l + 1] : 0, b1 = j2 >= 0 ? end[l + 1] : 0;
+        n = tc::union_segments<true>(list + a0, a1 - a0, list + b0, b1 - b0, blk_off + (size_t)b * (g.nbmax + 1), lane);
+    }
+    if (lane == 0) work[blockIdx.y * tiles + t] = n;
+}
+
+// Launch order: the tiles with the most segments first, over groups of `heads`
+// sample-heads (one CTA per group and direction).  Masks leave tiles of very
+// different lengths; started last, a long one runs alone at the end.  Tiles of
+// equal length come in no fixed order: no result depends on it but the order in
+// which dQ's partial sums arrive.
+constexpr int kBins = 1024;
+__global__ void __launch_bounds__(kBins) k_score_order(Geo g, int heads_f, int heads_b, const int *__restrict__ work,
+                                                       int *__restrict__ order) {
+    __shared__ int cursor[kBins];
+    __shared__ int sums[kBins / 32];
+    const int heads = blockIdx.y ? heads_b : heads_f;
+    const size_t tiles = (size_t)g.batch * g.heads * g.nbmax;
+    const size_t base = (size_t)blockIdx.x * heads * g.nbmax;
+    if (base >= tiles) return;
+    const int n = (int)min((size_t)heads * g.nbmax, tiles - base), tid = threadIdx.x, lane = tid & 31;
+    const int *w = work + blockIdx.y * tiles + base;
+    int *out = order + blockIdx.y * tiles + base;
+    auto bin = [](int v) { return kBins - 1 - min(v, kBins - 1); };  // longest first
+    cursor[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kBins) {
+        out[i] = -1;
+        if (w[i] >= 0) atomicAdd(&cursor[bin(w[i])], 1);
+    }
+    __syncthreads();
+    const int mine = cursor[tid];  // exclusive scan of the counts
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[tid >> 5] = x;
+    __syncthreads();
+    int before = 0;
+    for (int k = 0; k < (tid >> 5); ++k) before += sums[k];
+    __syncthreads();
+    cursor[tid] = before + x - mine;
+    __syncthreads();
+    for (int i = tid; i < n; i += kBins)
+        if (w[i] >= 0) out[atomicAdd(&cursor[bin(w[i])], 1)] = (int)(base + i);
+}
+
 // Rows of padding tokens become zero: what they hold (infinities, NaN) would
 // reach other rows through products with P = 0.
 __global__ void __launch_bounds__(kThreads) k_zero_padding(Geo g, const int *__restrict__ doc, __nv_bfloat16 *__restrict__ Qp,
@@ -138,6 +204,8 @@ int buffers(Plan &pl, Buf *out) {
     out[n++] = {(void **)&s.blk, (size_t)g.batch * g.nbmax * sizeof(BlockRange)};
     out[n++] = {(void **)&s.row_end, lists * sizeof(int)};
     out[n++] = {(void **)&s.colT_end, lists * sizeof(int)};
+    out[n++] = {(void **)&s.order, 2 * lists * sizeof(int)};
+    out[n++] = {(void **)&s.work, 2 * lists * sizeof(int)};
     out[n++] = {(void **)&s.Olo, (size_t)g.heads * tokens * g.D * 2};
     out[n++] = {(void **)&s.col, nnz * sizeof(int)};
     out[n++] = {(void **)&s.rowT, nnz * sizeof(int)};
@@ -201,6 +269,19 @@ prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
     PRISM_CUDA_OK(cudaGetLastError());
     k_score_filter<true><<<1184, kThreads, 0, st>>>(g, pl.colT_ptr, pl.rowT, s.blk, s.colT_end, s.rowT);
     PRISM_CUDA_OK(cudaGetLastError());
+    const size_t tiles = (size_t)g.batch * g.heads * g.nbmax;
+    k_score_work<<<dim3((unsigned)((tiles + kThreads / 32 - 1) / (kThreads / 32)), 2), kThreads, 0, st>>>(
+        g, pl.nqt, pl.qt_blk, pl.blk_off, pl.row_ptr, s.row_end, s.col, pl.colT_ptr, s.colT_end, s.rowT, s.work);
+    PRISM_CUDA_OK(cudaGetLastError());
+    // all heads together while what the running tiles share stays in L2 (forward: K
+    // and V; backward: the fp32 dQ that every tile adds to), else head by head: 8
+    // heads of 30720 tokens (126 MB each) took 2.41 ms together, 2.13 apart in the
+    // backward, and the same either way in the forward
+    const int BH = g.batch * g.heads;
+    const double mb = (double)BH * g.N * g.D * 4 / 1e6;
+    const int group_f = mb <= 160 ? BH : 1, group_b = mb <= 80 ? BH : 1;
+    k_score_order<<<dim3(group_f == BH && group_b == BH ? 1 : BH, 2), kBins, 0, st>>>(g, group_f, group_b, s.work, s.order);
+    PRISM_CUDA_OK(cudaGetLastError());
     if (s.has_doc) {
         const prism_status z = launch_zero_padding(pl, st);
         if (z != PRISM_OK) return z;
@@ -213,6 +294,7 @@ ScoreArgs score_args(const Plan &pl, bool backward) {
     const Score &s = pl.score;
     ScoreArgs a{};
     a.list_end = backward ? s.colT_end : s.row_end;
+    a.order = s.order + (backward ? (size_t)pl.g.batch * pl.g.heads * pl.g.nbmax : 0);
     a.pos = s.pos;
     a.vis = s.vis;
     a.doc = s.doc;
