@@ -238,10 +238,12 @@ __device__ __forceinline__ void load_weights(const void *p, int dt, int c0, int 
 // kS: steps in a thread's ring, by what a thread holds per step (bytes); at 512
 // to 1280 threads per SM this keeps 64 to 128 KB in flight.
 constexpr int ring(int bytes) { return bytes <= 64 ? 4 : bytes <= 96 ? 3 : 2; }
+constexpr int bwd_ring(int bytes) { return bytes <= 64 ? 4 : 3; }
 // NR: rows that a group of threads takes at once, so that short rows share the
 // cost of a step and their reductions overlap.
 constexpr int fwd_rows(int channels, bool cta) { return cta || channels > 16 ? 1 : channels > 8 ? 2 : 4; }
-constexpr int bwd_rows(int channels, bool cta) { return cta || channels > 8 ? 1 : 2; }
+// (cta: 0 lanes of a warp, 1 a CTA of up to 192 threads, 2 of up to 512)
+constexpr int bwd_rows(int channels, int cta) { return cta == 1 ? 2 : cta == 2 || channels > 8 ? 1 : 2; }
 
 // A CTA's walk over the rows: step `it` takes rows it * step + j * per + sub
 // (j < NR) past its first; all of them exist except in the last step.
@@ -477,14 +479,17 @@ struct BwdArgs {
 // Each thread adds up dgamma and dbeta of its own channels over the CTA's rows
 // in registers; the CTA writes one partial.  Rows past the last one, and
 // channels past C, count as dy = 0.
-template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
-__global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(BwdArgs a) {
-    constexpr int VP = VEC / 2, NR = bwd_rows(NV * VEC, kCta), NP = NR * NV, kS = ring(NP * 32);
+// kCkpt: 0 x, 1 x's checkpoint, 2 the same with rows of scales that are whole
+// 32-bit words: a piece's word then travels behind its codes in their slot.
+template <typename T, int VEC, int NV, int kCta, int kCkpt>
+__global__ void __launch_bounds__(kCta == 2 ? 512 : kCta ? 192 : 256, kCta == 2 ? 1 : 2) k_norm_bwd(BwdArgs a) {
+    constexpr int VP = VEC / 2, NR = bwd_rows(NV * VEC, kCta), NP = NR * NV, kS = bwd_ring(NP * 32);
     constexpr bool kRing = VEC * sizeof(T) == 16;
     extern __shared__ uint4 slots[];  // [kS][dy, x or its codes][NP][threads]
-    __shared__ __align__(16) float red[2][2][16];  // [row's parity]
+    __shared__ __align__(16) float red[2][2 * NR][16];  // [step's parity]
     __shared__ float fold[kCta ? 1 : 256 * NV * VEC];
-    if (kCta && threadIdx.x < 64) (&red[0][0][0])[threadIdx.x] = 0.f;
+    if (kCta)
+        for (int k = threadIdx.x; k < 64 * NR; k += blockDim.x) (&red[0][0][0])[k] = 0.f;
     const int tpr = kCta ? blockDim.x : a.tpr, t = kCta ? threadIdx.x : (threadIdx.x & (tpr - 1));
     Walk w;
     w.init(a.nrows, kCta ? 1 : 256 / tpr, NR, kCta ? 0 : threadIdx.x / tpr);
@@ -499,6 +504,7 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(Bwd
     // without a ring: one step ahead in registers
     Vec<T, VEC> ndy[kRing ? 1 : NP], nx[kRing || kCkpt ? 1 : NP];
     Codes<VEC> nc[kRing || !kCkpt ? 1 : NP];
+    const int ng = (a.C + kGroup - 1) / kGroup;
     int fit = 0;  // the step to fetch
     auto fetch = [&](int s) {
 #pragma unroll
@@ -512,8 +518,11 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(Bwd
                     if (live && in[i]) {
                         copy_async<16>(&slot(s, p), dyr + v * 16);
                         if constexpr (kCkpt) copy_async<VEC>(&slot(s, NP + p), xr + v * VEC);
-                        else copy_async<16>(&slot(s, NP + p), xr + v * 16);
-                    } else if (!kCta) {  // rows past the last: zeros over what an earlier step left
+                        if constexpr (kCkpt == 2)
+                            copy_async<4>(reinterpret_cast<char *>(&slot(s, NP + p)) + VEC,
+                                          a.scales + w.row(fit, j) * ng + v / (kGroup / VEC) / 4 * 4);
+                        if constexpr (!kCkpt) copy_async<16>(&slot(s, NP + p), xr + v * 16);
+                    } else if (kCta != 2) {  // rows past the last: zeros over what an earlier step left
                         slot(s, p) = make_uint4(0, 0, 0, 0);
                     }
                 } else {
@@ -541,7 +550,6 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(Bwd
     } else {
         fetch(0);
     }
-    const int ng = (a.C + kGroup - 1) / kGroup;
     uint32_t xs[NP];
     float mean[NR], rstd[NR];
     auto ahead = [&](int it) {  // what is small: one step ahead in registers
@@ -551,7 +559,7 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(Bwd
             const long long r = w.row(it, j);
             mean[j] = live ? a.mean[r] : 0.f;
             rstd[j] = live ? a.rstd[r] : 0.f;
-            if constexpr (kCkpt) {
+            if constexpr (kCkpt == 1) {
                 const uint8_t *sr = a.scales + r * ng;
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
@@ -588,7 +596,12 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_bwd(Bwd
                     Codes<VEC> c;
                     if constexpr (kRing) c.load(reinterpret_cast<const uint8_t *>(&slot(cur, NP + p)), 0, VEC);
                     else c = nc[p];
-                    c.template decode<float>(xs[p], a.fmt, xh[p]);
+                    uint32_t sb = xs[p];
+                    if constexpr (kCkpt == 2) {
+                        const uint32_t word = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const char *>(&slot(cur, NP + p)) + VEC);
+                        sb = (word >> (8 * ((i * tpr + t) / (kGroup / VEC) & 3))) & 0xffu;
+                    }
+                    c.template decode<float>(sb, a.fmt, xh[p]);
                 } else {
                     Vec<T, VEC> x;
                     if constexpr (kRing) x.set(slot(cur, NP + p));
@@ -694,17 +707,21 @@ Spread spread(int C, const int (&nvs)[N]) {
     return s;
 }
 
+// Dynamic shared memory that every kernel here may be given beside its static
+// part (at most 16.5 KB) of an SM's 227 KB.
+constexpr size_t kMostSmem = 208 * 1024;
+
 // Launches with dynamic shared memory; above 48 KB it has to be asked for,
 // once per kernel and device.
 template <typename Args>
 prism_status launch(void (*kernel)(Args), const Args &a, int grid, int threads, size_t smem,
                     std::atomic<unsigned long long> &asked, cudaStream_t st) {
-    if (smem > 48 * 1024 - 1024) {  // the kernels' static shared memory counts too
+    if (smem > 31 * 1024) {  // the static part counts towards the 48 KB too
         int dev = 0;
         PRISM_CUDA_OK(cudaGetDevice(&dev));
         const unsigned long long bit = 1ull << (dev & 63);
         if (!(asked.load(std::memory_order_relaxed) & bit)) {
-            PRISM_CUDA_OK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+            PRISM_CUDA_OK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem));
             asked.fetch_or(bit, std::memory_order_relaxed);
         }
     }
@@ -740,6 +757,15 @@ prism_status run_fwd(const FwdArgs &a, cudaStream_t st) {
     if (NV * VEC > 16) smem += (size_t)a.nvec * VEC * 8;  // gamma and beta
     return launch(k_norm_fwd<T, VEC, NV, kCta, kCkpt>, a, (int)(need < most ? need : most), threads, smem, asked, st);
 }
+// Whether a row's ring and its weights (fp32) fit: about 12500 channels of 16 bits, 8192 to 13000 of 32.
+template <typename T, int VEC>
+bool fwd_fits(int C) {
+    const int nvec = (C + VEC - 1) / VEC;
+    if (nvec <= 32 * 8) return true;
+    const int nv = nvec <= 512 * 4 ? 4 : 8, threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+    const size_t slots = VEC * sizeof(T) == 16 ? (size_t)ring(nv * 16) * nv * 16 * threads : 0;
+    return threads <= 512 && slots + (size_t)nvec * VEC * 8 <= kMostSmem;
+}
 template <typename T, int VEC, bool kCkpt>
 prism_status fwd_spread(FwdArgs &a, cudaStream_t st) {
     static const int nvs[] = {1, 2, 3, 4, 6, 8, VEC == 2 ? 16 : 8};
@@ -767,7 +793,7 @@ prism_status fwd_impl(const NormFwd &n, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
     const size_t row = (size_t)n.C * sizeof(T);
     const bool vec = aligned16(n.x, row) && aligned16(n.y, row);
-    if (n.C <= 512 * 8 * (vec ? VEC : 2)) {
+    if (vec ? fwd_fits<T, VEC>(n.C) : fwd_fits<T, 2>(n.C)) {
         FwdArgs a{n.x, n.y, n.gamma, n.beta, n.wdt, (((uintptr_t)n.gamma | (uintptr_t)n.beta) & 15) == 0,
                   n.mean, n.rstd, n.codes, n.scales, n.fmt, n.nrows, n.C, 0, 0, n.eps, 1.f / (float)n.C};
         if (vec) return n.codes ? fwd_spread<T, VEC, true>(a, st) : fwd_spread<T, VEC, false>(a, st);
@@ -786,30 +812,33 @@ prism_status fwd_impl(const NormFwd &n, cudaStream_t st) {
 template <int VEC>
 constexpr int kBwdNV = VEC == 8 ? 2 : 4;
 
-template <typename T, int VEC, int NV, bool kCta, bool kCkpt>
+template <typename T, int VEC, int NV, int kCta, int kCkpt>
 prism_status run_bwd(const BwdArgs &a, int &P, cudaStream_t st) {
     constexpr bool kRing = VEC * sizeof(T) == 16;
     constexpr int kNR = bwd_rows(NV * VEC, kCta);
     static std::atomic<unsigned long long> asked{0};
     const int per = (kCta ? 1 : 256 / a.tpr) * kNR, threads = kCta ? a.tpr : 256;
-    const long long need = (a.nrows + per - 1) / per, most = 148ll * (kCta ? (kRing ? 512 : 768) / a.tpr : 2);
+    const int per_sm = kCta == 0 ? 2 : kCta == 1 ? 384 / a.tpr : (kRing ? 512 : 768) / a.tpr;
+    const long long need = (a.nrows + per - 1) / per, most = 148ll * per_sm;
     if (P > need) P = (int)need;
     if (P > most) P = (int)most;
-    const size_t smem = kRing ? (size_t)ring(kNR * NV * 32) * kNR * NV * 32 * threads : 0;
+    const size_t smem = kRing ? (size_t)bwd_ring(kNR * NV * 32) * kNR * NV * 32 * threads : 0;
     return launch(k_norm_bwd<T, VEC, NV, kCta, kCkpt>, a, P, threads, smem, asked, st);
 }
 // P: partials allowed; on return the partials written
-template <typename T, int VEC, bool kCkpt>
+template <typename T, int VEC, int kCkpt>
 prism_status bwd_spread(BwdArgs &a, int &P, cudaStream_t st) {
     constexpr int kMost = kBwdNV<VEC>;
     static const int nvs[] = {kMost / 2, kMost};
     const Spread s = spread<VEC>(a.C, nvs);
     a.nvec = s.nvec;
     a.tpr = s.tpr;
-    if (s.nv) return s.nv == kMost ? run_bwd<T, VEC, kMost, false, kCkpt>(a, P, st)
-                                   : run_bwd<T, VEC, kMost / 2, false, kCkpt>(a, P, st);
+    if (s.nv) return s.nv == kMost ? run_bwd<T, VEC, kMost, 0, kCkpt>(a, P, st)
+                                   : run_bwd<T, VEC, kMost / 2, 0, kCkpt>(a, P, st);
     a.tpr = ((a.nvec + kMost - 1) / kMost + 31) / 32 * 32;
-    return run_bwd<T, VEC, kMost, true, kCkpt>(a, P, st);
+    if constexpr (VEC != 2)
+        if (a.tpr <= 192) return run_bwd<T, VEC, kMost, 1, kCkpt>(a, P, st);
+    return run_bwd<T, VEC, kMost, 2, kCkpt>(a, P, st);
 }
 
 template <typename T>
@@ -826,8 +855,11 @@ prism_status bwd_impl(const NormBwd &n, cudaStream_t st) {
         BwdArgs a{x, n.dy, n.dx, n.scales, n.fmt, n.gamma, n.wdt, ((uintptr_t)n.gamma & 15) == 0,
                   n.mean, n.rstd, part, n.nrows, n.C, 0, 0, 1.f / (float)n.C};
         prism_status s;
-        if (vec) s = n.codes ? bwd_spread<T, VEC, true>(a, P, st) : bwd_spread<T, VEC, false>(a, P, st);
-        else s = n.codes ? bwd_spread<T, 2, true>(a, P, st) : bwd_spread<T, 2, false>(a, P, st);
+        const bool words = (n.C + kGroup - 1) / kGroup % 4 == 0;
+        if (vec) s = !n.codes ? bwd_spread<T, VEC, 0>(a, P, st)
+                     : words  ? bwd_spread<T, VEC, 2>(a, P, st)
+                              : bwd_spread<T, VEC, 1>(a, P, st);
+        else s = n.codes ? bwd_spread<T, 2, 1>(a, P, st) : bwd_spread<T, 2, 0>(a, P, st);
         if (s != PRISM_OK) return s;
     } else {
         const Source<T> src{n.x, n.codes, n.scales, n.fmt, n.C};

@@ -288,6 +288,26 @@ def test_layer_norm_through_a_checkpoint(P, shape, kind, dtype, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_channel_counts_in_turn(P, dtype):
+    """Every way a row is laid over threads, small to large and back: a kernel's shared memory grows with the channels."""
+    t = DTYPES[dtype]
+    sizes = [8, 72, 256, 520, 768, 1024, 1280, 1536, 2048, 2056, 3328, 4096, 6144, 8184, 8192, 8200, 11264, 12288, 12544,
+             13312, 16384, 16400, 17408, 24576, 32768, 33000, 257, 511, 1023, 1027, 2049, 4095, 4097, 8191, 8193]
+    for C in sizes + sizes[::-1]:
+        x, dy = make((5, C), t, C), make((5, C), t, C + 1)
+        gamma = torch.linspace(0.5, 1.5, C, device="cuda")
+        y, mean, rstd, kept = P.prism_layer_norm_fwd(x, gamma, gamma, 1e-5, ckpt="int8")
+        (ry, rm, rr), (by, bm, br) = norm_fwd_reference(x, gamma, gamma, 1e-5)
+        close(y, ry, by, f"y {C}")
+        close(rstd, rr, br, f"rstd {C}")
+        for src in (x, kept):
+            want, bound = norm_bwd_reference(x if src is x else value_of(kept).cuda(), dy, gamma, mean, rstd)
+            for got, w, b, what in zip(P.prism_layer_norm_bwd(dy, src, gamma, mean, rstd), want, bound, ("dx", "dgamma", "dbeta")):
+                close(got, w, b, f"{what} {C}")
+
+
+@pytest.mark.gpu
 def test_layer_norm_gradient_against_differences(P):
     """d(sum y w)/d(x, gamma, beta) by central differences of the 64-bit definition."""
     x, w = make((6, 48), torch.float32, 9), make((6, 48), torch.float32, 10)
