@@ -368,6 +368,8 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_fwd(Fwd
     };
     if (kCta) __syncthreads();
     const int ng = (a.C + kGroup - 1) / kGroup;
+    uint8_t *cw = a.codes + (w.first + w.sub) * a.C, *sw = a.scales + (w.first + w.sub) * ng;
+    const long long cinc = w.step * a.C, sinc = w.step * ng;
     for (int it = 0; it < w.steps; ++it) {
         f2 x[NP][VP];
         if constexpr (kRing) copy_wait<kS - 2>();
@@ -402,18 +404,20 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_fwd(Fwd
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
                 const bool live = w.live(it, j);
-                const long long r = w.row(it, j);
+                uint8_t *cr = cw + j * w.per * (long long)a.C, *sr = sw + j * w.per * (long long)ng;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int v = i * tpr + t, k = group_exponent<VEC>(top_of(x[j * NV + i]), a.fmt);
                     if (in[i] && live) {
                         Codes<VEC> c;
                         c.encode(x[j * NV + i], code_inv_scale(k), a.fmt);
-                        c.store(a.codes + r * a.C, v, a.C);
-                        if (v % (kGroup / VEC) == 0) a.scales[r * ng + v / (kGroup / VEC)] = (uint8_t)(k + 127);
+                        c.store(cr, v, a.C);
+                        if (v % (kGroup / VEC) == 0) sr[v / (kGroup / VEC)] = (uint8_t)(k + 127);
                     }
                 }
             }
+            cw += cinc;
+            sw += sinc;
         }
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
@@ -505,6 +509,9 @@ __global__ void __launch_bounds__(kCta == 2 ? 512 : kCta ? 192 : 256, kCta == 2 
     Vec<T, VEC> ndy[kRing ? 1 : NP], nx[kRing || kCkpt ? 1 : NP];
     Codes<VEC> nc[kRing || !kCkpt ? 1 : NP];
     const int ng = (a.C + kGroup - 1) / kGroup;
+    int sbit[NV];  // where a piece's scale lies in its word
+#pragma unroll
+    for (int i = 0; i < NV; ++i) sbit[i] = 8 * ((i * tpr + t) / (kGroup / VEC) & 3);
     int fit = 0;  // the step to fetch
     auto fetch = [&](int s) {
 #pragma unroll
@@ -599,9 +606,9 @@ __global__ void __launch_bounds__(kCta == 2 ? 512 : kCta ? 192 : 256, kCta == 2 
                     uint32_t sb = xs[p];
                     if constexpr (kCkpt == 2) {
                         const uint32_t word = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const char *>(&slot(cur, NP + p)) + VEC);
-                        sb = (word >> (8 * ((i * tpr + t) / (kGroup / VEC) & 3))) & 0xffu;
+                        sb = (word >> sbit[i]) & 0xffu;
                     }
-                    c.template decode<float>(sb, a.fmt, xh[p]);
+                    c.decode_norm(sb, a.fmt, mean[j], rs[j], xh[p]);
                 } else {
                     Vec<T, VEC> x;
                     if constexpr (kRing) x.set(slot(cur, NP + p));
@@ -611,7 +618,7 @@ __global__ void __launch_bounds__(kCta == 2 ? 512 : kCta ? 192 : 256, kCta == 2 
                 }
 #pragma unroll
                 for (int e = 0; e < VP; ++e) {
-                    xh[p][e] = mul2(add2(xh[p][e], mm), r2);
+                    if constexpr (!kCkpt) xh[p][e] = mul2(add2(xh[p][e], mm), r2);
                     const f2 d = dy.pair(e);
                     dg[i][e] = fma2(d, xh[p][e], dg[i][e]);
                     db[i][e] = add2(db[i][e], d);

@@ -73,8 +73,8 @@ __device__ __forceinline__ int code_exponent(float amax, int fmt) {
 __device__ __forceinline__ float code_inv_scale(int k) { return k == 128 ? 0.f : __uint_as_float((uint32_t)(127 - k) << 23); }
 // 2^k of a scale byte
 __device__ __forceinline__ float code_scale(uint32_t byte) {
-    if (byte == 255u) return __uint_as_float(0x7fc00000u);
-    return byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+    const uint32_t u = max(byte << 23, 0x00400000u);  // 2^-127 is no normal number
+    return __uint_as_float(byte == 255u ? 0x7fc00000u : u);
 }
 // The largest finite value: a code may stand for a little more than it.
 template <typename T>
@@ -265,26 +265,41 @@ struct Codes {
             for (int i = 0; i < W; ++i) w[i] = h[2 * i] | (h[(2 * i + 1) % VP] << 16);
         }
     }
+    // (q 2^k - mean) rstd of the codes, scale byte sb: q 2^k - mean is one
+    // multiply-add, rounded once.
+    __device__ __forceinline__ void decode_norm(uint32_t sb, int fmt, float mean, float rstd, f2 (&x)[VP]) const {
+        const f2 sc = both(code_scale(sb)), m2 = both(-mean), r2 = both(rstd);
+        if (fmt == PRISM_CKPT_INT8) {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) x[i] = mul2(fma2(whole(i), sc, m2), r2);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) x[i] = mul2(fma2(small_float(i), sc, m2), r2);
+        }
+    }
+    // pair i's codes as int8 (byte + 128 in the mantissa of 2^23) and as e4m3
+    __device__ __forceinline__ f2 whole(int i) const {
+        const uint32_t u = (VEC == 2 ? w[0] | second << 8 : w[i / 2]) ^ 0x80808080u;
+        const uint32_t lo = __byte_perm(u, 0x4b000000u, i & 1 ? 0x7542 : 0x7540);
+        const uint32_t hi = __byte_perm(u, 0x4b000000u, i & 1 ? 0x7543 : 0x7541);
+        return add2((f2)lo | ((f2)hi << 32), both(-8388736.f));
+    }
+    __device__ __forceinline__ f2 small_float(int i) const {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)(VEC == 2 ? w[0] | second << 8 : w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        return make2(f.x, f.y);
+    }
     // the values q 2^k of the codes, scale byte sb, held within T's range
     template <typename T>
     __device__ __forceinline__ void decode(uint32_t sb, int fmt, f2 (&x)[VP]) const {
         const f2 sc = both(code_scale(sb));
-        if (fmt == PRISM_CKPT_INT8) {  // byte + 128 in the mantissa of 2^23
+        if (fmt == PRISM_CKPT_INT8) {
 #pragma unroll
-            for (int i = 0; i < VP; ++i) {
-                const uint32_t u = (VEC == 2 ? w[0] | second << 8 : w[i / 2]) ^ 0x80808080u;
-                const uint32_t lo = __byte_perm(u, 0x4b000000u, i & 1 ? 0x7542 : 0x7540);
-                const uint32_t hi = __byte_perm(u, 0x4b000000u, i & 1 ? 0x7543 : 0x7541);
-                x[i] = mul2(add2((f2)lo | ((f2)hi << 32), both(-8388736.f)), sc);
-            }
+            for (int i = 0; i < VP; ++i) x[i] = mul2(whole(i), sc);
         } else {
 #pragma unroll
-            for (int i = 0; i < VP; ++i) {
-                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                    (__nv_fp8x2_storage_t)(VEC == 2 ? w[0] | second << 8 : w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-                const float2 f = __half22float2(__half2(h));
-                x[i] = mul2(make2(f.x, f.y), sc);
-            }
+            for (int i = 0; i < VP; ++i) x[i] = mul2(small_float(i), sc);
         }
         // 127 * 2^119 and 448 * 2^119 are finite; fp16 ends sooner
         if (sb >= (sizeof(T) == 2 && largest<T>() < 1e5f ? 128u : 247u) && sb != 255u) {
