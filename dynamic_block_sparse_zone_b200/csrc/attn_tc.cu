@@ -41,24 +41,16 @@
 // blocks of S_i); each softmax warp then turns a chunk's 128 entries into
 // float biases in its own buffer.  One online softmax covers both parts.
 //
-// Scored variants (kScore): the selection is the one without hidden block
-// pairs (score.cu); the score is cap tanh(s / cap) - slope_h |p_q - p_k|, and in
-// the pairs that are only partly visible a key counts where its document is the
-// query's and the query's position has reached its visibility.  The producer
-// brings a chunk's key positions, visibilities and documents (128 each) into
-// one of two slots beside the segment mask; wholly visible pairs, most of
-// them, skip the mask.  What the score needs makes the softmax the longest
-// stage, so it has eight warps (two threads per row, 64 keys each) instead of
-// four: with four, capped scores issued 0.32 instructions per cycle and
-// scheduler, held by latency.  P of the second 64 keys then lies over its own
-// scores, TMEM columns [64, 128).  P goes to the tensor cores as hi + lo, two
-// bf16 numbers and two products with V: an 8-bit O is kept for the backward, and
-// a P of 8 bits moves O by about half a step of bf16, enough for every tenth
-// 8-bit code to fall on the other side and Delta with it (dQ off by up to
-// 0.012 in relative norm, 0.003 so).
+// Scored variants (kScore): the tiles that the scored forward proper
+// (attn_scored_tc.cu, where the scores are described) puts off because a row's
+// logits lie too far from 0 for a fixed reference: the same scores with a
+// running maximum.  The producer brings a chunk's key positions, visibilities
+// and documents (128 each) into one of two slots beside the segment mask.
+// Eight softmax warps: two threads per row, 64 keys each; P of the second 64
+// keys lies over its own scores, TMEM columns [64, 128).
 #include <cuda.h>
 
-#include "tc_common.cuh"
+#include "score_tc.cuh"
 
 namespace prism {
 
@@ -120,9 +112,10 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
     const uint32_t sbase = smem_u32(smem);
 
     int tile = blockIdx.x, bh = blockIdx.y;
-    if constexpr (kEnc) {  // long tiles first
-        const int t = sc.order[blockIdx.y * gridDim.x + blockIdx.x];
-        if (t < 0) return;
+    if constexpr (kEnc) {  // the tiles that k_attn_fwd_scored has put off
+        const int id = blockIdx.y * gridDim.x + blockIdx.x;
+        if (id >= sc.redo[0]) return;
+        const int t = sc.redo[1 + id];
         bh = t / g.nbmax;
         tile = t - bh * g.nbmax;
     }
@@ -355,63 +348,7 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
                     tmem_ld32(tSr + 32 * q, sr);
                     const uint32_t meta = sbase + L::kMeta + (c & 1) * L::kMetaSlot + seg * 256 + q * 128;
                     tmem_wait_ld();
-                    float k = scale_log2, a = 0.f;  // the logit is what is in place times k, plus a and the bias
-                    if constexpr ((kScore & kCap) != 0) {
-                        float ma = 0.f, mb = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float *x = reinterpret_cast<const float *>(&sr[e]);
-                            ma = fmax3_abs(ma, x[0], x[1]);
-                            mb = fmax3_abs(mb, x[2], x[3]);
-                        }
-                        if (__all_sync(0xffffffffu, fmaxf(ma, mb) <= sc.cap_one)) {  // tanh in place
-                            const uint64_t ku = splat2(sc.cap_u);
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float *x = reinterpret_cast<float *>(&sr[e]);
-                                const uint64_t t = tanh_small2(x[0], x[1], ku);
-                                x[0] = plo(t), x[1] = phi(t);
-                            }
-                            k = sc.cap_out;
-                        } else {  // q of every score in place
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                float *x = reinterpret_cast<float *>(&sr[e]);
-                                uint64_t q02, q13;
-                                logistic4(x[0], x[1], x[2], x[3], sc.cap_in, q02, q13);
-                                x[0] = plo(q02), x[1] = plo(q13), x[2] = phi(q02), x[3] = phi(q13);
-                            }
-                            k = -2.f * sc.cap_out;
-                            a = sc.cap_out;
-                        }
-                    }
-                    if constexpr (kScaled) {
-                        const uint64_t k2 = splat2(k);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float *x = reinterpret_cast<float *>(&sr[e]);
-                            uint64_t a01 = splat2(a), a23 = splat2(a);
-                            if constexpr ((kScore & kBias) != 0) {
-                                const float4 pk = lds_f4(meta + e * 4);
-                                a01 = pair2(fmaf(-slope2, fabsf(pq - pk.x), a), fmaf(-slope2, fabsf(pq - pk.y), a));
-                                a23 = pair2(fmaf(-slope2, fabsf(pq - pk.z), a), fmaf(-slope2, fabsf(pq - pk.w), a));
-                            }
-                            const uint64_t y01 = pfma(pair2(x[0], x[1]), k2, a01), y23 = pfma(pair2(x[2], x[3]), k2, a23);
-                            x[0] = plo(y01), x[1] = phi(y01), x[2] = plo(y23), x[3] = phi(y23);
-                        }
-                    }
-                    if (part) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 vk = lds_f4(meta + 512 + e * 4);
-                            const float4 dk = lds_f4(meta + 1024 + e * 4);
-                            const uint32_t ninf = 0xff800000u;
-                            if (!(vk.x <= pq && __float_as_int(dk.x) == dq)) sr[e] = ninf;
-                            if (!(vk.y <= pq && __float_as_int(dk.y) == dq)) sr[e + 1] = ninf;
-                            if (!(vk.z <= pq && __float_as_int(dk.z) == dq)) sr[e + 2] = ninf;
-                            if (!(vk.w <= pq && __float_as_int(dk.w) == dq)) sr[e + 3] = ninf;
-                        }
-                    }
+                    logits32<kScore>(sr, sc, scale_log2, slope2, pq, dq, meta, meta + 512, meta + 1024, part);
                     if (kScaled || part) tmem_st32(tSr + 32 * q, sr);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
@@ -474,17 +411,7 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float x0, x1;
-                        fma2(__uint_as_float(sr[q][2 * e]), __uint_as_float(sr[q][2 * e + 1]), s2, c2, x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        add2(acc2, p0, p1);
-                        const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-                        hi[e] = __byte_perm(u0, u1, 0x7632);
-                        const uint64_t d = psub(pair2(p0, p1), (uint64_t)(u0 & 0xffff0000u) | (uint64_t)(u1 & 0xffff0000u) << 32);
-                        lo[e] = pack_bf16x2(plo(d), phi(d));
-                    }
+                    split_exp32(sr[q], s2, c2, acc2, hi, lo);
                     tmem_st16(tSr + 16 * q, hi);
                     tmem_st16(tSr + 32 + 16 * q, lo);
                 }
@@ -876,7 +803,7 @@ static prism_status fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t st) {
     }
 }
 
-prism_status launch_attn_fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t st) {
+prism_status launch_attn_fwd_scored_redo(Plan &pl, void *O, float *lse, cudaStream_t st) {
     return pl.g.D == 64 ? fwd_scored<64>(pl, O, lse, st) : fwd_scored<128>(pl, O, lse, st);
 }
 

@@ -38,6 +38,7 @@ int host_shape_table(int (*e)[3]);
 prism_status configure_plan_kernels(const Plan &pl);
 prism_status configure_attn_tc_kernels();
 prism_status configure_attn_bwd_tc_kernels();
+prism_status configure_attn_scored_kernels();
 prism_status launch_selftest_bounded_wait(Plan &pl, cudaStream_t st);
 size_t select_smem_bytes(const Plan &pl);
 
@@ -306,6 +307,7 @@ prism_status prism_plan_create(const prism_params *params, prism_plan **out) {
     s = configure_plan_kernels(pl);
     if (s == PRISM_OK) s = configure_attn_tc_kernels();
     if (s == PRISM_OK) s = configure_attn_bwd_tc_kernels();
+    if (s == PRISM_OK) s = configure_attn_scored_kernels();
     if (s == PRISM_OK) s = make_tensor_maps(pl);
     if (s == PRISM_OK && pl.p.hilbert_block) s = setup_hilbert_plan(pl);
 

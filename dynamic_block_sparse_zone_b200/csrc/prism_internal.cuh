@@ -61,6 +61,7 @@ struct Score {
     int *order;             // [2][batch*heads*nbmax] sample*head * nbmax + tile in launch order, the forward's query
                             // tiles and the backward's key tiles; -1: none
     int *work;              // [2][batch*heads*nbmax] 64-row segments of each tile
+    int *redo;              // [1 + batch*heads*nbmax] count, then the forward's tiles to be done with a running maximum
 };
 
 // Everything a plan owns (device pointers unless noted).
@@ -162,6 +163,7 @@ prism_status launch_attn_bwd_ckpt(Plan &pl, const prism_attn_ckpt &c, const void
                                   bool scored, cudaStream_t st);
 
 prism_status launch_attn_fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t st);
+prism_status launch_attn_fwd_scored_redo(Plan &pl, void *O, float *lse, cudaStream_t st);
 prism_status launch_attn_bwd_tc_scored(Plan &pl, void *dK, void *dV, cudaStream_t st);
 prism_status set_score(Plan &pl, const prism_score &s, cudaStream_t st);
 prism_status launch_zero_padding(Plan &pl, cudaStream_t st);  // padding tokens' rows of Qp, Kp, Vp
@@ -171,6 +173,7 @@ void release_score(Plan &pl);
 struct ScoreArgs {
     const int *list_end;        // row_end (forward) or colT_end (backward)
     const int *order;           // tile of each CTA
+    int *redo;                  // the forward's tiles put off (Score::redo)
     const float *pos, *vis;
     const int *doc;
     const float *slopes;

@@ -206,6 +206,7 @@ int buffers(Plan &pl, Buf *out) {
     out[n++] = {(void **)&s.colT_end, lists * sizeof(int)};
     out[n++] = {(void **)&s.order, 2 * lists * sizeof(int)};
     out[n++] = {(void **)&s.work, 2 * lists * sizeof(int)};
+    out[n++] = {(void **)&s.redo, (1 + lists) * sizeof(int)};
     out[n++] = {(void **)&s.Olo, (size_t)g.heads * tokens * g.D * 2};
     out[n++] = {(void **)&s.col, nnz * sizeof(int)};
     out[n++] = {(void **)&s.rowT, nnz * sizeof(int)};
@@ -300,6 +301,7 @@ ScoreArgs score_args(const Plan &pl, bool backward) {
     a.doc = s.doc;
     a.slopes = s.slopes;
     a.Olo = s.Olo;
+    a.redo = s.redo;
     if (s.cap > 0.f) {
         a.cap_one = (float)(sqrt((double)pl.g.D) * (double)s.cap);
         a.cap_u = (float)(1.0 / (sqrt((double)pl.g.D) * (double)s.cap));
