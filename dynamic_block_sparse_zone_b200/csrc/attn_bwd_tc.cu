@@ -50,9 +50,9 @@
 // Scored variants (kScore): the columns without hidden block pairs (score.cu);
 // S becomes cap tanh(S / cap) - slope_h |p_q - p_k|, dS gets the factor
 // 1 - tanh^2, and in a pair that is only partly visible a hidden key's P and dS
-// are 0.  A key's position, visibility and document stay in its row's
-// registers; those of a chunk's queries come from global memory (L1: the
-// shared memory is full), one broadcast load per four.
+// are 0 (its logit -inf).  Positions, visibilities and documents come from
+// global memory (L1: the shared memory is full, and 80 registers hold no more),
+// a chunk's queries as one broadcast load per four.
 //
 // Warp roles (704 threads): warp 0 TMA producer (K, V once; Q, dO, LSE,
 // Delta per chunk into a three-stage ring; LSE is kept negated, in log2
@@ -106,6 +106,22 @@ __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t adesc, uint
         mma_ss8<2, 4, 6, 1024, 1026, 1028, 1030, 2, 4, 6, 512, 514, 516, 518>(d_tmem, adesc, bdesc, idesc, 0u);
     else
         mma_ss4<2, 4, 6, 2, 4, 6>(d_tmem, adesc, bdesc, idesc, 0u);
+}
+
+// Scored: -inf for the scores of those of the 16 queries from row q0 on (in the
+// sample whose tokens start at n0) that do not see key kn.
+__device__ __forceinline__ void hide16(uint32_t (&sv)[16], const ScoreArgs &sc, size_t n0, int q0, int kn) {
+    const float vk = __ldg(sc.vis + n0 + kn);
+    const int dk = __ldg(sc.doc + n0 + kn);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 pq = __ldg(reinterpret_cast<const float4 *>(sc.pos + n0 + q0) + j);
+        const int4 dq = __ldg(reinterpret_cast<const int4 *>(sc.doc + n0 + q0) + j);
+        if (!(vk <= pq.x && dq.x == dk)) sv[4 * j] = 0xff800000u;
+        if (!(vk <= pq.y && dq.y == dk)) sv[4 * j + 1] = 0xff800000u;
+        if (!(vk <= pq.z && dq.z == dk)) sv[4 * j + 2] = 0xff800000u;
+        if (!(vk <= pq.w && dq.w == dk)) sv[4 * j + 3] = 0xff800000u;
+    }
 }
 
 enum { kSiteKV = 11, kSiteQFull, kSiteQEmpty, kSiteS, kSiteDQFull = 16, kSiteDQEmpty, kSiteDone, kSiteToken };
@@ -258,16 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = rowid < kvalid;
         const int half = shared_tile ? (quad >> 1) : 0;  // which key block's rows (warp-uniform)
         bool ok = true;
-        // scored: this key's position, visibility and document (no query has -2), the slope in log2 units
-        float pk = 0.f, vk = 0.f, slope2 = 0.f;
-        int dk = -2;
-        if constexpr (kEnc) {
-            if (live) {
-                pk = sc.pos[(size_t)b * g.N + k0 + rowid];
-                vk = sc.vis[(size_t)b * g.N + k0 + rowid];
-                dk = sc.doc[(size_t)b * g.N + k0 + rowid];
-            }
-            if (kScore & kBias) slope2 = sc.slopes[h] * 1.4426950408889634f;
+        // scored, with a bias: this key's position and the slope in log2 units
+        float pk = 0.f, slope2 = 0.f;
+        if constexpr ((kScore & kBias) != 0) {
+            if (live) pk = sc.pos[(size_t)b * g.N + k0 + rowid];
+            slope2 = sc.slopes[h] * 1.4426950408889634f;
         }
         const bool issuer = ((warp - 2) & 7) == 0;  // the group's first warp issues its products
         constexpr uint32_t idST = idesc_bf16(128, 64, false);
@@ -306,7 +317,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t mw = mask_s[st];
                 const bool act = live && ((mw >> half) & 1u);
                 const bool part = kEnc && ((mw >> (2 + half)) & 1u);
-                const size_t qn = kEnc ? (size_t)b * g.N + (mw >> 4) : 0;  // the chunk's first query
                 const uint32_t dsrow = sbase + L::kDS + (c & 1) * 16384 + rowid * 128;
 #pragma unroll 1
                 for (int sub = 0; sub < 2; ++sub) {
@@ -317,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld16(tmem + kColDP + (c & 1) * 64 + 16 * cq + lane_off, dv);
                     const uint32_t vec = sbase + L::kVec + st * 512 + cq * 64;
                     uint32_t pd[16];
-                    if constexpr (!kEnc) {
+                    if constexpr ((kScore & (kCap | kBias)) == 0) {
                         float4 N4[4], D4[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -327,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         if (act) {
                             const uint64_t s2 = splat2(scale_log2);
+                            if (kEnc && part) hide16(sv, sc, (size_t)b * g.N, (int)(mw >> 4) + 16 * cq, k0 + rowid);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int q = 4 * j;
@@ -346,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int e = 0; e < 16; ++e) pd[e] = 0u;
                         }
                     } else {
-                        // the scored form of the same: x from cap tanh(S / cap) and the bias, P = 0 where
-                        // the key is hidden, dS times tanh's derivative 1 - tanh^2
+                        // the same with the logit from cap tanh(S / cap) and the bias, and dS times
+                        // tanh's derivative 1 - tanh^2
                         tmem_wait_ld();
                         bool small = true;
                         if constexpr ((kScore & kCap) != 0) {  // (rows that are not active do not matter)
@@ -360,18 +371,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                             small = __all_sync(0xffffffffu, !act || fmaxf(ma, mb) <= sc.cap_one);
                         }
                         if (act) {
+                            const size_t qi = (size_t)b * g.N + (mw >> 4) + 16 * cq;  // the first query
+                            float vk = 0.f;  // this key's visibility and document
+                            int dk = 0;
+                            if (part) {
+                                vk = __ldg(sc.vis + (size_t)b * g.N + k0 + rowid);
+                                dk = __ldg(sc.doc + (size_t)b * g.N + k0 + rowid);
+                            }
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int q = 4 * j;
-                                const size_t qi = qn + 16 * cq + 4 * j;
-                                float4 pq = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if ((kScore & kBias) || part) pq = __ldg(reinterpret_cast<const float4 *>(sc.pos + qi));
+                                // what is added to the scaled score: -LSE, the bias, -inf where the key is hidden
+                                float4 N = lds_f4(vec + 16 * j);
+                                if ((kScore & kBias) || part) {
+                                    const float4 pq = __ldg(reinterpret_cast<const float4 *>(sc.pos + qi) + j);
+                                    if constexpr ((kScore & kBias) != 0) {
+                                        N.x = fmaf(-slope2, fabsf(pq.x - pk), N.x), N.y = fmaf(-slope2, fabsf(pq.y - pk), N.y);
+                                        N.z = fmaf(-slope2, fabsf(pq.z - pk), N.z), N.w = fmaf(-slope2, fabsf(pq.w - pk), N.w);
+                                    }
+                                    if (part) {
+                                        const int4 dq = __ldg(reinterpret_cast<const int4 *>(sc.doc + qi) + j);
+                                        if (!(vk <= pq.x && dq.x == dk)) N.x = -INFINITY;
+                                        if (!(vk <= pq.y && dq.y == dk)) N.y = -INFINITY;
+                                        if (!(vk <= pq.z && dq.z == dk)) N.z = -INFINITY;
+                                        if (!(vk <= pq.w && dq.w == dk)) N.w = -INFINITY;
+                                    }
+                                }
                                 float x0 = __uint_as_float(sv[q]), x1 = __uint_as_float(sv[q + 1]);
                                 float x2 = __uint_as_float(sv[q + 2]), x3 = __uint_as_float(sv[q + 3]);
                                 float m4 = scale_log2;
                                 uint64_t g01 = 0, g23 = 0;  // 1 - tanh^2
-                                float4 N = lds_f4(vec + 16 * j);
-                                const float4 dl = lds_f4(vec + 256 + 16 * j);
                                 if constexpr ((kScore & kCap) != 0) {
                                     if (small) {
                                         const uint64_t ku = splat2(sc.cap_u), one = splat2(1.f), neg = splat2(-1.f);
@@ -390,23 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         N.x += sc.cap_out, N.y += sc.cap_out, N.z += sc.cap_out, N.w += sc.cap_out;
                                     }
                                 }
-                                if constexpr ((kScore & kBias) != 0) {
-                                    x0 = fmaf(x0, m4, fmaf(-slope2, fabsf(pq.x - pk), N.x));
-                                    x1 = fmaf(x1, m4, fmaf(-slope2, fabsf(pq.y - pk), N.y));
-                                    x2 = fmaf(x2, m4, fmaf(-slope2, fabsf(pq.z - pk), N.z));
-                                    x3 = fmaf(x3, m4, fmaf(-slope2, fabsf(pq.w - pk), N.w));
-                                } else {
-                                    fma2(x0, x1, splat2(m4), pair2(N.x, N.y), x0, x1);
-                                    fma2(x2, x3, splat2(m4), pair2(N.z, N.w), x2, x3);
-                                }
-                                float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
-                                if (part) {
-                                    const int4 dq = __ldg(reinterpret_cast<const int4 *>(sc.doc + qi));
-                                    if (!(vk <= pq.x && dq.x == dk)) p0 = 0.f;
-                                    if (!(vk <= pq.y && dq.y == dk)) p1 = 0.f;
-                                    if (!(vk <= pq.z && dq.z == dk)) p2 = 0.f;
-                                    if (!(vk <= pq.w && dq.w == dk)) p3 = 0.f;
-                                }
+                                fma2(x0, x1, splat2(m4), pair2(N.x, N.y), x0, x1);
+                                fma2(x2, x3, splat2(m4), pair2(N.z, N.w), x2, x3);
+                                const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+                                const float4 dl = lds_f4(vec + 256 + 16 * j);
                                 float d0, d1, d2, d3;
                                 mul_sub2(p0, p1, __uint_as_float(dv[q]), __uint_as_float(dv[q + 1]), dl.x, dl.y, d0, d1);
                                 mul_sub2(p2, p3, __uint_as_float(dv[q + 2]), __uint_as_float(dv[q + 3]), dl.z, dl.w, d2, d3);

@@ -31,8 +31,8 @@
 // V: an 8-bit O may be kept for the backward, and a P of 8 bits moves O by about
 // half a step of bf16, enough for every tenth 8-bit code to fall on the other
 // side and Delta with it (dQ off by up to 0.012 in relative norm, 0.0025 so).
-// TMEM columns: S / P of the chains [0, 64) and [64, 128) (hi in a chain's first
-// 32, lo in the second), O [128, 128 + D).
+// TMEM columns: S / P of the chains [0, 64) and [64, 128) (in each 32 of them, hi
+// in the first 16 and lo in the second), O [128, 128 + D).
 #include <cuda.h>
 
 #include "score_tc.cuh"
@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (!__all_sync(0xffffffffu, mbar_wait(bar_p + 8 * s, (i >> 1) & 1, status, kSiteP, abort_flag))) break;
             if (!__all_sync(0xffffffffu, mbar_wait(bar_vf + 8 * s, (i >> 1) & 1, status, kSiteV, abort_flag))) break;
             tc_fence_after();
-            // k-step kk (16 keys): P columns 8 kk, V rows 2048 B (128 descriptor units) further
-            mma_ts4<8, 16, 24, 128, 256, 384>(tO, tmem + 64 * s, bV + 512 * s, idPV, i > 0);
-            mma_ts4<8, 16, 24, 128, 256, 384>(tO, tmem + 64 * s + 32, bV + 512 * s, idPV, 1u);
+            // k-step kk (16 keys): P columns 0, 8, 32, 40, V rows 2048 B (128 descriptor units) further
+            mma_ts4<8, 32, 40, 128, 256, 384>(tO, tmem + 64 * s, bV + 512 * s, idPV, i > 0);
+            mma_ts4<8, 32, 40, 128, 256, 384>(tO, tmem + 64 * s + 16, bV + 512 * s, idPV, 1u);
             mma_commit(bar_ve + 8 * s);
             // S_{i+2} over P_i: the tensor cores run a CTA's products in issue order
             if (i + 2 < nseg) ok = issue_s(i + 2);
@@ -266,26 +266,24 @@ __global__ void __launch_bounds__(kThreads, 2)
             if ((mw >> half) & 1u) {  // the segment is in this query block's selection
                 const bool part = (mw >> (2 + half)) & 1u;
                 const uint32_t meta = sbase + L::kMeta + (i & 3) * L::kMetaSlot;
-                uint32_t sr[2][32];
-                tmem_ld32(tS, sr[0]);
-                tmem_ld32(tS + 32, sr[1]);
-                tmem_wait_ld();
                 uint64_t acc2 = 0;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    logits32<kScore>(sr[q], sc, scale_log2, slope2, pq, dq, meta + 128 * q, meta + 256 + 128 * q,
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {  // 32 keys at a time, P over their own scores
+                    uint32_t sr[32];
+                    tmem_ld32(tS + 32 * q, sr);
+                    tmem_wait_ld();
+                    logits32<kScore>(sr, sc, scale_log2, slope2, pq, dq, meta + 128 * q, meta + 256 + 128 * q,
                                      meta + 512 + 128 * q, part);
                     if (part) {
                         float mx = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            mx = fmax3(mx, __uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
+                        for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
                         seen = seen || mx != -INFINITY;
                     }
                     uint32_t hi[16], lo[16];
-                    split_exp32(sr[q], s2, 0, acc2, hi, lo);
-                    tmem_st16(tS + 16 * q, hi);
-                    tmem_st16(tS + 32 + 16 * q, lo);
+                    split_exp32(sr, s2, 0, acc2, hi, lo);
+                    tmem_st16(tS + 32 * q, hi);
+                    tmem_st16(tS + 32 * q + 16, lo);
                 }
                 seen = seen || !part;
                 l += sum2(acc2);

@@ -129,23 +129,24 @@ __global__ void __launch_bounds__(kThreads) k_score_work(Geo g, const int *__res
     if (lane == 0) work[blockIdx.y * tiles + t] = n;
 }
 
-// Launch order: the tiles with the most segments first, over groups of `heads`
-// sample-heads (one CTA per group and direction).  Masks leave tiles of very
-// different lengths; started last, a long one runs alone at the end.  Tiles of
-// equal length come in no fixed order: no result depends on it but the order in
-// which dQ's partial sums arrive.
+// Launch order of all tiles (one CTA per direction): the ones with the most
+// segments first, or as they are.  Masks leave tiles of very different lengths;
+// started last, a long one runs alone at the end.  Tiles of equal length come in
+// no fixed order: no result depends on it but the order in which dQ's partial
+// sums arrive.
 constexpr int kBins = 1024;
-__global__ void __launch_bounds__(kBins) k_score_order(Geo g, int heads_f, int heads_b, const int *__restrict__ work,
+__global__ void __launch_bounds__(kBins) k_score_order(Geo g, bool sort_f, bool sort_b, const int *__restrict__ work,
                                                        int *__restrict__ order) {
     __shared__ int cursor[kBins];
     __shared__ int sums[kBins / 32];
-    const int heads = blockIdx.y ? heads_b : heads_f;
     const size_t tiles = (size_t)g.batch * g.heads * g.nbmax;
-    const size_t base = (size_t)blockIdx.x * heads * g.nbmax;
-    if (base >= tiles) return;
-    const int n = (int)min((size_t)heads * g.nbmax, tiles - base), tid = threadIdx.x, lane = tid & 31;
-    const int *w = work + blockIdx.y * tiles + base;
-    int *out = order + blockIdx.y * tiles + base;
+    const int n = (int)tiles, tid = threadIdx.x, lane = tid & 31;
+    const int *w = work + blockIdx.y * tiles;
+    int *out = order + blockIdx.y * tiles;
+    if (!(blockIdx.y ? sort_b : sort_f)) {
+        for (int i = tid; i < n; i += kBins) out[i] = w[i] >= 0 ? i : -1;
+        return;
+    }
     auto bin = [](int v) { return kBins - 1 - min(v, kBins - 1); };  // longest first
     cursor[tid] = 0;
     __syncthreads();
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kBins) k_score_order(Geo g, int heads_f, int h
     cursor[tid] = before + x - mine;
     __syncthreads();
     for (int i = tid; i < n; i += kBins)
-        if (w[i] >= 0) out[atomicAdd(&cursor[bin(w[i])], 1)] = (int)(base + i);
+        if (w[i] >= 0) out[atomicAdd(&cursor[bin(w[i])], 1)] = i;
 }
 
 // Rows of padding tokens become zero: what they hold (infinities, NaN) would
@@ -274,14 +275,13 @@ prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
     k_score_work<<<dim3((unsigned)((tiles + kThreads / 32 - 1) / (kThreads / 32)), 2), kThreads, 0, st>>>(
         g, pl.nqt, pl.qt_blk, pl.blk_off, pl.row_ptr, s.row_end, s.col, pl.colT_ptr, s.colT_end, s.rowT, s.work);
     PRISM_CUDA_OK(cudaGetLastError());
-    // all heads together while what the running tiles share stays in L2 (forward: K
-    // and V; backward: the fp32 dQ that every tile adds to), else head by head: 8
-    // heads of 30720 tokens (126 MB each) took 2.41 ms together, 2.13 apart in the
-    // backward, and the same either way in the forward
+    // Sorted while the tail counts more than neighbouring tiles' common blocks in L2:
+    // forward, K and V of all heads within L2 or nearly (8 heads of 30720 tokens, 126
+    // MB: 2.29 -> 2.16 ms); backward, up to eight tiles per SM (3 per SM: 990 -> 828
+    // us; 13 per SM: 2.08 -> 2.41 ms, so not there).
     const int BH = g.batch * g.heads;
-    const double mb = (double)BH * g.N * g.D * 4 / 1e6;
-    const int group_f = mb <= 160 ? BH : 1, group_b = mb <= 80 ? BH : 1;
-    k_score_order<<<dim3(group_f == BH && group_b == BH ? 1 : BH, 2), kBins, 0, st>>>(g, group_f, group_b, s.work, s.order);
+    const bool sort_f = (double)BH * g.N * g.D * 4 <= 160e6, sort_b = (long long)BH * (g.N / 128) <= 8 * 148;
+    k_score_order<<<dim3(1, 2), kBins, 0, st>>>(g, sort_f, sort_b, s.work, s.order);
     PRISM_CUDA_OK(cudaGetLastError());
     if (s.has_doc) {
         const prism_status z = launch_zero_padding(pl, st);
