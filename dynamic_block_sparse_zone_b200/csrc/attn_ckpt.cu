@@ -104,12 +104,14 @@ prism_status launch_regather_ckpt(Plan &pl, const prism_attn_ckpt &c, cudaStream
             pl.Kbar);
     }
     PRISM_CUDA_OK(cudaGetLastError());
-    return pl.score.set && pl.score.has_doc ? launch_zero_padding(pl, st) : PRISM_OK;
+    pl.score.zeroed = false;
+    return PRISM_OK;
 }
 
 prism_status launch_attn_bwd_ckpt(Plan &pl, const prism_attn_ckpt &c, const void *dO, void *dQ, void *dK, void *dV,
                                   bool scored, cudaStream_t st) {
     prism_status s = launch_regather_ckpt(pl, c, st);
+    if (s == PRISM_OK && scored) s = launch_zero_padding(pl, st);
     if (s != PRISM_OK) return s;
     const Geo &g = pl.g;
     k_restore_lse<<<dim3((g.N + 255) / 256, g.batch * g.heads), 256, 0, st>>>(g, pl.perm, c.lse, pl.nlse_p);

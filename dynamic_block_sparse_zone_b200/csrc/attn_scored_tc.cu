@@ -402,8 +402,10 @@ static prism_status run_any(Plan &pl, void *O, float *lse, cudaStream_t st) {
 }
 
 prism_status launch_attn_fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t st) {
+    prism_status s = launch_zero_padding(pl, st);
+    if (s != PRISM_OK) return s;
     PRISM_CUDA_OK(cudaMemsetAsync(pl.score.redo, 0, sizeof(int), st));
-    const prism_status s = pl.g.D == 64 ? run_any<64>(pl, O, lse, st) : run_any<128>(pl, O, lse, st);
+    s = pl.g.D == 64 ? run_any<64>(pl, O, lse, st) : run_any<128>(pl, O, lse, st);
     return s == PRISM_OK ? launch_attn_fwd_scored_redo(pl, O, lse, st) : s;
 }
 

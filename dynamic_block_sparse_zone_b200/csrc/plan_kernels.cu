@@ -1071,7 +1071,7 @@ static void launch_permute_pool(Plan &pl, const __nv_bfloat16 *Q, const __nv_bfl
 static prism_status launch_gather_select(Plan &pl, const __nv_bfloat16 *Q, const __nv_bfloat16 *K,
                                         const __nv_bfloat16 *V, cudaStream_t st) {
     const Geo &g = pl.g;
-    pl.score.set = false;  // its order and selection belong to the previous build
+    pl.score.set = pl.score.zeroed = false;  // the scores' order and selection belong to the previous build
     launch_permute_pool(pl, Q, K, V, st);
     PRISM_CUDA_OK(cudaGetLastError());
     const size_t rows = (size_t)g.batch * g.heads * g.nbmax;
@@ -1129,7 +1129,8 @@ prism_status launch_regather(Plan &pl, const void *Qv, const void *Kv, const voi
     launch_permute_pool(pl, static_cast<const __nv_bfloat16 *>(Qv), static_cast<const __nv_bfloat16 *>(Kv),
                         static_cast<const __nv_bfloat16 *>(Vv), st);
     PRISM_CUDA_OK(cudaGetLastError());
-    return pl.score.set && pl.score.has_doc ? launch_zero_padding(pl, st) : PRISM_OK;
+    pl.score.zeroed = false;
+    return PRISM_OK;
 }
 
 // Zone statistics and volume / shape decisions alone, on caller-provided

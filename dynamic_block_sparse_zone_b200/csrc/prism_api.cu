@@ -464,8 +464,9 @@ prism_status prism_plan_set_score(prism_plan *plan, const prism_score *score, vo
     prism_status s = device_guard(plan->pl);
     if (s != PRISM_OK) return s;
     if (!plan->pl.built) return fail(PRISM_ERR_STATE, "prism_plan_set_score needs a built plan");
-    plan->pl.have_fwd = 0;
-    return set_score(plan->pl, *score, static_cast<cudaStream_t>(stream));
+    s = set_score(plan->pl, *score, static_cast<cudaStream_t>(stream));
+    if (s == PRISM_OK) plan->pl.have_fwd = 0;
+    return s;
 }
 
 prism_status prism_attn_fwd_scored(prism_plan *plan, void *O, float *lse, void *stream) {

@@ -49,6 +49,7 @@ struct BlockRange {  // of a block's tokens that are not padding
 struct Score {
     bool set;               // valid for the plan's current build
     bool has_bias, has_doc;
+    bool zeroed;            // a scored forward has zeroed padding rows of the current Qp, Kp, Vp
     float cap;              // 0: none
     float *slopes;          // [heads]
     float *pos;             // [batch][N] position of each token

@@ -174,17 +174,21 @@ __global__ void __launch_bounds__(kBins) k_score_order(Geo g, bool sort_f, bool 
 }
 
 // Rows of padding tokens become zero: what they hold (infinities, NaN) would
-// reach other rows through products with P = 0.
+// reach other rows through products with P = 0.  A thread looks at one token;
+// CTAs without padding are done then.
 __global__ void __launch_bounds__(kThreads) k_zero_padding(Geo g, const int *__restrict__ doc, __nv_bfloat16 *__restrict__ Qp,
                                                            __nv_bfloat16 *__restrict__ Kp, __nv_bfloat16 *__restrict__ Vp) {
-    const int b = blockIdx.y, n = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (n >= g.N || doc[(size_t)b * g.N + n] >= 0) return;
+    const int b = blockIdx.y, n0 = blockIdx.x * kThreads + (threadIdx.x & ~31), lane = threadIdx.x & 31;
+    const bool pad = n0 + lane < g.N && doc[(size_t)b * g.N + n0 + lane] < 0;
     const int per = g.D / 8;
-    for (int i = lane; i < g.heads * per; i += 32) {
-        const size_t at = (((size_t)b * g.heads + i / per) * g.N + n) * g.D + i % per * 8;
-        *reinterpret_cast<uint4 *>(Qp + at) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(Kp + at) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(Vp + at) = make_uint4(0, 0, 0, 0);
+    for (unsigned left = __ballot_sync(0xffffffffu, pad); left; left &= left - 1) {
+        const int n = n0 + __ffs(left) - 1;
+        for (int i = lane; i < g.heads * per; i += 32) {
+            const size_t at = (((size_t)b * g.heads + i / per) * g.N + n) * g.D + i % per * 8;
+            *reinterpret_cast<uint4 *>(Qp + at) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(Kp + at) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(Vp + at) = make_uint4(0, 0, 0, 0);
+        }
     }
 }
 
@@ -227,10 +231,13 @@ void release_score(Plan &pl) {
     pl.score.set = false;
 }
 
+// Before every scored pass over the plan's copies (not once for all: a captured
+// forward may be replayed behind an update that was not captured).
 prism_status launch_zero_padding(Plan &pl, cudaStream_t st) {
     const Geo &g = pl.g;
-    k_zero_padding<<<dim3((g.N + kThreads / 32 - 1) / (kThreads / 32), g.batch), kThreads, 0, st>>>(g, pl.score.doc, pl.Qp,
-                                                                                                  pl.Kp, pl.Vp);
+    if (!pl.score.has_doc) return PRISM_OK;
+    pl.score.zeroed = true;
+    k_zero_padding<<<dim3((g.N + kThreads - 1) / kThreads, g.batch), kThreads, 0, st>>>(g, pl.score.doc, pl.Qp, pl.Kp, pl.Vp);
     PRISM_CUDA_OK(cudaGetLastError());
     return PRISM_OK;
 }
@@ -238,6 +245,9 @@ prism_status launch_zero_padding(Plan &pl, cudaStream_t st) {
 prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
     const Geo &g = pl.g;
     Score &s = pl.score;
+    if (s.zeroed)
+        return fail(PRISM_ERR_STATE, "a scored forward has zeroed padding tokens in the plan's Q, K, V: bring them in again "
+                                     "(build or update_qkv) before other scores");
     s.set = false;
     if (!s.rowT) {
         cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -283,10 +293,6 @@ prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
     const bool sort_f = (double)BH * g.N * g.D * 4 <= 160e6, sort_b = (long long)BH * (g.N / 128) <= 8 * 148;
     k_score_order<<<dim3(1, 2), kBins, 0, st>>>(g, sort_f, sort_b, s.work, s.order);
     PRISM_CUDA_OK(cudaGetLastError());
-    if (s.has_doc) {
-        const prism_status z = launch_zero_padding(pl, st);
-        if (z != PRISM_OK) return z;
-    }
     s.set = true;
     return PRISM_OK;
 }

@@ -258,14 +258,17 @@ PRISM_API prism_status prism_attn_bwd(prism_plan *plan, const void *O, const voi
  *   prefix  device fp32 [batch]; keys at positions below it are visible to
  *           every query of their clip; NULL: none (needs causal)
  * prism_plan_set_score copies what it is given (the arrays may be freed once
- * the work on `stream` is done), removes the hidden block pairs from its own
- * copy of the selection, and zeroes the rows of padding tokens in the plan's
- * copies of Q, K and V (as do later prism_plan_update_qkv calls), so that what
- * padding holds reaches nothing; values of visible tokens must be finite.  It
- * belongs to the plan's current build: every build drops it.  The first call on
- * a plan allocates (about 8 bytes per selectable block pair, 12 per token and 2 per value of O;
- * PRISM_ERR_STATE while `stream` is being captured); it forgets the last
- * forward.  PRISM_ERR_STATE before a build.                                 */
+ * the work on `stream` is done) and removes the hidden block pairs from its own
+ * copy of the selection.  It belongs to the plan's current build: every build
+ * drops it, prism_plan_update_qkv keeps it.  It forgets the last forward.  The
+ * first call on a plan allocates (about 8 bytes per selectable block pair, 12
+ * per token and 2 per value of O; PRISM_ERR_STATE while `stream` is being
+ * captured).
+ * With doc, a scored pass first zeroes the rows of padding tokens in the plan's
+ * copies of Q, K and V, so that what padding holds reaches nothing; values of
+ * visible tokens must be finite.  From then on until the next build or update
+ * unscored passes see those zeros, and another prism_plan_set_score is refused.
+ * PRISM_ERR_STATE in that case and before a build.                           */
 typedef struct prism_score {
     float cap;
     const float *slopes, *pos;

@@ -192,6 +192,7 @@ def test_rows_without_a_key(P):
     c = Case(P, 16, 16, 8, 2, 64, top_k=1, frac=0.01, causal=True, clips=5, padding=2, seed=3)
     _, empty = c.check()
     assert empty > 1000
+    c.plan.update_qkv(c.Q, c.K, c.V)
     c.plan.set_score(doc=torch.full((1, c.N), -1, dtype=torch.int32, device="cuda"))  # nothing but padding
     c.doc, c.causal = torch.full((1, c.N), -1, dtype=torch.int32, device="cuda"), False
     _, empty = c.check()
@@ -219,6 +220,41 @@ def test_what_padding_holds_reaches_nothing(P):
 
 
 @pytest.mark.gpu
+def test_other_documents_for_the_same_tokens(P):
+    """Tokens that were padding under one score are themselves again under the next: the zeros that a scored forward
+    writes over padding must not outlive it, so new scores need the tensors brought in again."""
+    c = Case(P, 16, 16, 8, 2, 64, clips=2, padding=6, seed=16)
+    c.plan.set_score(doc=c.doc)          # twice without a forward between them: nothing is zeroed yet
+    c.run()
+    with pytest.raises(P.PrismError, match="zeroed padding"):
+        c.plan.set_score(causal=True)
+    c.run()                              # the refused call has changed nothing
+    c.plan.update_qkv(c.Q, c.K, c.V)
+    c.doc, c.causal = None, True
+    c.plan.set_score(causal=True)
+    c.check()
+    c.plan.close()
+
+
+@pytest.mark.gpu
+def test_a_captured_forward_behind_an_eager_update(P):
+    c = Case(P, 16, 16, 8, 2, 64, clips=2, padding=4, seed=17)
+    want = c.run(backward=False)
+    out = torch.empty_like(c.Q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.plan.fwd(out, scored=True, want_lse=False)
+    pad = c.doc[0] < 0
+    for x in (c.Q, c.K, c.V):
+        x[0, pad] = math.nan
+    c.plan.update_qkv(c.Q, c.K, c.V)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want["O"])
+    c.plan.close()
+
+
+@pytest.mark.gpu
 def test_large_logits_and_far_positions(P):
     for kw in (dict(gain=12.0, cap=0.01), dict(gain=12.0, cap=1e5), dict(gain=12.0, slope=40.0), dict(gain=40.0, cap=50.0)):
         c = Case(P, 16, 8, 16, 2, 64, seed=5, **kw)
@@ -230,6 +266,23 @@ def test_large_logits_and_far_positions(P):
             assert ((O[0, :, h].double() - ref["O"]).abs() <= err["O"] + slack * 8).all(), kw
             assert (lse[0, h].double() - ref["lse"]).abs().max() < 2 * slack, kw
         c.plan.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift", [-70.0, 0.0, 70.0])
+def test_rows_far_from_the_fixed_reference(P, shift):
+    """Logits around +-70: sums of exponentials far outside fp32's middle range, with masks and gradients.  The shift is
+    one that no row sees: K gets a component along a direction in which every query has the same extent."""
+    c = Case(P, 16, 8, 16, 2, 64, clips=2, causal=True, seed=18)
+    c.Q[..., 0] = 8.0
+    c.K[..., 0] = shift          # adds 8 shift / sqrt(64) = shift to every logit
+    c.plan.update_qkv(c.Q, c.K, c.V)
+    c.check()
+    # one tile's rows out of range beside others in range
+    c.K[:, : c.N // 2, :, 0] = 0.0
+    c.plan.update_qkv(c.Q, c.K, c.V)
+    c.check()
+    c.plan.close()
 
 
 @pytest.mark.gpu
