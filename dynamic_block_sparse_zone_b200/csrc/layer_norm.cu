@@ -340,7 +340,12 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_fwd(Fwd
         fetch(0);
     }
     f2 gw[kKeep ? NV : 1][VP], bw[kKeep ? NV : 1][VP];
-    f2 *wsm = reinterpret_cast<f2 *>(slots + (kRing ? kS * NP * blockDim.x : 0));  // [2][nvec][VP]
+    // [gamma, beta][VP / 2][nvec] quadruples (VEC = 2: [gamma, beta][nvec] pairs): neighbouring
+    // lanes read neighbouring 16 bytes, without bank conflicts
+    f2 *wsm = reinterpret_cast<f2 *>(slots + (kRing ? kS * NP * blockDim.x : 0));
+    auto weight_slot = [&](int which, int v, int e) {
+        return VEC == 2 ? which * a.nvec + v : ((which * (VP / 2) + e / 2) * a.nvec + v) * 2 + (e & 1);
+    };
     if constexpr (kKeep) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -353,10 +358,10 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_fwd(Fwd
             f2 u[VP];
             load_weights<VEC>(a.gamma, a.wdt, v * VEC, a.C, a.wvec, 1.f, u);
 #pragma unroll
-            for (int e = 0; e < VP; ++e) wsm[v * VP + e] = u[e];
+            for (int e = 0; e < VP; ++e) wsm[weight_slot(0, v, e)] = u[e];
             load_weights<VEC>(a.beta, a.wdt, v * VEC, a.C, a.wvec, 0.f, u);
 #pragma unroll
-            for (int e = 0; e < VP; ++e) wsm[(a.nvec + v) * VP + e] = u[e];
+            for (int e = 0; e < VP; ++e) wsm[weight_slot(1, v, e)] = u[e];
         }
         __syncthreads();
     }
@@ -448,10 +453,24 @@ __global__ void __launch_bounds__(kCta ? 512 : 256, kCta ? 1 : 2) k_norm_fwd(Fwd
                     if (in[i]) {
                         const int v = i * tpr + t;
                         Vec<T, VEC> o;
+                        f2 gs[VP], bs[VP];
+                        if constexpr (!kKeep) {
+                            if constexpr (VEC == 2) {
+                                gs[0] = wsm[weight_slot(0, v, 0)];
+                                bs[0] = wsm[weight_slot(1, v, 0)];
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < VP; e += 2) {
+                                    const ulonglong2 g2 = *reinterpret_cast<const ulonglong2 *>(wsm + weight_slot(0, v, e));
+                                    const ulonglong2 b2 = *reinterpret_cast<const ulonglong2 *>(wsm + weight_slot(1, v, e));
+                                    gs[e] = g2.x, gs[e + 1] = g2.y, bs[e] = b2.x, bs[e + 1] = b2.y;
+                                }
+                            }
+                        }
 #pragma unroll
                         for (int e = 0; e < VP; ++e) {
-                            const f2 g = kKeep ? gw[kKeep ? i : 0][e] : wsm[v * VP + e];
-                            const f2 b = kKeep ? bw[kKeep ? i : 0][e] : wsm[(a.nvec + v) * VP + e];
+                            const f2 g = kKeep ? gw[kKeep ? i : 0][e] : gs[e];
+                            const f2 b = kKeep ? bw[kKeep ? i : 0][e] : bs[e];
                             o.set_pair(e, fma2(x[j * NV + i][e], mul2(g, rs), b));
                         }
                         o.store(yr, v, a.C);
