@@ -47,9 +47,23 @@ prism_status check_rows(const prism_rows *t, const char *name, long long nrows, 
         if (nrows > t->group && t->group_stride < C)
             return fail(PRISM_ERR_INVALID_ARG, "%s: group_stride %lld is less than %d channels", name, t->group_stride, C);
     }
+    // (in doubles: the products below must stay far from 2^63)
+    const double far = t->group > 0 ? (double)(nrows / t->group) * (double)t->group_stride + (double)(t->group - 1) * (double)t->stride
+                                    : (double)nrows * (double)t->stride;
+    if (far > 1e17) return fail(PRISM_ERR_INVALID_ARG, "%s reaches past any address space", name);
     *out = RowPtr{static_cast<char *>(t->data), t->stride * (long long)es, t->group_stride * (long long)es,
                   (unsigned)t->group};
     return PRISM_OK;
+}
+
+// An output's rows are apart when its groups follow one another, or when all
+// groups' k-th rows lie before any group's k+1-th.
+prism_status check_output(const RowPtr &p, const char *name, long long nrows, int C, size_t es) {
+    if (!p.group || nrows <= p.group || p.group == 1) return PRISM_OK;  // evenly spaced, at least C apart
+    const long long row = (long long)C * es, groups = (nrows + p.group - 1) / p.group;
+    if (p.group_stride >= (long long)(p.group - 1) * p.stride + row || p.stride >= (groups - 1) * p.group_stride + row)
+        return PRISM_OK;
+    return fail(PRISM_ERR_INVALID_ARG, "%s: rows of one group reach into another's", name);
 }
 
 // First and one-past-last byte.
@@ -138,6 +152,7 @@ prism_status prism_ckpt_unpack(const prism_ckpt *in, const prism_rows *y, int dt
     TRY(check_size(nrows, channels, dtype));
     TRY(check_ckpt(in, nrows));
     TRY(check_rows(y, "y", nrows, channels, dtype, &py));
+    TRY(check_output(py, "y", nrows, channels, dtype_size(dtype)));
     return launch_ckpt_unpack(*in, py, dtype, nrows, channels, static_cast<cudaStream_t>(stream));
 }
 
@@ -157,6 +172,7 @@ prism_status prism_layer_norm_fwd(const prism_rows *x, const void *gamma, const 
     TRY(check_ptr(gamma, "gamma", dtype_size(weight_dtype)));
     TRY(check_ptr(beta, "beta", dtype_size(weight_dtype)));
     const size_t es = dtype_size(dtype);
+    TRY(check_output(a.y, "y", nrows, channels, es));
     TRY(check_apart(a.x, es, "x", a.y, es, "y", nrows, channels));
     if (ckpt) {
         TRY(check_ckpt(ckpt, nrows));
@@ -201,6 +217,7 @@ prism_status prism_layer_norm_bwd(const prism_rows *x, const prism_ckpt *ckpt, c
     TRY(check_ptr(dgamma, "dgamma", dtype_size(weight_dtype)));
     TRY(check_ptr(dbeta, "dbeta", dtype_size(weight_dtype)));
     const size_t es = dtype_size(dtype);
+    TRY(check_output(a.dx, "dx", nrows, channels, es));
     TRY(check_apart(a.dy, es, "dy", a.dx, es, "dx", nrows, channels));
     if (x) {
         TRY(check_apart(a.x, es, "x", a.dx, es, "dx", nrows, channels));

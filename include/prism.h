@@ -268,6 +268,8 @@ PRISM_API prism_status prism_attn_bwd(prism_plan *plan, const void *O, const voi
  * copies of Q, K and V, so that what padding holds reaches nothing; values of
  * visible tokens must be finite.  From then on until the next build or update
  * unscored passes see those zeros, and another prism_plan_set_score is refused.
+ * (The replay of a captured scored pass does the same unseen by that check:
+ * bring the tensors in again before setting other scores by hand.)
  * PRISM_ERR_STATE in that case and before a build.                           */
 typedef struct prism_score {
     float cap;
@@ -319,7 +321,8 @@ PRISM_API prism_status prism_audio_norms(const void *h, float *a, int batch, int
  * projection has group = heads, stride = head_dim, group_stride =
  * 3 * heads * head_dim.  group > 0 needs rows < 2^31.  data is aligned to the
  * element; 16-byte aligned rows of a multiple of 16 bytes take the fast path.
- * Outputs must not share elements with any other argument (tensors that lie
+ * An output's rows must not share elements, nor an output with any other
+ * argument (PRISM_ERR_INVALID_ARG where rows, x, y, dy, dx, do; tensors that lie
  * in one buffer without sharing elements are fine).                        */
 typedef enum prism_dtype { PRISM_BF16 = 0, PRISM_FP16 = 1, PRISM_FP32 = 2 } prism_dtype;
 typedef struct prism_rows {

@@ -84,6 +84,36 @@ def test_row_arguments_are_checked_on_the_host(P):
     assert fwd(n=0) == 0
 
 
+def test_an_outputs_own_rows_are_checked(P):
+    """Groups of an output that reach into one another are refused, and strides past any address; groups that follow one
+    another or lie between one another's rows are not (what is refused then is the checkpoint's format, so nothing is
+    launched)."""
+    B, lib = _lib(P)
+    A, C, D = 1 << 24, 1 << 30, 1 << 34
+    at = lambda p, stride=64, gs=0, g=0: ctypes.byref(B.prism_rows(p, stride, gs, g))  # noqa: E731  never dereferenced
+    bad_fmt = ctypes.byref(B.prism_ckpt(1 << 20, 1 << 21, 7))
+
+    def fwd(y, x=at(A), n=12, k=bad_fmt):
+        assert lib.prism_layer_norm_fwd(x, None, None, y, 256, 512, k, n, 64, 1e-6, 0, 2, None) == 1
+        return lib.prism_last_error()
+
+    assert b"reach into" in fwd(at(C, 64, 64, 4))         # groups of 4 rows, 64 elements apart
+    assert b"reach into" in fwd(at(C, 128, 64, 4))
+    assert b"reach into" in fwd(at(C, 64, 255, 4))
+    assert b"reach into" in fwd(at(C, 191, 64, 4))        # three groups of 64 between rows 191 apart
+    assert b"format" in fwd(at(C, 192, 64, 4))
+    assert b"format" in fwd(at(C, 64, 256, 4))
+    assert b"format" in fwd(at(C, 64, 64, 1))
+    assert b"format" in fwd(at(C, 64, 64, 4), n=4)        # one group
+    assert b"format" in fwd(at(C, 64, 256, 4), x=at(A, 64, 64, 4))  # an input may repeat rows
+    assert b"address space" in fwd(at(C, 1 << 40), n=1 << 40)
+    assert b"address space" in fwd(at(C, 64, 1 << 40, 4), n=1 << 30)
+    assert lib.prism_layer_norm_bwd(at(A), None, at(C), None, 256, 512, at(D, 64, 64, 4), None, None, None, 0, 12, 64, 0, 2,
+                                    None) == 1 and b"dx" in lib.prism_last_error()
+    good = ctypes.byref(B.prism_ckpt(1 << 20, 1 << 21, 0))
+    assert lib.prism_ckpt_unpack(good, at(D, 64, 64, 4), 0, 12, 64, None) == 1 and b"reach" in lib.prism_last_error()
+
+
 def test_tensors_are_checked_by_the_binding(P):
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
