@@ -16,7 +16,7 @@
 // nothing ties one segment to the next but the sum in O:
 //   - the reference of the exponential is 0, not a running maximum: P and the
 //     sums are floating point, so a row is right as long as its sum lies in
-//     [2^-60, 2^80] (logits up to +-40).  A tile with a row outside is put on a
+//     [2^-30, 2^80] (largest logits of -20 to 55) and O stays finite.  A tile with a row outside is put on a
 //     list and done again by the variant with a running maximum (attn_tc.cu),
 //     launched behind this kernel; the list is empty for ordinary scores;
 //   - segments alternate between two independent chains, each with its own 64
@@ -45,7 +45,7 @@ namespace segtc {
 
 constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 256;
-constexpr float kLeast = 8.67361738e-19f, kMost = 1.20892582e24f;  // 2^-60, 2^80
+constexpr float kLeast = 9.31322575e-10f, kMost = 1.20892582e24f;  // 2^-30, 2^80
 
 template <int D>
 struct Layout {
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         l = sums[rowid] + sums[128 + rowid];
         const int fl = flags[rowid] | flags[128 + rowid];
         if (__any_sync(0xffffffffu, fl & 2)) ok = false;
-        if (ok && nseg > 0)  // the last product P V must have landed
+        if (ok)  // the last product P V must have landed
             ok = __all_sync(0xffffffffu, mbar_wait(bar_o, 0, status, kSiteO, abort_flag));
         if (ok) {
             tc_fence_after();
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int n = q0 + rowid;
             const bool write = rowid < qvalid;
             const int tok = write ? perm[(size_t)b * g.N + n] : 0;
-            if (__any_sync(0xffffffffu, write && !empty && !(l >= kLeast && l <= kMost)) && lane == 0) *put_off = 1;
+            float past = 0.f;  // NaN once an O is past fp32: values near bf16's largest times a large P
             __nv_bfloat16 *dst = O + (((size_t)b * g.N + tok) * g.heads + h) * D + s * (D / 2);
 #pragma unroll 1
             for (int q = 0; q < D / 64; ++q) {
@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int e = 0; e < 16; ++e) {
                     const float o0 = empty ? 0.f : __uint_as_float(orr[2 * e]) * inv;
                     const float o1 = empty ? 0.f : __uint_as_float(orr[2 * e + 1]) * inv;
+                    past = fmaf(o0, 0.f, fmaf(o1, 0.f, past));
                     pw[e] = pack_bf16x2(o0, o1);
                     lw[e] = pack_bf16x2(o0 - __uint_as_float(pw[e] << 16), o1 - __uint_as_float(pw[e] & 0xffff0000u));
                 }
@@ -343,6 +344,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
             }
+            if (__any_sync(0xffffffffu, write && !empty && !(l >= kLeast && l <= kMost && past == 0.f)) && lane == 0)
+                *put_off = 1;
             if (write && s == 0) {
                 const float lse2 = empty ? -INFINITY : __log2f(l);
                 // negated: the backward's exp2 addend; an empty row's is -inf (P = 0)

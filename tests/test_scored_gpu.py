@@ -286,6 +286,25 @@ def test_rows_far_from_the_fixed_reference(P, shift):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shift,power", [(35.0, 90), (50.0, 60), (0.0, 110), (-18.0, -60), (-30.0, -60), (0.0, -60)])
+def test_large_and_small_values(P, shift, power):
+    """V of 2^power under logits around `shift`: their products pass fp32's largest (or fall below its least normal)
+    number where the exponentials are taken as they are, O itself does not.  O is linear in V: the result over 2^power
+    has the bounds of power = 0."""
+    c = Case(P, 16, 8, 16, 2, 64, clips=2, causal=True, seed=21)
+    c.Q[..., 0] = 8.0
+    c.K[..., 0] = shift
+    c.plan.update_qkv(c.Q, c.K, c.V * 2.0 ** power)  # a power of two: nothing is rounded
+    O, _ = c.plan.fwd(scored=True)
+    c.plan.check()
+    for h in range(2):
+        ref, err = c.reference(0, h)
+        off = (O[0, :, h].double() * 2.0 ** -power - ref["O"]).abs()
+        assert (off <= err["O"] + 1e-30).all(), (h, (off - err["O"]).max().item())
+    c.plan.close()
+
+
+@pytest.mark.gpu
 def test_without_scores_it_is_the_sparse_attention(P):
     """No cap, bias or mask: fwd() and bwd() and their scored forms compute the same thing.  The two forwards round P
     against different reference maxima, so they may differ by the sum of their bounds, no more."""
