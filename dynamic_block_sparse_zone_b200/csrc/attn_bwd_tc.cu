@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (issuer) mma_commit(bar_done);  // both groups' products: done counts two commits
         // epilogue: column groups 0, 1 write halves of dK (scaled), 2, 3 halves of dV
-        if (ok && nchunk > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar_done, 0, status, kSiteDone, abort_flag));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_done, 0, status, kSiteDone, abort_flag));
         if (ok) {
             tc_fence_after();
             const int tok = live ? perm[(size_t)b * g.N + k0 + rowid] : 0;
