@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
                         // the same with the logit from cap tanh(S / cap) and the bias, and dS times
-                        // tanh's derivative 1 - tanh^2
+                        // tanh's derivative 1 - tanh^2: in phases over all 16 scores, each without a
+                        // branch and in place, so that a thread's chains run beside one another
                         tmem_wait_ld();
                         bool small = true;
                         if constexpr ((kScore & kCap) != 0) {  // (rows that are not active do not matter)
@@ -371,69 +372,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                             small = __all_sync(0xffffffffu, !act || fmaxf(ma, mb) <= sc.cap_one);
                         }
                         if (act) {
+                            float *x = reinterpret_cast<float *>(sv), *y = reinterpret_cast<float *>(dv);
                             const size_t qi = (size_t)b * g.N + (mw >> 4) + 16 * cq;  // the first query
-                            float vk = 0.f;  // this key's visibility and document
-                            int dk = 0;
-                            if (part) {
-                                vk = __ldg(sc.vis + (size_t)b * g.N + k0 + rowid);
-                                dk = __ldg(sc.doc + (size_t)b * g.N + k0 + rowid);
+                            float m4 = scale_log2, a4 = 0.f;
+                            // y = (dP - Delta) (1 - tanh^2), x = what the logit is linear in
+                            if constexpr ((kScore & kCap) == 0) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const float4 dl = lds_f4(vec + 256 + 16 * j);
+                                    const uint64_t v01 = psub(pair2(y[4 * j], y[4 * j + 1]), pair2(dl.x, dl.y));
+                                    const uint64_t v23 = psub(pair2(y[4 * j + 2], y[4 * j + 3]), pair2(dl.z, dl.w));
+                                    y[4 * j] = plo(v01), y[4 * j + 1] = phi(v01), y[4 * j + 2] = plo(v23), y[4 * j + 3] = phi(v23);
+                                }
+                            } else if (small) {
+                                const uint64_t ku = splat2(sc.cap_u), one = splat2(1.f), neg = splat2(-1.f);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const float4 dl = lds_f4(vec + 256 + 16 * j);
+#pragma unroll
+                                    for (int e = 4 * j; e < 4 * j + 4; e += 2) {
+                                        const uint64_t t = tanh_small2(x[e], x[e + 1], ku);
+                                        const uint64_t d = psub(pair2(y[e], y[e + 1]), e & 2 ? pair2(dl.z, dl.w) : pair2(dl.x, dl.y));
+                                        const uint64_t v = pmul(d, pfma(pmul(t, t), neg, one));
+                                        x[e] = plo(t), x[e + 1] = phi(t), y[e] = plo(v), y[e + 1] = phi(v);
+                                    }
+                                }
+                                m4 = sc.cap_out;
+                            } else {
+                                const uint64_t four = splat2(4.f), neg = splat2(-4.f);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const float4 dl = lds_f4(vec + 256 + 16 * j);
+                                    uint64_t q02, q13;
+                                    logistic4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3], sc.cap_in, q02, q13);
+                                    const uint64_t v02 = pmul(psub(pair2(y[4 * j], y[4 * j + 2]), pair2(dl.x, dl.z)), pmul(q02, pfma(q02, neg, four)));
+                                    const uint64_t v13 = pmul(psub(pair2(y[4 * j + 1], y[4 * j + 3]), pair2(dl.y, dl.w)), pmul(q13, pfma(q13, neg, four)));
+                                    x[4 * j] = plo(q02), x[4 * j + 1] = plo(q13), x[4 * j + 2] = phi(q02), x[4 * j + 3] = phi(q13);
+                                    y[4 * j] = plo(v02), y[4 * j + 1] = plo(v13), y[4 * j + 2] = phi(v02), y[4 * j + 3] = phi(v13);
+                                }
+                                m4 = -2.f * sc.cap_out;
+                                a4 = sc.cap_out;
                             }
+                            // x = the logit less LSE
+                            const uint64_t k2 = splat2(m4);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const int q = 4 * j;
-                                // what is added to the scaled score: -LSE, the bias, -inf where the key is hidden
                                 float4 N = lds_f4(vec + 16 * j);
-                                if ((kScore & kBias) || part) {
+                                if constexpr ((kScore & kBias) != 0) {
                                     const float4 pq = __ldg(reinterpret_cast<const float4 *>(sc.pos + qi) + j);
-                                    if constexpr ((kScore & kBias) != 0) {
-                                        N.x = fmaf(-slope2, fabsf(pq.x - pk), N.x), N.y = fmaf(-slope2, fabsf(pq.y - pk), N.y);
-                                        N.z = fmaf(-slope2, fabsf(pq.z - pk), N.z), N.w = fmaf(-slope2, fabsf(pq.w - pk), N.w);
-                                    }
-                                    if (part) {
-                                        const int4 dq = __ldg(reinterpret_cast<const int4 *>(sc.doc + qi) + j);
-                                        if (!(vk <= pq.x && dq.x == dk)) N.x = -INFINITY;
-                                        if (!(vk <= pq.y && dq.y == dk)) N.y = -INFINITY;
-                                        if (!(vk <= pq.z && dq.z == dk)) N.z = -INFINITY;
-                                        if (!(vk <= pq.w && dq.w == dk)) N.w = -INFINITY;
-                                    }
+                                    N.x = fmaf(-slope2, fabsf(pq.x - pk), N.x), N.y = fmaf(-slope2, fabsf(pq.y - pk), N.y);
+                                    N.z = fmaf(-slope2, fabsf(pq.z - pk), N.z), N.w = fmaf(-slope2, fabsf(pq.w - pk), N.w);
                                 }
-                                float x0 = __uint_as_float(sv[q]), x1 = __uint_as_float(sv[q + 1]);
-                                float x2 = __uint_as_float(sv[q + 2]), x3 = __uint_as_float(sv[q + 3]);
-                                float m4 = scale_log2;
-                                uint64_t g01 = 0, g23 = 0;  // 1 - tanh^2
-                                if constexpr ((kScore & kCap) != 0) {
-                                    if (small) {
-                                        const uint64_t ku = splat2(sc.cap_u), one = splat2(1.f), neg = splat2(-1.f);
-                                        const uint64_t t01 = tanh_small2(x0, x1, ku), t23 = tanh_small2(x2, x3, ku);
-                                        g01 = pfma(pmul(t01, t01), neg, one), g23 = pfma(pmul(t23, t23), neg, one);
-                                        x0 = plo(t01), x1 = phi(t01), x2 = plo(t23), x3 = phi(t23);
-                                        m4 = sc.cap_out;
-                                    } else {
-                                        uint64_t q02, q13;
-                                        logistic4(x0, x1, x2, x3, sc.cap_in, q02, q13);
-                                        x0 = plo(q02), x1 = plo(q13), x2 = phi(q02), x3 = phi(q13);
-                                        const uint64_t q01 = pair2(x0, x1), q23 = pair2(x2, x3);
-                                        const uint64_t four = splat2(4.f), m4q = splat2(-4.f);
-                                        g01 = pmul(q01, pfma(q01, m4q, four)), g23 = pmul(q23, pfma(q23, m4q, four));
-                                        m4 = -2.f * sc.cap_out;
-                                        N.x += sc.cap_out, N.y += sc.cap_out, N.z += sc.cap_out, N.w += sc.cap_out;
-                                    }
-                                }
-                                fma2(x0, x1, splat2(m4), pair2(N.x, N.y), x0, x1);
-                                fma2(x2, x3, splat2(m4), pair2(N.z, N.w), x2, x3);
-                                const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
-                                const float4 dl = lds_f4(vec + 256 + 16 * j);
-                                float d0, d1, d2, d3;
-                                mul_sub2(p0, p1, __uint_as_float(dv[q]), __uint_as_float(dv[q + 1]), dl.x, dl.y, d0, d1);
-                                mul_sub2(p2, p3, __uint_as_float(dv[q + 2]), __uint_as_float(dv[q + 3]), dl.z, dl.w, d2, d3);
-                                if constexpr ((kScore & kCap) != 0) {
-                                    const uint64_t y01 = pmul(pair2(d0, d1), g01), y23 = pmul(pair2(d2, d3), g23);
-                                    d0 = plo(y01), d1 = phi(y01), d2 = plo(y23), d3 = phi(y23);
-                                }
-                                pd[2 * j] = pack_bf16x2(p0, p1);
-                                pd[2 * j + 1] = pack_bf16x2(p2, p3);
-                                pd[8 + 2 * j] = pack_bf16x2(d0, d1);
-                                pd[8 + 2 * j + 1] = pack_bf16x2(d2, d3);
+                                uint64_t n01 = pair2(N.x, N.y), n23 = pair2(N.z, N.w);
+                                if constexpr ((kScore & kCap) != 0) n01 = padd(n01, splat2(a4)), n23 = padd(n23, splat2(a4));
+                                const uint64_t y01 = pfma(pair2(x[4 * j], x[4 * j + 1]), k2, n01);
+                                const uint64_t y23 = pfma(pair2(x[4 * j + 2], x[4 * j + 3]), k2, n23);
+                                x[4 * j] = plo(y01), x[4 * j + 1] = phi(y01), x[4 * j + 2] = plo(y23), x[4 * j + 3] = phi(y23);
+                            }
+                            if (part) hide16(sv, sc, (size_t)b * g.N, (int)(mw >> 4) + 16 * cq, k0 + rowid);
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float p0 = ex2(x[e]), p1 = ex2(x[e + 1]);
+                                const uint64_t v = pmul(pair2(p0, p1), pair2(y[e], y[e + 1]));
+                                pd[e / 2] = pack_bf16x2(p0, p1);
+                                pd[8 + e / 2] = pack_bf16x2(plo(v), phi(v));
                             }
                         } else {
 #pragma unroll
