@@ -315,12 +315,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) {
                 tc_fence_after();
                 const uint32_t mw = mask_s[st];
-                const bool act = live && ((mw >> half) & 1u);
-                const bool part = kEnc && ((mw >> (2 + half)) & 1u);
+                bool act = live && ((mw >> half) & 1u);
+                bool part = kEnc && ((mw >> (2 + half)) & 1u);
                 const uint32_t dsrow = sbase + L::kDS + (c & 1) * 16384 + rowid * 128;
 #pragma unroll 1
                 for (int sub = 0; sub < 2; ++sub) {
                     const int cq = 2 * cg2 + sub;  // 16 query columns [16 cq, 16 cq + 16)
+                    if constexpr (kEnc) {  // (live rows are whole warps: all of this is warp-uniform)
+                        act = live && ((mw >> half) & 1u);
+                        part = act && ((mw >> (2 + half)) & 1u);
+                        if (part) {
+                            const size_t n0 = (size_t)b * g.N;
+                            const float4 qr = __ldg(reinterpret_cast<const float4 *>(sc.qgrp + (n0 + (mw >> 4)) / 16 + cq));
+                            const float4 kr = __ldg(reinterpret_cast<const float4 *>(sc.kgrp + (n0 + k0) / 32 + quad));
+                            const int cls = group_class(qr.x, qr.y, __float_as_int(qr.z), __float_as_int(qr.w), kr.x, kr.y,
+                                                        __float_as_int(kr.z), __float_as_int(kr.w));
+                            act = cls != 0;
+                            part = cls == 2;
+                        }
+                    }
                     const uint32_t tST = tmem + kColST + (c & 1) * 64 + 16 * cq + lane_off;
                     uint32_t sv[16], dv[16];
                     tmem_ld16(tST, sv);

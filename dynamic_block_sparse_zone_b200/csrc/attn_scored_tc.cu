@@ -59,7 +59,7 @@ struct Layout {
     static constexpr uint32_t kNumBars = 2 + 6 * 2 + 4;
     static constexpr uint32_t kWords = kBars + kNumBars * 8;  // tmem slot, abort, put-off flag, -, mask[4]
     static constexpr uint32_t kMeta = (kWords + 32 + 15) & ~15u;
-    static constexpr uint32_t kMetaSlot = 3 * 256;            // positions, visibilities, documents of 64 keys
+    static constexpr uint32_t kMetaSlot = 3 * 256 + 32;       // positions, visibilities, documents of 64 keys, their ranges
     static constexpr uint32_t kExch = kMeta + 4 * kMetaSlot;  // [chain][row] sums, then "has seen a key"
     static constexpr uint32_t kAlloc = kExch + 4 * 512 + 1024;
 };
@@ -156,11 +156,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const size_t n0 = (size_t)b * g.N + wk.r;
                 const uint32_t meta = sbase + L::kMeta + ms * L::kMetaSlot, bm = bar_m + 8 * ms;
                 mask_w[ms] = (uint32_t)wk.mask;  // published by the arrive below
-                mbar_expect_tx(bm, ((kScore & kBias) ? 256 : 0) + (part ? 512 : 0));
+                mbar_expect_tx(bm, ((kScore & kBias) ? 256 : 0) + (part ? 512 + 32 : 0));
                 if (kScore & kBias) bulk_load(meta, sc.pos + n0, 256, bm);
                 if (part) {
                     bulk_load(meta + 256, sc.vis + n0, 256, bm);
                     bulk_load(meta + 512, sc.doc + n0, 256, bm);
+                    bulk_load(meta + 768, sc.kgrp + n0 / 32, 32, bm);
                 }
                 mbar_expect_tx(bar_kf + 8 * s, 64 * D * 2);
                 for (int hf = 0; hf < L::kHalves; ++hf)
@@ -254,6 +255,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             dq = sc.doc[(size_t)b * g.N + q0 + rowid];
         }
         if (kScore & kBias) slope2 = sc.slopes[h] * 1.4426950408889634f;
+        // of the warp's 32 queries (all or none of them are valid)
+        GroupRange qr{INFINITY, -INFINITY, -2, -2};
+        if (quad * 32 < qvalid) {
+            const GroupRange *p = sc.qgrp + ((size_t)b * g.N + q0 + quad * 32) / 16;
+            const GroupRange r0 = p[0], r1 = p[1];
+            qr = GroupRange{fminf(r0.lo, r1.lo), fmaxf(r0.hi, r1.hi), min(r0.dmin, r1.dmin), max(r0.dmax, r1.dmax)};
+        }
         const uint64_t s2 = splat2((kScore & (kCap | kBias)) ? 1.0f : scale_log2);
         float l = 0.f;
         bool ok = true, seen = false;  // seen: a key is visible to this row
@@ -270,11 +278,24 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
                 for (int q = 0; q < 2; ++q) {  // 32 keys at a time, P over their own scores
                     uint32_t sr[32];
+                    int cls = 1;
+                    if (part) {
+                        const float4 kr = lds_f4(meta + 768 + 16 * q);
+                        cls = group_class(qr.lo, qr.hi, qr.dmin, qr.dmax, kr.x, kr.y, __float_as_int(kr.z),
+                                          __float_as_int(kr.w));
+                    }
+                    if (cls == 0) {  // none of these queries sees any of these keys
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) sr[e] = 0u;
+                        tmem_st32(tS + 32 * q, sr);
+                        continue;
+                    }
                     tmem_ld32(tS + 32 * q, sr);
                     tmem_wait_ld();
                     logits32<kScore>(sr, sc, scale_log2, slope2, pq, dq, meta + 128 * q, meta + 256 + 128 * q,
-                                     meta + 512 + 128 * q, part);
-                    if (part) {
+                                     meta + 512 + 128 * q, cls == 2);
+                    seen = seen || cls == 1;
+                    if (cls == 2) {
                         float mx = -INFINITY;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
@@ -285,7 +306,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                     tmem_st16(tS + 32 * q, hi);
                     tmem_st16(tS + 32 * q + 16, lo);
                 }
-                seen = seen || !part;
                 l += sum2(acc2);
             } else {
                 uint32_t z[32];

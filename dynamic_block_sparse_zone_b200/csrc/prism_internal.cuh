@@ -46,6 +46,13 @@ struct BlockRange {  // of a block's tokens that are not padding
     int dmin, dmax;    // documents
     int tokens, pads;  // how many tokens, how many of padding
 };
+// Of the 16 tokens of a query group or the 32 of a key group: positions of its
+// queries (padding left out), or positions from which its keys are visible, and
+// documents (padding: -1).  16 bytes, read as one.
+struct alignas(16) GroupRange {
+    float lo, hi;
+    int dmin, dmax;
+};
 struct Score {
     bool set;               // valid for the plan's current build
     bool has_bias, has_doc;
@@ -56,6 +63,8 @@ struct Score {
     float *vis;             // [batch][N] a key is visible to queries at positions >= this (+inf: padding)
     int *doc;               // [batch][N] document, -1: padding
     BlockRange *blk;        // [batch][nbmax]
+    GroupRange *qgrp;       // [batch][N / 16]
+    GroupRange *kgrp;       // [batch][N / 32]
     __nv_bfloat16 *Olo;     // [batch*heads][N][D] what the last scored forward's bf16 O leaves of its fp32 O
     int *row_end, *col;     // the CSR again, rows starting at row_ptr: 2 j + (partly visible), see list_block
     int *colT_end, *rowT;   // and its transpose, columns starting at colT_ptr
@@ -177,6 +186,7 @@ struct ScoreArgs {
     int *redo;                  // the forward's tiles put off (Score::redo)
     const float *pos, *vis;
     const int *doc;
+    const GroupRange *qgrp, *kgrp;
     const float *slopes;
     __nv_bfloat16 *Olo;         // written by the forward
     float cap_u;                // 1 / (sqrt(D) cap)

@@ -21,17 +21,31 @@ __global__ void __launch_bounds__(kThreads) k_score_tokens(Geo g, const int *__r
                                                            bool causal, const float *__restrict__ prefix,
                                                            const float *__restrict__ slopes,
                                                            float *__restrict__ pos_p, float *__restrict__ vis_p,
-                                                           int *__restrict__ doc_p, float *__restrict__ slopes_p) {
+                                                           int *__restrict__ doc_p, float *__restrict__ slopes_p,
+                                                           GroupRange *__restrict__ qgrp, GroupRange *__restrict__ kgrp) {
     const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
     if (slopes && i < (size_t)g.heads) slopes_p[i] = slopes[i];
-    if (i >= (size_t)g.batch * g.N) return;
+    if (i >= (size_t)g.batch * g.N) return;  // N is a multiple of 64: whole warps
     const int b = (int)(i / g.N), tok = perm[i];
     const size_t src = (size_t)b * g.N + tok;
     const float p = pos ? pos[src] : (float)(tok / (g.H * g.W));
     const int d = doc ? doc[src] : 0;
     pos_p[i] = p;
     doc_p[i] = d < 0 ? -1 : d;
-    vis_p[i] = d < 0 ? INFINITY : !causal || (prefix && p < prefix[b]) ? -INFINITY : p;
+    const float v = d < 0 ? INFINITY : !causal || (prefix && p < prefix[b]) ? -INFINITY : p;
+    vis_p[i] = v;
+    GroupRange q{d < 0 ? INFINITY : p, d < 0 ? -INFINITY : p, max(d, -1), max(d, -1)}, k{v, v, q.dmin, q.dmax};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        if (o == 16 && (i & 15) == 0) qgrp[i / 16] = q;
+        q.lo = fminf(q.lo, __shfl_xor_sync(0xffffffffu, q.lo, o));
+        q.hi = fmaxf(q.hi, __shfl_xor_sync(0xffffffffu, q.hi, o));
+        k.lo = fminf(k.lo, __shfl_xor_sync(0xffffffffu, k.lo, o));
+        k.hi = fmaxf(k.hi, __shfl_xor_sync(0xffffffffu, k.hi, o));
+        q.dmin = min(q.dmin, __shfl_xor_sync(0xffffffffu, q.dmin, o));
+        q.dmax = max(q.dmax, __shfl_xor_sync(0xffffffffu, q.dmax, o));
+    }
+    if ((i & 31) == 0) kgrp[i / 32] = GroupRange{k.lo, k.hi, q.dmin, q.dmax};
 }
 
 // One warp per block.
@@ -196,6 +210,7 @@ struct Buf {
     void **p;
     size_t bytes;
 };
+constexpr int kBuffers = 16;
 int buffers(Plan &pl, Buf *out) {
     const Geo &g = pl.g;
     Score &s = pl.score;
@@ -207,6 +222,8 @@ int buffers(Plan &pl, Buf *out) {
     out[n++] = {(void **)&s.vis, tokens * sizeof(float)};
     out[n++] = {(void **)&s.doc, tokens * sizeof(int)};
     out[n++] = {(void **)&s.blk, (size_t)g.batch * g.nbmax * sizeof(BlockRange)};
+    out[n++] = {(void **)&s.qgrp, tokens / 16 * sizeof(GroupRange)};
+    out[n++] = {(void **)&s.kgrp, tokens / 32 * sizeof(GroupRange)};
     out[n++] = {(void **)&s.row_end, lists * sizeof(int)};
     out[n++] = {(void **)&s.colT_end, lists * sizeof(int)};
     out[n++] = {(void **)&s.order, 2 * lists * sizeof(int)};
@@ -221,7 +238,7 @@ int buffers(Plan &pl, Buf *out) {
 }  // namespace
 
 void release_score(Plan &pl) {
-    Buf b[16];
+    Buf b[kBuffers];
     const int n = buffers(pl, b);
     for (int k = 0; k < n; ++k)
         if (*b[k].p) {
@@ -254,7 +271,7 @@ prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
         PRISM_CUDA_OK(cudaStreamIsCapturing(st, &cap));
         if (cap != cudaStreamCaptureStatusNone)
             return fail(PRISM_ERR_STATE, "a plan's first prism_plan_set_score allocates: make it before the capture");
-        Buf b[16];
+        Buf b[kBuffers];
         const int n = buffers(pl, b);
         for (int k = 0; k < n; ++k) {
             const cudaError_t e = cudaMalloc(b[k].p, b[k].bytes);
@@ -272,7 +289,7 @@ prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
     size_t n = (size_t)g.batch * g.N;
     if ((size_t)g.heads > n) n = g.heads;
     k_score_tokens<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(
-        g, pl.perm, in.pos, in.doc, in.causal != 0, in.prefix, in.slopes, s.pos, s.vis, s.doc, s.slopes);
+        g, pl.perm, in.pos, in.doc, in.causal != 0, in.prefix, in.slopes, s.pos, s.vis, s.doc, s.slopes, s.qgrp, s.kgrp);
     PRISM_CUDA_OK(cudaGetLastError());
     k_score_blocks<<<dim3((g.nbmax + kThreads / 32 - 1) / (kThreads / 32), g.batch), kThreads, 0, st>>>(
         g, pl.nb, pl.blk_off, s.pos, s.vis, s.doc, s.blk);
@@ -305,6 +322,8 @@ ScoreArgs score_args(const Plan &pl, bool backward) {
     a.pos = s.pos;
     a.vis = s.vis;
     a.doc = s.doc;
+    a.qgrp = s.qgrp;
+    a.kgrp = s.kgrp;
     a.slopes = s.slopes;
     a.Olo = s.Olo;
     a.redo = s.redo;

@@ -70,6 +70,13 @@ __device__ __forceinline__ void tile_blocks(int code, int &j1, int &j2) {
 // its token pairs and 2 j for one it leaves whole; a plain list holds j.
 template <bool kEnc>
 __device__ __forceinline__ int list_block(int v) { return kEnc ? v >> 1 : v; }
+// What a group of queries sees of a group of keys: 0 nothing, 1 everything, 2 to
+// be found out token by token.
+__device__ __forceinline__ int group_class(float qlo, float qhi, int qdmin, int qdmax, float klo, float khi, int kdmin,
+                                           int kdmax) {
+    if (qdmax < kdmin || kdmax < qdmin || klo > qhi) return 0;
+    return qdmin == qdmax && kdmin == kdmax && qdmin == kdmin && khi <= qlo ? 1 : 2;
+}
 // Is j in the ascending list L[0..n)?
 template <bool kEnc>
 __device__ __forceinline__ bool sorted_has(const int *L, int n, int j) {
