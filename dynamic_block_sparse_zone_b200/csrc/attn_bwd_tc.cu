@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int u2_end = shared_tile ? (kEnc ? sc.list_end[colid + 1] : colT_ptr[colid + 2]) : 0;
 
     // 64-row query chunks of the column(s)
-    const int nchunk = union_segments<kEnc>(rowT + u_begin, u_end - u_begin, rowT + u2_begin, u2_end - u2_begin, bo, lane);
+    const int own = kEnc ? (k0 - bo[jblk]) >> 7 : 0;  // which 128 rows of its block the tile is
+    const int nchunk = union_segments<kEnc>(rowT + u_begin, u_end - u_begin, rowT + u2_begin, u2_end - u2_begin, bo, own, lane);
 
     const uint32_t bar_kv = sbase + L::kBars;
     const uint32_t bar_qf = bar_kv + 8, bar_qe = bar_qf + 8 * kStages, bar_sf = bar_qe + 8 * kStages;
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 rowbase + k0 + rh * 64);
                 }
             SegWalk<kEnc> wk;
-            wk.init(u_begin, u_end, u2_begin, u2_end, rowT, bo);
+            wk.init(u_begin, u_end, u2_begin, u2_end, rowT, bo, own);
             int issued = 0;
             for (int c = 0; c < nchunk; ++c) {
                 const int st = c % kStages;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const bool leader = (warp == 2 + kSoftmaxWarps && lane == 0);
         SegWalk<kEnc> wk;
-        wk.init(u_begin, u_end, u2_begin, u2_end, rowT, bo);
+        wk.init(u_begin, u_end, u2_begin, u2_end, rowT, bo, own);
         for (int c = 0; c < nchunk; ++c) {
             if (!__all_sync(0xffffffffu,
                             mbar_wait(bar_df + 8 * (c & 1), (c >> 1) & 1, status, kSiteDQFull, abort_flag))) {

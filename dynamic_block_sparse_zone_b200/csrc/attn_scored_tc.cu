@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int c_begin = row_ptr[crow], c_end = sc.list_end[crow];
     // the second query block's selection (empty unless the tile is shared)
     const int c2_begin = shared_tile ? row_ptr[crow + 1] : 0, c2_end = shared_tile ? sc.list_end[crow + 1] : 0;
-    const int nseg = union_segments<true>(col + c_begin, c_end - c_begin, col + c2_begin, c2_end - c2_begin, bo, lane);
+    const int own = (q0 - bo[iblk]) >> 7;  // which 128 rows of its block the tile is
+    const int nseg = union_segments<true>(col + c_begin, c_end - c_begin, col + c2_begin, c2_end - c2_begin, bo, own, lane);
 
     const uint32_t bar_q = sbase + L::kBars, bar_o = bar_q + 8;
     const uint32_t bar_kf = bar_q + 16, bar_ke = bar_kf + 16, bar_vf = bar_ke + 16, bar_ve = bar_vf + 16;
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     tma_load_2d(sbase + L::kQ + hf * L::kTileBytes + rh * 8192, &tmQ, bar_q, hf * 64,
                                 rowbase + q0 + rh * 64);
             SegWalk<true> wk;
-            wk.init(c_begin, c_end, c2_begin, c2_end, col, bo);
+            wk.init(c_begin, c_end, c2_begin, c2_end, col, bo, own);
             int kissued = 0, vissued = 0;
             // K of segment i and its keys' data, once S_{i-2} has read the K buffer.  The
             // data's slot is free then too: S_{i-2} was issued behind P_{i-4} V_{i-4}, so

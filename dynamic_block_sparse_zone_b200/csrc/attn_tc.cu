@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
     const int c2_end = shared_tile ? (kEnc ? sc.list_end[crow + 1] : row_ptr[crow + 2]) : 0;
 
     // number of 64-row key segments of the selection (every warp computes it)
-    const int nseg = union_segments<kEnc>(col + c_begin, c_end - c_begin, col + c2_begin, c2_end - c2_begin, bo, lane);
+    const int own = kEnc ? (q0 - bo[iblk]) >> 7 : 0;  // which 128 rows of its block the tile is
+    const int nseg = union_segments<kEnc>(col + c_begin, c_end - c_begin, col + c2_begin, c2_end - c2_begin, bo, own, lane);
     const int nchunk = (nseg + 1) >> 1;
     // Taylor variant: pooled chunks follow the selected ones
     const int nbb = kTaylor ? nbv[b] : 0;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
                     tma_load_2d(sbase + L::kQ + hf * L::kTileBytes + rh * 8192, &tmQ, bar_q, hf * 64,
                                 rowbase + q0 + rh * 64);
             SegWalk<kEnc> wk;
-            wk.init(c_begin, c_end, c2_begin, c2_end, col, bo);
+            wk.init(c_begin, c_end, c2_begin, c2_end, col, bo, own);
             int kissued = 0, vissued = 0, missued = 0;
             for (int c = 0; c < nchunk_all; ++c) {
                 const bool pooled = kTaylor && c >= nchunk;

@@ -65,8 +65,9 @@ struct Score {
     BlockRange *blk;        // [batch][nbmax]
     GroupRange *qgrp;       // [batch][N / 16]
     GroupRange *kgrp;       // [batch][N / 32]
+    GroupRange *seg;        // [2][batch][N / 64]: of 64 queries, of 64 keys
     __nv_bfloat16 *Olo;     // [batch*heads][N][D] what the last scored forward's bf16 O leaves of its fp32 O
-    int *row_end, *col;     // the CSR again, rows starting at row_ptr: 2 j + (partly visible), see list_block
+    int *row_end, *col;     // the CSR again, rows starting at row_ptr: with what is seen of each block, see list_block
     int *colT_end, *rowT;   // and its transpose, columns starting at colT_ptr
     int *order;             // [2][batch*heads*nbmax] sample*head * nbmax + tile in launch order, the forward's query
                             // tiles and the backward's key tiles; -1: none

@@ -66,10 +66,13 @@ __device__ __forceinline__ void tile_blocks(int code, int &j1, int &j2) {
     j1 = code < 0 ? ~code : code;
     j2 = code < 0 ? j1 + 1 : -1;
 }
-// A scored list (kEnc) holds 2 j + 1 for a block pair whose mask hides some of
-// its token pairs and 2 j for one it leaves whole; a plain list holds j.
+// A plain list holds j.  A scored list (kEnc) holds j << 9 | seen << 1 | partly:
+// bit 4 t + s of seen says whether anything is visible between the 128 rows t of
+// the list's own block and the 64-row segment s of block j (blocks have up to
+// 256 rows), partly whether the mask hides some of the token pairs in question.
 template <bool kEnc>
-__device__ __forceinline__ int list_block(int v) { return kEnc ? v >> 1 : v; }
+__device__ __forceinline__ int list_block(int v) { return kEnc ? v >> 9 : v; }
+__device__ __forceinline__ int seen_segments(int v, int t) { return v >> (1 + 4 * t) & 15; }
 // What a group of queries sees of a group of keys: 0 nothing, 1 everything, 2 to
 // be found out token by token.
 __device__ __forceinline__ int group_class(float qlo, float qhi, int qdmin, int qdmax, float klo, float khi, int kdmin,
@@ -77,31 +80,34 @@ __device__ __forceinline__ int group_class(float qlo, float qhi, int qdmin, int 
     if (qdmax < kdmin || kdmax < qdmin || klo > qhi) return 0;
     return qdmin == qdmax && kdmin == kdmax && qdmin == kdmin && khi <= qlo ? 1 : 2;
 }
-// Is j in the ascending list L[0..n)?
+// The entry of block j in the ascending list L[0..n), -1 without one.
 template <bool kEnc>
-__device__ __forceinline__ bool sorted_has(const int *L, int n, int j) {
+__device__ __forceinline__ int sorted_find(const int *L, int n, int j) {
     int lo = 0, hi = n - 1;
     while (lo <= hi) {
         const int mid = (lo + hi) >> 1;
-        const int v = list_block<kEnc>(L[mid]);
-        if (v == j) return true;
+        const int e = L[mid], v = list_block<kEnc>(e);
+        if (v == j) return e;
         if (v < j) lo = mid + 1;
         else hi = mid - 1;
     }
-    return false;
+    return -1;
 }
 // 64-row segments of the union of two ascending block lists (every lane of
-// the warp gets the total).
+// the warp gets the total); scored: those in which the 128 rows t of the
+// lists' own block see anything.
 template <bool kEnc>
-__device__ __forceinline__ int union_segments(const int *A, int na, const int *B, int nb, const int *bo, int lane) {
+__device__ __forceinline__ int union_segments(const int *A, int na, const int *B, int nb, const int *bo, int t, int lane) {
     int n = 0;
     for (int u = lane; u < na; u += 32) {
         const int j = list_block<kEnc>(A[u]);
-        n += (bo[j + 1] - bo[j]) >> 6;
+        n += kEnc ? __popc(seen_segments(A[u], t)) : (bo[j + 1] - bo[j]) >> 6;
     }
     for (int u = lane; u < nb; u += 32) {
         const int j = list_block<kEnc>(B[u]);
-        if (!sorted_has<kEnc>(A, na, j)) n += (bo[j + 1] - bo[j]) >> 6;
+        const int e = sorted_find<kEnc>(A, na, j);
+        if constexpr (kEnc) n += __popc(seen_segments(B[u], t) & ~(e < 0 ? 0 : seen_segments(e, t)));
+        else if (e < 0) n += (bo[j + 1] - bo[j]) >> 6;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -109,20 +115,41 @@ __device__ __forceinline__ int union_segments(const int *A, int na, const int *B
 }
 // Walk over those segments in ascending block order, the two lists being the
 // index ranges [ua, a_end) and [ub, b_end) of one array L: r is the
-// segment's first block-contiguous row, mask bit 0 / bit 1 say whether its
-// block is in the first / second list, bit 2 / bit 3 (scored lists) whether
+// segment's first block-contiguous row, mask bit 0 / bit 1 say whether it is
+// in the first / second list, bit 2 / bit 3 (scored lists) whether
 // the pair is only partly visible.  L and the block offsets bo are passed
 // to each step rather than kept (the kernels are short of registers).
 template <bool kEnc>
 struct SegWalk {
     int ua, a_end, ub, b_end;
     int r, r_end, mask;
+    int va_, vb_, todo, t_;  // scored: the entries of r's block (bits of seen, partly) and its segments to come
+    __device__ __forceinline__ void pick_seen(const int *L, const int *bo) {
+        while (todo == 0) {
+            const int va = ua < a_end ? L[ua] : 0x7fffffff, vb = ub < b_end ? L[ub] : 0x7fffffff;
+            const int ja = list_block<true>(va), jb = list_block<true>(vb), j = min(ja, jb);
+            if (j == list_block<true>(0x7fffffff)) {
+                r = mask = 0;
+                return;
+            }
+            va_ = ja == j ? seen_segments(va, t_) << 1 | (va & 1) : 0;
+            vb_ = jb == j ? seen_segments(vb, t_) << 1 | (vb & 1) : 0;
+            todo = (va_ | vb_) >> 1;
+            ua += ja == j;
+            ub += jb == j;
+            r_end = bo[j];  // here: the block's first row
+        }
+        const int s = __ffs(todo) - 1;
+        todo &= todo - 1;
+        r = r_end + 64 * s;
+        mask = (va_ >> (s + 1) & 1) * (1 + 4 * (va_ & 1)) + (vb_ >> (s + 1) & 1) * (2 + 8 * (vb_ & 1));
+    }
     __device__ __forceinline__ void pick(const int *L, const int *bo) {
+        if constexpr (kEnc) return pick_seen(L, bo);
         const int va = ua < a_end ? L[ua] : 0x7fffffff, vb = ub < b_end ? L[ub] : 0x7fffffff;
         const int ja = list_block<kEnc>(va), jb = list_block<kEnc>(vb);
         const int j = min(ja, jb);
         mask = (ja == j ? 1 : 0) | (jb == j ? 2 : 0);
-        if (kEnc) mask |= (ja == j ? (va & 1) << 2 : 0) | (jb == j ? (vb & 1) << 3 : 0);
         ua += ja == j;
         ub += jb == j;
         if (j != list_block<kEnc>(0x7fffffff)) {
@@ -133,7 +160,9 @@ struct SegWalk {
             mask = 0;
         }
     }
-    __device__ __forceinline__ void init(int a0, int a1, int b0, int b1, const int *L, const int *bo) {
+    __device__ __forceinline__ void init(int a0, int a1, int b0, int b1, const int *L, const int *bo, int t) {
+        todo = 0;
+        t_ = t;
         ua = a0;
         a_end = a1;
         ub = b0;
@@ -141,6 +170,7 @@ struct SegWalk {
         pick(L, bo);
     }
     __device__ __forceinline__ void advance(const int *L, const int *bo) {
+        if constexpr (kEnc) return pick_seen(L, bo);
         r += 64;
         if (r >= r_end) pick(L, bo);
     }
