@@ -317,12 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t mw = mask_s[st];
                 bool act = live && ((mw >> half) & 1u);
-                bool part = kEnc && ((mw >> (2 + half)) & 1u);
+                bool part = false;
                 const uint32_t dsrow = sbase + L::kDS + (c & 1) * 16384 + rowid * 128;
 #pragma unroll 1
                 for (int sub = 0; sub < 2; ++sub) {
                     const int cq = 2 * cg2 + sub;  // 16 query columns [16 cq, 16 cq + 16)
-                    if constexpr (kEnc) {  // (live rows are whole warps: all of this is warp-uniform)
+                    if constexpr ((kScore & kMask) != 0) {  // (live rows are whole warps: all of this is warp-uniform)
                         act = live && ((mw >> half) & 1u);
                         part = act && ((mw >> (2 + half)) & 1u);
                         if (part) {
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         if (act) {
                             const uint64_t s2 = splat2(scale_log2);
-                            if (kEnc && part) hide16(sv, sc, (size_t)b * g.N, (int)(mw >> 4) + 16 * cq, k0 + rowid);
+                            if (part) hide16(sv, sc, (size_t)b * g.N, (int)(mw >> 4) + 16 * cq, k0 + rowid);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int q = 4 * j;
@@ -587,6 +587,14 @@ static prism_status configure_bwd() {
         cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
     PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kCap | kBias>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kMask>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kCap | kMask>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kBias | kMask>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(bwdtc::k_attn_bwd_tc<D, kScored | kCap | kBias | kMask>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
     return PRISM_OK;
 }
 
@@ -618,11 +626,15 @@ prism_status launch_attn_bwd_tc_main(Plan &pl, void *dK, void *dV, cudaStream_t 
 
 template <int D>
 static prism_status bwd_scored(Plan &pl, void *dK, void *dV, cudaStream_t st) {
-    switch (score_flags(pl.score)) {
+    switch (score_flags(pl.score) | (score_masks(pl.score) ? kMask : 0)) {
         case kScored: return bwd_tc_main<D, kScored>(pl, dK, dV, st);
         case kScored | kCap: return bwd_tc_main<D, kScored | kCap>(pl, dK, dV, st);
         case kScored | kBias: return bwd_tc_main<D, kScored | kBias>(pl, dK, dV, st);
-        default: return bwd_tc_main<D, kScored | kCap | kBias>(pl, dK, dV, st);
+        case kScored | kCap | kBias: return bwd_tc_main<D, kScored | kCap | kBias>(pl, dK, dV, st);
+        case kScored | kMask: return bwd_tc_main<D, kScored | kMask>(pl, dK, dV, st);
+        case kScored | kCap | kMask: return bwd_tc_main<D, kScored | kCap | kMask>(pl, dK, dV, st);
+        case kScored | kBias | kMask: return bwd_tc_main<D, kScored | kBias | kMask>(pl, dK, dV, st);
+        default: return bwd_tc_main<D, kScored | kCap | kBias | kMask>(pl, dK, dV, st);
     }
 }
 

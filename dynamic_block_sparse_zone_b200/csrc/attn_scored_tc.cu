@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             auto issue_k = [&](int i) -> bool {
                 const int s = i & 1, ms = i & 3;
                 if (i >= 2 && !mbar_wait(bar_ke + 8 * s, ((i >> 1) - 1) & 1, status, kSiteKEmpty, abort_flag)) return false;
-                const bool part = wk.mask >> 2;
+                const bool part = (kScore & kMask) && wk.mask >> 2;
                 const size_t n0 = (size_t)b * g.N + wk.r;
                 const uint32_t meta = sbase + L::kMeta + ms * L::kMetaSlot, bm = bar_m + 8 * ms;
                 mask_w[ms] = (uint32_t)wk.mask;  // published by the arrive below
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (kScore & kBias) slope2 = sc.slopes[h] * 1.4426950408889634f;
         // of the warp's 32 queries (all or none of them are valid)
         GroupRange qr{INFINITY, -INFINITY, -2, -2};
-        if (quad * 32 < qvalid) {
+        if ((kScore & kMask) && quad * 32 < qvalid) {
             const GroupRange *p = sc.qgrp + ((size_t)b * g.N + q0 + quad * 32) / 16;
             const GroupRange r0 = p[0], r1 = p[1];
             qr = GroupRange{fminf(r0.lo, r1.lo), fmaxf(r0.hi, r1.hi), min(r0.dmin, r1.dmin), max(r0.dmax, r1.dmax)};
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             tc_fence_after();
             const uint32_t mw = mask_w[i & 3];
             if ((mw >> half) & 1u) {  // the segment is in this query block's selection
-                const bool part = (mw >> (2 + half)) & 1u;
+                const bool part = (kScore & kMask) && ((mw >> (2 + half)) & 1u);
                 const uint32_t meta = sbase + L::kMeta + (i & 3) * L::kMetaSlot;
                 uint64_t acc2 = 0;
 #pragma unroll 1
@@ -394,6 +394,10 @@ static prism_status configure() {
     PRISM_CUDA_OK(cudaFuncSetAttribute(segtc::k_attn_fwd_scored<D, kScored | kCap>, attr, bytes));
     PRISM_CUDA_OK(cudaFuncSetAttribute(segtc::k_attn_fwd_scored<D, kScored | kBias>, attr, bytes));
     PRISM_CUDA_OK(cudaFuncSetAttribute(segtc::k_attn_fwd_scored<D, kScored | kCap | kBias>, attr, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(segtc::k_attn_fwd_scored<D, kScored | kMask>, attr, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(segtc::k_attn_fwd_scored<D, kScored | kCap | kMask>, attr, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(segtc::k_attn_fwd_scored<D, kScored | kBias | kMask>, attr, bytes));
+    PRISM_CUDA_OK(cudaFuncSetAttribute(segtc::k_attn_fwd_scored<D, kScored | kCap | kBias | kMask>, attr, bytes));
     return PRISM_OK;
 }
 
@@ -417,11 +421,17 @@ static prism_status run(Plan &pl, void *O, float *lse, cudaStream_t st) {
 
 template <int D>
 static prism_status run_any(Plan &pl, void *O, float *lse, cudaStream_t st) {
-    switch (score_flags(pl.score)) {
+    // without a mask the kernel carries no code for one: the registers it takes cost a capped
+    // forward (16 x 32 x 32, 8 heads of 128) 3 to 6%
+    switch (score_flags(pl.score) | (score_masks(pl.score) ? kMask : 0)) {
         case kScored: return run<D, kScored>(pl, O, lse, st);
         case kScored | kCap: return run<D, kScored | kCap>(pl, O, lse, st);
         case kScored | kBias: return run<D, kScored | kBias>(pl, O, lse, st);
-        default: return run<D, kScored | kCap | kBias>(pl, O, lse, st);
+        case kScored | kCap | kBias: return run<D, kScored | kCap | kBias>(pl, O, lse, st);
+        case kScored | kMask: return run<D, kScored | kMask>(pl, O, lse, st);
+        case kScored | kCap | kMask: return run<D, kScored | kCap | kMask>(pl, O, lse, st);
+        case kScored | kBias | kMask: return run<D, kScored | kBias | kMask>(pl, O, lse, st);
+        default: return run<D, kScored | kCap | kBias | kMask>(pl, O, lse, st);
     }
 }
 

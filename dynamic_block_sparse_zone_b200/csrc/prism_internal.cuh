@@ -55,7 +55,7 @@ struct alignas(16) GroupRange {
 };
 struct Score {
     bool set;               // valid for the plan's current build
-    bool has_bias, has_doc;
+    bool has_bias, has_doc, causal;
     bool zeroed;            // a scored forward has zeroed padding rows of the current Qp, Kp, Vp
     float cap;              // 0: none
     float *slopes;          // [heads]
@@ -196,8 +196,9 @@ struct ScoreArgs {
     float cap_out;              // cap log2(e)
 };
 ScoreArgs score_args(const Plan &pl, bool backward);
-constexpr int kScored = 1, kCap = 2, kBias = 4;  // template flags of those kernels
+constexpr int kScored = 1, kCap = 2, kBias = 4, kMask = 8;  // template flags of those kernels (kMask: some pair may be hidden)
 inline int score_flags(const Score &s) { return kScored | (s.cap > 0.f ? kCap : 0) | (s.has_bias ? kBias : 0); }
+inline bool score_masks(const Score &s) { return s.has_doc || s.causal; }
 
 prism_status launch_audio_norms(const void *h, float *a, long long rows, int C, cudaStream_t st);
 

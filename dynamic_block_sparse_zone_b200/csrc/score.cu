@@ -336,6 +336,7 @@ prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
     s.cap = in.cap;
     s.has_bias = in.slopes != nullptr;
     s.has_doc = in.doc != nullptr;
+    s.causal = in.causal != 0;
     size_t n = (size_t)g.batch * g.N;
     if ((size_t)g.heads > n) n = g.heads;
     k_score_tokens<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(

@@ -261,7 +261,7 @@ PRISM_API prism_status prism_attn_bwd(prism_plan *plan, const void *O, const voi
  * the work on `stream` is done) and removes the hidden block pairs from its own
  * copy of the selection.  It belongs to the plan's current build: every build
  * drops it, prism_plan_update_qkv keeps it.  It forgets the last forward.  The
- * first call on a plan allocates (about 8 bytes per selectable block pair, 12
+ * first call on a plan allocates (about 8 bytes per selectable block pair, 14
  * per token and 2 per value of O; PRISM_ERR_STATE while `stream` is being
  * captured).
  * With doc, a scored pass first zeroes the rows of padding tokens in the plan's
