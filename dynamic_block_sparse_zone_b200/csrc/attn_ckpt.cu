@@ -15,21 +15,22 @@ using namespace rows;
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 8;
+constexpr int kRows = 16;  // blocks are multiples of 64 tokens
 
 struct Codes8 {
     const uint8_t *codes, *scales;
     int fmt;
 };
 
-__global__ void __launch_bounds__(kThreads, 4) k_permute_pool_ckpt(Codes8 Q, Codes8 K, Codes8 V, Geo g,
-                                                                   const int *__restrict__ nb,
-                                                                   const int *__restrict__ blk_off,
-                                                                   const int *__restrict__ perm,
-                                                                   __nv_bfloat16 *__restrict__ Qp,
-                                                                   __nv_bfloat16 *__restrict__ Kp,
-                                                                   __nv_bfloat16 *__restrict__ Vp,
-                                                                   double *__restrict__ Qbar, double *__restrict__ Kbar) {
+struct Restore {  // of Q, K, V: the checkpoint, the plan's copy and the block means (V has none)
+    Codes8 from[3];
+    __nv_bfloat16 *to[3];
+    double *mean[3];
+};
+
+__global__ void __launch_bounds__(kThreads) k_permute_pool_ckpt(Restore a, Geo g, const int *__restrict__ nb,
+                                                                const int *__restrict__ blk_off,
+                                                                const int *__restrict__ perm) {
     const int nslice = (g.C / 4 + kThreads - 1) / kThreads;
     const int j = blockIdx.x / nslice, slice = blockIdx.x % nslice, b = blockIdx.y;
     if (j >= nb[b]) return;
@@ -38,45 +39,36 @@ __global__ void __launch_bounds__(kThreads, 4) k_permute_pool_ckpt(Codes8 Q, Cod
     const int *pb = perm + (size_t)b * g.N + off;
     const int c = 4 * (slice * kThreads + threadIdx.x);
     if (c >= g.C) return;
+    const Codes8 from = a.from[blockIdx.z];
+    __nv_bfloat16 *to = a.to[blockIdx.z];
     const int hd = c / g.D, d0 = c % g.D;
     const size_t bh = (size_t)b * g.heads + hd, dst0 = (bh * g.N + off) * g.D + d0;
-    double sq[4] = {0.0, 0.0, 0.0, 0.0}, sk[4] = {0.0, 0.0, 0.0, 0.0};
+    double sum[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 1
     for (int r0 = 0; r0 < B; r0 += kRows) {
-        Codes<4> q[kRows], k[kRows], v[kRows];
-        uint32_t qs[kRows], ks[kRows], vs[kRows];
+        Codes<4> k[kRows];
+        uint32_t ks[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const size_t row = (size_t)b * g.N + pb[r0 + i], at = row * g.C + c, sat = row * ng + c / kGroup;
-            q[i].w[0] = __ldg(reinterpret_cast<const uint32_t *>(Q.codes + at));
-            k[i].w[0] = __ldg(reinterpret_cast<const uint32_t *>(K.codes + at));
-            v[i].w[0] = __ldg(reinterpret_cast<const uint32_t *>(V.codes + at));
-            qs[i] = __ldg(Q.scales + sat);
-            ks[i] = __ldg(K.scales + sat);
-            vs[i] = __ldg(V.scales + sat);
+            const size_t row = (size_t)b * g.N + pb[r0 + i];
+            k[i].w[0] = __ldg(reinterpret_cast<const uint32_t *>(from.codes + row * g.C + c));
+            ks[i] = __ldg(from.scales + row * ng + c / kGroup);
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const size_t dst = dst0 + (size_t)(r0 + i) * g.D;
             f2 x[2];
-            q[i].decode<__nv_bfloat16>(qs[i], Q.fmt, x);
-            *reinterpret_cast<uint2 *>(Qp + dst) = make_uint2(narrow<__nv_bfloat16>(x[0]), narrow<__nv_bfloat16>(x[1]));
-            sq[0] += (double)low(x[0]), sq[1] += (double)high(x[0]);
-            sq[2] += (double)low(x[1]), sq[3] += (double)high(x[1]);
-            k[i].decode<__nv_bfloat16>(ks[i], K.fmt, x);
-            *reinterpret_cast<uint2 *>(Kp + dst) = make_uint2(narrow<__nv_bfloat16>(x[0]), narrow<__nv_bfloat16>(x[1]));
-            sk[0] += (double)low(x[0]), sk[1] += (double)high(x[0]);
-            sk[2] += (double)low(x[1]), sk[3] += (double)high(x[1]);
-            v[i].decode<__nv_bfloat16>(vs[i], V.fmt, x);
-            *reinterpret_cast<uint2 *>(Vp + dst) = make_uint2(narrow<__nv_bfloat16>(x[0]), narrow<__nv_bfloat16>(x[1]));
+            k[i].decode<__nv_bfloat16>(ks[i], from.fmt, x);
+            *reinterpret_cast<uint2 *>(to + dst0 + (size_t)(r0 + i) * g.D) =
+                make_uint2(narrow<__nv_bfloat16>(x[0]), narrow<__nv_bfloat16>(x[1]));
+            sum[0] += (double)low(x[0]), sum[1] += (double)high(x[0]);
+            sum[2] += (double)low(x[1]), sum[3] += (double)high(x[1]);
         }
     }
-    const double inv = 1.0 / (double)B;
-    double *oq = Qbar + (bh * g.nbmax + j) * g.D + d0, *ok = Kbar + (bh * g.nbmax + j) * g.D + d0;
+    if (a.mean[blockIdx.z]) {
+        const double inv = 1.0 / (double)B;
+        double *o = a.mean[blockIdx.z] + (bh * g.nbmax + j) * g.D + d0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        oq[e] = sq[e] * inv;
-        ok[e] = sk[e] * inv;
+        for (int e = 0; e < 4; ++e) o[e] = sum[e] * inv;
     }
 }
 
@@ -99,9 +91,9 @@ prism_status launch_regather_ckpt(Plan &pl, const prism_attn_ckpt &c, cudaStream
     const Geo &g = pl.g;
     {
         TimerScope ts(pl, kTPermutePool, st);
-        k_permute_pool_ckpt<<<dim3((g.C / 4 + kThreads - 1) / kThreads * g.nbmax, g.batch), kThreads, 0, st>>>(
-            codes_of(c.Q), codes_of(c.K), codes_of(c.V), g, pl.nb, pl.blk_off, pl.perm, pl.Qp, pl.Kp, pl.Vp, pl.Qbar,
-            pl.Kbar);
+        const Restore r{{codes_of(c.Q), codes_of(c.K), codes_of(c.V)}, {pl.Qp, pl.Kp, pl.Vp}, {pl.Qbar, pl.Kbar, nullptr}};
+        k_permute_pool_ckpt<<<dim3((g.C / 4 + kThreads - 1) / kThreads * g.nbmax, g.batch, 3), kThreads, 0, st>>>(
+            r, g, pl.nb, pl.blk_off, pl.perm);
     }
     PRISM_CUDA_OK(cudaGetLastError());
     pl.score.zeroed = false;
