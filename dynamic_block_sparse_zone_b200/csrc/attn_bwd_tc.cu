@@ -47,12 +47,18 @@
 // keeps them in chunk order (deterministic sums), and dK and dV start from zero
 // (written by the drain warps before the first chunk), so no product needs to
 // know whether it is the first.
-// Scored variants (kScore): the columns without hidden block pairs (score.cu);
-// S becomes cap tanh(S / cap) - slope_h |p_q - p_k|, dS gets the factor
-// 1 - tanh^2, and in a pair that is only partly visible a hidden key's P and dS
-// are 0 (its logit -inf).  Positions, visibilities and documents come from
+// Scored variants (kScore): the columns without hidden units (score.cu); S
+// becomes cap tanh(S / cap) - slope_h |p_q - p_k|, dS gets the factor
+// 1 - tanh^2.  Where a pair of blocks is only partly visible, 16 queries by a
+// warp's 32 keys at a time are looked at by their ranges: hidden ones are zeros
+// without further work, and only in mixed ones is the mask applied key by key (a
+// hidden key's logit is -inf).  Positions, visibilities and documents come from
 // global memory (L1: the shared memory is full, and 80 registers hold no more),
-// a chunk's queries as one broadcast load per four.
+// a chunk's queries as one broadcast load per four.  Measured on 24 x 32 x 40
+// tokens, 8 heads of 128 (unscored: 2.51 ms): without scores 2.88, cap 3.39, bias
+// 3.26, both 3.74 ms; both on 16 x 32 x 32: 0.50 instructions per cycle and
+// scheduler, tensor cores busy 35%: the softmax's latency lengthens the loop
+// through the chunk's products.
 //
 // Warp roles (704 threads): warp 0 TMA producer (K, V once; Q, dO, LSE,
 // Delta per chunk into a three-stage ring; LSE is kept negated, in log2

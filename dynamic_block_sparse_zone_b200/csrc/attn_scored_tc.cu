@@ -31,6 +31,12 @@
 // V: an 8-bit O may be kept for the backward, and a P of 8 bits moves O by about
 // half a step of bf16, enough for every tenth 8-bit code to fall on the other
 // side and Delta with it (dQ off by up to 0.012 in relative norm, 0.0025 so).
+// Measured on 24 x 32 x 40 tokens, 8 heads of 128, 9.7e11 FLOP of selected pairs
+// (none, with the same selection unscored: 1.03 ms, 942 TFLOP/s): without scores
+// 1.16 ms, cap 1.59, bias 1.25, both 1.75 ms; 16 x 32 x 32 tokens with both:
+// 514 us, 510 TFLOP/s, where the tensor cores are busy 44% of the cycles, the
+// FMA pipe 49% and 0.54 instructions are issued per cycle and scheduler: bound by
+// the latency of the softmax's instructions, 14 per score.
 // TMEM columns: S / P of the chains [0, 64) and [64, 128) (in each 32 of them, hi
 // in the first 16 and lo in the second), O [128, 128 + D).
 #include <cuda.h>

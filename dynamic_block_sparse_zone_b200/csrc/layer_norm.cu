@@ -10,6 +10,19 @@
 // second look at the row), not from squares, so an offset costs no digits.
 // The weight gradients are summed in a fixed order: every run gives the same
 // bits.
+//
+// Bound: HBM, by a read of each input and a write of each output.  Measured,
+// bf16 with fp32 weights, as a share of the 6456 GB/s that a copy reaches:
+//   rows x channels   forward       with checkpoint  backward      from 8 bits
+//   1048576 x 128     103 us 0.81   163 us 0.64      157 us 0.79   170 us 0.62
+//   92160 x 1536      108 us 0.81   123 us 0.90      147 us 0.90   167 us 0.66
+//   92160 x 2048      140 us 0.83   162 us 0.91      190 us 0.92   222 us 0.66
+//   40000 x 5120      157 us 0.81   239 us 0.67      281 us 0.68   456 us 0.35
+//   40000 x 1001       72 us 0.34   127 us 0.24       87 us 0.43   100 us 0.31
+// What holds the others: from 8 bits, the instructions of the decoding (a byte
+// permute, a multiply-add and a multiply per pair beside the gradient's own);
+// rows of more than 4096 channels backward, one CTA per SM, whose barrier is not
+// hidden by another's work; odd rows, element-wise loads and stores.
 #include <atomic>
 
 #include "rows.cuh"
