@@ -645,6 +645,16 @@ def _rows(t: torch.Tensor, name: str, device=None, dtype=None):
     return prism_rows(t.data_ptr(), levels[0][1], levels[1][1], levels[0][0]), count, C
 
 
+def _out(t, name, like, C):
+    """The output t, or a new one, with its rows: (tensor, prism_rows)."""
+    if t is None:  # (empty_like keeps a contiguous tensor's layout and takes half of empty's time)
+        t = torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return t, prism_rows(t.data_ptr(), C, 0, 0)
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    return t, _rows(t, name, like.device, like.dtype)[0]
+
+
 def _weights(x, channels, **weights):
     """Checks gamma and beta against x; their common dtype (fp32 without any)."""
     kind = None
@@ -754,13 +764,9 @@ def prism_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, 
     (y, mean, rstd, Checkpoint) -- what prism_layer_norm_bwd can take in x's place."""
     rx, n, C = _rows(x, "x")
     wdt = _weights(x, C, gamma=gamma, beta=beta)
-    dev, shape = x.device, x.shape
-    if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
-    elif y.shape != shape:
-        raise ValueError("y must have x's shape")
-    ry, _, _ = _rows(y, "y", dev, x.dtype)
-    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    dev = x.device
+    y, ry = _out(y, "y", x, C)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     kept = _new_ckpt(x, n, C, ckpt) if ckpt is not None else None
     with _on(dev):
@@ -790,16 +796,12 @@ def prism_layer_norm_bwd(dy: torch.Tensor, x, gamma: Optional[torch.Tensor], mea
         c = x.to_c()
     else:
         rx = _rows(x, "x", dev, dy.dtype)[0]
-    if dx is None:
-        dx = torch.empty(shape, dtype=dy.dtype, device=dev)
-    elif dx.shape != shape:
-        raise ValueError("dx must have dy's shape")
-    rdx, _, _ = _rows(dx, "dx", dev, dy.dtype)
+    dx, rdx = _out(dx, "dx", dy, C)
     lib = load_library()
     dgamma = dbeta = work = None
     nbytes = 0
     if weight_grads:
-        dgamma = torch.empty(C, dtype=wdt, device=dev)
+        dgamma = torch.empty(C, dtype=wdt, device=dev) if gamma is None else torch.empty_like(gamma)
         dbeta = torch.empty_like(dgamma)
         nbytes = lib.prism_layer_norm_bwd_workspace(n, C)
         work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
