@@ -7,9 +7,11 @@
 // neighbouring lanes that hold a scale group agree on its exponent by
 // shuffles.  Four vectors per lane are in flight.  Rows that follow each other
 // without a gap, with whole groups in each, are taken as one long row.
-// Measured, 92160 x 2048 bf16: pack 102 us, 0.87 of what a copy reaches, unpack
-// 111 us, 0.80; 40000 rows of 1001 channels (element-wise, bound by the byte
-// stores): 178 us and 118 us, 0.11 and 0.16.
+// A lane's vectors lie at constant distances from its first, which is found
+// once: with a row, a vector and 64-bit addresses worked out for each, twice the
+// registers halved the warps (92160 x 2048 bf16: pack 102 us, unpack 111 us).
+// Measured: 94 us each, 0.94 of what a copy reaches; 40000 rows of 1001 channels
+// (element-wise, bound by instructions): 71 us and 64 us, 0.27 and 0.30.
 #include "rows.cuh"
 
 namespace prism {
@@ -30,24 +32,53 @@ struct CkptArgs {
     int lanes;              // lanes per row (a power of two; 32: a warp walks along a row)
 };
 
-// The row and the vector in it of this lane's u-th access in warp item `it`.
+// Where a lane's kU vectors of warp item `it` are.  kLong: side by side in one
+// row, 32 apart, at constant distances from the first; otherwise one each in kU
+// rows that lie 32 / lanes apart.
+template <bool kLong, int VEC, int kBytes>
 struct Place {
-    long long r, v;
-    bool in;
-};
-__device__ __forceinline__ Place place(const CkptArgs &a, long long it, long long per_row, int u) {
-    const int lane = threadIdx.x & 31;
-    Place p;
-    if (a.lanes == 32) {
-        p.r = per_row == 1 ? it : it / per_row;
-        p.v = (it - p.r * per_row) * (32 * kU) + u * 32 + lane;
-    } else {
-        p.r = (it * kU + u) * (32 / a.lanes) + lane / a.lanes;
-        p.v = lane & (a.lanes - 1);
+    const char *x;    // kLong: this lane's first vector, else NULL
+    long long at, g;  // kLong: its first code and scale
+    int left, c;      // kLong: vectors of 32 lanes' steps left, channels left
+    long long r0, v;
+    __device__ __forceinline__ void init(const CkptArgs &a, long long it, long long per_row, long long ng) {
+        const int lane = threadIdx.x & 31;
+        if constexpr (kLong) {
+            long long r = it, v0 = lane;
+            if (per_row > 1) {
+                r = (it | per_row) >> 32 ? it / per_row : (long long)((unsigned)it / (unsigned)per_row);
+                v0 += (it - r * per_row) * (32 * kU);
+            }
+            x = a.x(r) + v0 * kBytes;
+            at = r * a.C + v0 * VEC;
+            g = r * ng + v0 / (kGroup / VEC);
+            const long long l = a.nvec - v0, cl = a.C - v0 * VEC;
+            left = l < 32 * kU ? (int)l : 32 * kU;
+            c = cl < 32 * kU * VEC ? (int)cl : 32 * kU * VEC;
+        } else {
+            r0 = it * kU * (32 / a.lanes) + lane / a.lanes;
+            v = lane & (a.lanes - 1);
+        }
     }
-    p.in = p.r < a.nrows && p.v < a.nvec;
-    return p;
-}
+    __device__ __forceinline__ bool in(const CkptArgs &a, int u) const {
+        return kLong ? u * 32 < left : v < a.nvec && row(a, u) < a.nrows;
+    }
+    __device__ __forceinline__ long long row(const CkptArgs &a, int u) const { return r0 + u * (32 / a.lanes); }
+    // the u-th vector is number vec(u) from data() on, of channels() channels
+    __device__ __forceinline__ char *data(const CkptArgs &a, int u) const {
+        return kLong ? const_cast<char *>(x) : a.x(row(a, u));
+    }
+    __device__ __forceinline__ uint8_t *codes(const CkptArgs &a, int u) const {
+        return a.codes + (kLong ? at : row(a, u) * a.C);
+    }
+    __device__ __forceinline__ uint8_t *scale(const CkptArgs &a, int u, long long ng) const {
+        return a.scales + (kLong ? g + u * (VEC * 32 / kGroup) : row(a, u) * ng + v / (kGroup / VEC));
+    }
+    __device__ __forceinline__ long long vec(int u) const { return kLong ? u * 32 : v; }
+    __device__ __forceinline__ long long channels(const CkptArgs &a) const { return kLong ? c : a.C; }
+    // lanes per row are a multiple of those that share a scale
+    __device__ __forceinline__ bool first() const { return (threadIdx.x & (kGroup / VEC - 1)) == 0; }
+};
 __device__ __forceinline__ long long items(const CkptArgs &a, long long &per_row) {
     per_row = (a.nvec + 32 * kU - 1) / (32 * kU);
     const long long rows_per_item = (long long)kU * (32 / a.lanes);
@@ -60,21 +91,21 @@ struct CkptBatch {
     CkptArgs a[N];
 };
 
-template <typename T, int VEC, int N>
+template <typename T, int VEC, int N, bool kLong>
 __global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptBatch<N> batch) {
     const CkptArgs &a = batch.a[N == 1 ? 0 : blockIdx.y];
-    constexpr int VP = VEC / 2, kPer = kGroup / VEC;
+    constexpr int VP = VEC / 2;
     long long per_row;
     const long long n = items(a, per_row), ng = (a.C + kGroup - 1) / kGroup;
     for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < n;
          it += (long long)gridDim.x * (kThreads / 32)) {
         Vec<T, VEC> raw[kU];
-        Place p[kU];
+        Place<kLong, VEC, VEC * sizeof(T)> p;
+        p.init(a, it, per_row, ng);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            p[u] = place(a, it, per_row, u);
-            if (p[u].in) raw[u].load(a.x(p[u].r), p[u].v, a.C);
-            else raw[u].zero();
+            raw[u].zero();
+            if (p.in(a, u)) raw[u].load(p.data(a, u), p.vec(u), p.channels(a));
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -82,43 +113,43 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_pack(CkptBatch<N> batch) {
 #pragma unroll
             for (int e = 0; e < VP; ++e) x[e] = raw[u].pair(e);
             const int k = group_exponent<VEC>(top_of(x), a.fmt);
-            if (p[u].in) {
+            if (p.in(a, u)) {
                 Codes<VEC> c;
                 c.encode(x, code_inv_scale(k), a.fmt);
-                c.store(a.codes + p[u].r * a.C, p[u].v, a.C);
-                if (p[u].v % kPer == 0) a.scales[p[u].r * ng + p[u].v / kPer] = (uint8_t)(k + 127);
+                c.store(p.codes(a, u), p.vec(u), p.channels(a));
+                if (p.first()) *p.scale(a, u, ng) = (uint8_t)(k + 127);
             }
         }
     }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool kLong>
 __global__ void __launch_bounds__(kThreads) k_ckpt_unpack(CkptArgs a) {
-    constexpr int VP = VEC / 2, kPer = kGroup / VEC;
+    constexpr int VP = VEC / 2;
     long long per_row;
     const long long n = items(a, per_row), ng = (a.C + kGroup - 1) / kGroup;
     for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < n;
          it += (long long)gridDim.x * (kThreads / 32)) {
         Codes<VEC> c[kU];
         uint32_t sb[kU];
-        Place p[kU];
+        Place<kLong, VEC, VEC * sizeof(T)> p;
+        p.init(a, it, per_row, ng);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            p[u] = place(a, it, per_row, u);
-            if (p[u].in) {
-                c[u].load(a.codes + p[u].r * a.C, p[u].v, a.C);
-                sb[u] = a.scales[p[u].r * ng + p[u].v / kPer];
+            if (p.in(a, u)) {
+                c[u].load(p.codes(a, u), p.vec(u), p.channels(a));
+                sb[u] = *p.scale(a, u, ng);
             }
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-            if (p[u].in) {
+            if (p.in(a, u)) {
                 f2 x[VP];
                 c[u].template decode<T>(sb[u], a.fmt, x);
                 Vec<T, VEC> o;
 #pragma unroll
                 for (int e = 0; e < VP; ++e) o.set_pair(e, x[e]);
-                o.store(a.x(p[u].r), p[u].v, a.C);
+                o.store(p.data(a, u), p.vec(u), p.channels(a));
             }
     }
 }
@@ -142,8 +173,14 @@ int lay_out(CkptArgs &a, bool dense) {
 template <typename T, int VEC, bool kPack>
 prism_status run(CkptArgs a, bool dense, cudaStream_t st) {
     const int grid = lay_out<VEC>(a, dense);
-    if constexpr (kPack) k_ckpt_pack<T, VEC, 1><<<grid, kThreads, 0, st>>>(CkptBatch<1>{{a}});
-    else k_ckpt_unpack<T, VEC><<<grid, kThreads, 0, st>>>(a);
+    const bool wide = a.lanes == 32;
+    if constexpr (kPack) {
+        if (wide) k_ckpt_pack<T, VEC, 1, true><<<grid, kThreads, 0, st>>>(CkptBatch<1>{{a}});
+        else k_ckpt_pack<T, VEC, 1, false><<<grid, kThreads, 0, st>>>(CkptBatch<1>{{a}});
+    } else {
+        if (wide) k_ckpt_unpack<T, VEC, true><<<grid, kThreads, 0, st>>>(a);
+        else k_ckpt_unpack<T, VEC, false><<<grid, kThreads, 0, st>>>(a);
+    }
     PRISM_CUDA_OK(cudaGetLastError());
     return PRISM_OK;
 }
@@ -179,7 +216,8 @@ prism_status launch_ckpt_pack4(const void *const (&x)[4], const prism_ckpt *cons
                           static_cast<uint8_t *>(k[i]->scales), k[i]->format, nrows, 0, C, 0};
         grid = lay_out<8>(b.a[i], true);
     }
-    k_ckpt_pack<__nv_bfloat16, 8, 4><<<dim3(grid, 4), kThreads, 0, st>>>(b);
+    // (heads * head_dim is a multiple of 32: one long row each)
+    k_ckpt_pack<__nv_bfloat16, 8, 4, true><<<dim3(grid, 4), kThreads, 0, st>>>(b);
     PRISM_CUDA_OK(cudaGetLastError());
     return PRISM_OK;
 }
