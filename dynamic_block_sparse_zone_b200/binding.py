@@ -181,6 +181,14 @@ def _need(t: torch.Tensor, name: str, dtype, shape):
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _here(**tensors):
+    """A plan's calls run on the current device: refuses tensors of another one."""
+    now = torch._C._cuda_getDevice()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != now:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{now}")
+
+
 class _DevArray:
     """Zero-copy view of device memory via __cuda_array_interface__."""
 
@@ -333,6 +341,7 @@ class PrismPlan:
                              (doc, "doc", torch.int32, (p.batch, p.N)), (prefix, "prefix", torch.float32, (p.batch,))):
             if t is not None:
                 _need(t, n, dt, sh)
+        _here(slopes=slopes, pos=pos, doc=doc, prefix=prefix)
         c = prism_score(float(cap), *(None if t is None else t.data_ptr() for t in (slopes, pos, doc)), int(bool(causal)),
                         None if prefix is None else prefix.data_ptr())
         _check(load_library().prism_plan_set_score(self._h, ctypes.byref(c), _stream()))
@@ -380,6 +389,7 @@ class PrismPlan:
         for t, n in ((Q, "Q"), (K, "K"), (V, "V"), (O, "O")):
             _need(t, n, torch.bfloat16, self._qkv_shape())
         _need(lse, "lse", torch.float32, (p.batch, p.heads, p.N))
+        _here(Q=Q, K=K, V=V, O=O, lse=lse)
         kept = [_new_ckpt(t, p.batch * p.N, p.heads * p.head_dim, fmt) for t in (Q, K, V, O)]
         out = AttnCheckpoint(*kept, lse)
         c = out.to_c(p)
@@ -389,6 +399,7 @@ class PrismPlan:
     def update_qkv_ckpt(self, ckpt: "AttnCheckpoint"):
         """update_qkv with the values that the checkpoint's 8-bit Q, K, V stand for."""
         c = ckpt.to_c(self.params)
+        _here(Q=ckpt.Q, K=ckpt.K, V=ckpt.V)
         _check(load_library().prism_plan_update_qkv_ckpt(self._h, ctypes.byref(c), _stream()))
         return self
 
@@ -400,6 +411,7 @@ class PrismPlan:
         for t, n in zip(grads, ("dQ", "dK", "dV")):
             _need(t, n, torch.bfloat16, shp)
         c = ckpt.to_c(self.params)
+        _here(Q=ckpt.Q, K=ckpt.K, V=ckpt.V, O=ckpt.O, lse=ckpt.lse, dO=dO, dQ=grads[0], dK=grads[1], dV=grads[2])
         _check(load_library().prism_attn_bwd_ckpt(self._h, ctypes.byref(c), _ptr(dO), *(_ptr(t) for t in grads),
                                                   int(bool(scored)), _stream()))
         return tuple(grads)

@@ -368,6 +368,18 @@ def test_graph_replay_and_another_stream(P):
 
 
 @pytest.mark.gpu
+def test_tensors_of_another_device_are_refused(P):
+    """(One GPU: what the calls are given only says that it lies elsewhere, and is never read.)"""
+    from types import SimpleNamespace
+
+    from dynamic_block_sparse_zone_b200 import binding as B
+    away = SimpleNamespace(device=torch.device("cuda", torch.cuda.current_device() + 1))
+    B._here(doc=None, pos=torch.zeros(1, device="cuda"))
+    with pytest.raises(ValueError, match="slopes is on cuda"):
+        B._here(doc=None, slopes=away)
+
+
+@pytest.mark.gpu
 def test_refusals(P):
     c = Case(P, 8, 16, 16, 2, 64, seed=9)
     plan = c.plan
