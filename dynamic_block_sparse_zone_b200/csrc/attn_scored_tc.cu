@@ -302,10 +302,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     logits32<kScore>(sr, sc, scale_log2, slope2, pq, dq, meta + 128 * q, meta + 256 + 128 * q,
                                      meta + 512 + 128 * q, cls == 2);
                     seen = seen || cls == 1;
-                    if (cls == 2) {
+                    if (cls == 2) {  // a score that is NaN is not hidden either
                         float mx = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+                        for (int e = 0; e < 32; e += 2) mx = fmax3_nan(mx, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
                         seen = seen || mx != -INFINITY;
                     }
                     uint32_t hi[16], lo[16];

@@ -423,6 +423,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// the same, NaN if any of them is
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // Packed pairs held as 64-bit values.
 __device__ __forceinline__ uint64_t pfma(uint64_t a, uint64_t b, uint64_t c) {

@@ -282,8 +282,9 @@ PRISM_API prism_status prism_plan_set_score(prism_plan *plan, const prism_score 
 
 /* The forward with the scores of the last prism_plan_set_score: arguments,
  * layouts and errors as prism_attn_fwd.  A query that sees no key (padding, or
- * a row whose selected blocks are all hidden) gets O = 0 and lse = -inf.  The
- * logits, their softmax and the log-sum-exp are fp32.                       */
+ * a row whose selected blocks are all hidden) gets O = 0 and lse = -inf.  A query
+ * that sees a score that is NaN gets NaN for both.  The logits, their softmax and
+ * the log-sum-exp are fp32.                                                 */
 PRISM_API prism_status prism_attn_fwd_scored(prism_plan *plan, void *O, float *lse, void *stream);
 
 /* Its gradient with respect to Q, K and V: as prism_attn_bwd, with the factor
