@@ -114,6 +114,24 @@ __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t adesc, uint
         mma_ss4<2, 4, 6, 2, 4, 6>(d_tmem, adesc, bdesc, idesc, 0u);
 }
 
+// x = q of the 16 scores (logistic4), y = (y - Delta) (1 - tanh^2); delta: the
+// shared-window address of the queries' Delta.
+template <bool kNan>
+__device__ __forceinline__ void logistic16(uint32_t (&sv)[16], uint32_t (&dv)[16], uint32_t delta, float cap_in) {
+    float *x = reinterpret_cast<float *>(sv), *y = reinterpret_cast<float *>(dv);
+    const uint64_t four = splat2(4.f), neg = splat2(-4.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 dl = lds_f4(delta + 16 * j);
+        uint64_t q02, q13;
+        logistic4<kNan>(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3], cap_in, q02, q13);
+        const uint64_t v02 = pmul(psub(pair2(y[4 * j], y[4 * j + 2]), pair2(dl.x, dl.z)), pmul(q02, pfma(q02, neg, four)));
+        const uint64_t v13 = pmul(psub(pair2(y[4 * j + 1], y[4 * j + 3]), pair2(dl.y, dl.w)), pmul(q13, pfma(q13, neg, four)));
+        x[4 * j] = plo(q02), x[4 * j + 1] = plo(q13), x[4 * j + 2] = phi(q02), x[4 * j + 3] = phi(q13);
+        y[4 * j] = plo(v02), y[4 * j + 1] = plo(v13), y[4 * j + 2] = phi(v02), y[4 * j + 3] = phi(v13);
+    }
+}
+
 // Scored: -inf for the scores of those of the 16 queries from row q0 on (in the
 // sample whose tokens start at n0) that do not see key kn.
 __device__ __forceinline__ void hide16(uint32_t (&sv)[16], const ScoreArgs &sc, size_t n0, int q0, int kn) {
@@ -419,17 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                                 m4 = sc.cap_out;
                             } else {
-                                const uint64_t four = splat2(4.f), neg = splat2(-4.f);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const float4 dl = lds_f4(vec + 256 + 16 * j);
-                                    uint64_t q02, q13;
-                                    logistic4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3], sc.cap_in, q02, q13);
-                                    const uint64_t v02 = pmul(psub(pair2(y[4 * j], y[4 * j + 2]), pair2(dl.x, dl.z)), pmul(q02, pfma(q02, neg, four)));
-                                    const uint64_t v13 = pmul(psub(pair2(y[4 * j + 1], y[4 * j + 3]), pair2(dl.y, dl.w)), pmul(q13, pfma(q13, neg, four)));
-                                    x[4 * j] = plo(q02), x[4 * j + 1] = plo(q13), x[4 * j + 2] = phi(q02), x[4 * j + 3] = phi(q13);
-                                    y[4 * j] = plo(v02), y[4 * j + 1] = plo(v13), y[4 * j + 2] = phi(v02), y[4 * j + 3] = phi(v13);
-                                }
+                                if (any_nan(sv)) logistic16<true>(sv, dv, vec + 256, sc.cap_in);
+                                else logistic16<false>(sv, dv, vec + 256, sc.cap_in);
                                 m4 = -2.f * sc.cap_out;
                                 a4 = sc.cap_out;
                             }

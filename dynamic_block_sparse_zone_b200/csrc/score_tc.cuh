@@ -7,6 +7,17 @@
 namespace prism {
 namespace tc {
 
+template <bool kNan>
+__device__ __forceinline__ void logistic32(uint32_t (&sr)[32], float cap_in) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        float *x = reinterpret_cast<float *>(&sr[e]);
+        uint64_t q02, q13;
+        logistic4<kNan>(x[0], x[1], x[2], x[3], cap_in, q02, q13);
+        x[0] = plo(q02), x[1] = plo(q13), x[2] = phi(q02), x[3] = phi(q13);
+    }
+}
+
 // x becomes the logit in log2 units (without cap and bias: stays the raw score),
 // -inf where the key is hidden.  pos, vis and doc: shared-window addresses of
 // the 32 keys' positions, visibilities and documents (vis and doc only read
@@ -33,13 +44,8 @@ __device__ __forceinline__ void logits32(uint32_t (&sr)[32], const ScoreArgs &sc
             }
             k = sc.cap_out;
         } else {  // q of every score in place
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                float *x = reinterpret_cast<float *>(&sr[e]);
-                uint64_t q02, q13;
-                logistic4(x[0], x[1], x[2], x[3], sc.cap_in, q02, q13);
-                x[0] = plo(q02), x[1] = plo(q13), x[2] = phi(q02), x[3] = phi(q13);
-            }
+            if (any_nan(sr)) logistic32<true>(sr, sc.cap_in);
+            else logistic32<false>(sr, sc.cap_in);
             k = -2.f * sc.cap_out;
             a = sc.cap_out;
         }

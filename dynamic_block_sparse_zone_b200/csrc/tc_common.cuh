@@ -486,7 +486,10 @@ __device__ __forceinline__ uint64_t tanh_small2(float x0, float x1, uint64_t k) 
 // error of tanh about 2e-7.  The four reciprocals are one of the product
 // (exponents are held below 30, so it stays under 2^121; tanh is 1 to fp32
 // beyond 10.4).  5 instructions and 1.25 special-function results per score; a
-// quotient of polynomials on [0, 9] took 9 instructions.
+// quotient of polynomials on [0, 9] took 9 instructions.  An infinite x is an
+// ordinary one.  A NaN counts as +infinity, so that it stays out of the product;
+// with kNan it is put back at the end.
+template <bool kNan>
 __device__ __forceinline__ void logistic4(float x0, float x1, float x2, float x3, float k2, uint64_t &q02, uint64_t &q13) {
     const float e0 = ex2(fminf(x0 * k2, 30.f)), e1 = ex2(fminf(x1 * k2, 30.f));
     const float e2 = ex2(fminf(x2 * k2, 30.f)), e3 = ex2(fminf(x3 * k2, 30.f));
@@ -496,9 +499,21 @@ __device__ __forceinline__ void logistic4(float x0, float x1, float x2, float x3
     const uint64_t r = pmul(splat2(rcp(plo(m) * phi(m))), pair2(phi(m), plo(m)));  // their reciprocals
     q02 = pmul(r, b);
     q13 = pmul(r, a);
+    if constexpr (kNan) {
+        q02 = pair2(x0 != x0 ? x0 : plo(q02), x2 != x2 ? x2 : phi(q02));
+        q13 = pair2(x1 != x1 ? x1 : plo(q13), x3 != x3 ? x3 : phi(q13));
+    }
 }
 // max(m, |a|, |b|)
 __device__ __forceinline__ float fmax3_abs(float m, float a, float b) { return fmax3(m, fabsf(a), fabsf(b)); }
+// Is any of the warp's scores NaN?  One instruction per two scores.
+template <int N>
+__device__ __forceinline__ bool any_nan(const uint32_t (&x)[N]) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) m = fmax3_nan(m, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+    return __any_sync(__activemask(), m != m);
+}
 
 }  // namespace tc
 }  // namespace prism

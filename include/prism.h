@@ -265,9 +265,12 @@ PRISM_API prism_status prism_attn_bwd(prism_plan *plan, const void *O, const voi
  * per token and 2 per value of O; PRISM_ERR_STATE while `stream` is being
  * captured).
  * With doc, a scored pass first zeroes the rows of padding tokens in the plan's
- * copies of Q, K and V, so that what padding holds reaches nothing; values of
- * visible tokens must be finite.  From then on until the next build or update
- * unscored passes see those zeros, and another prism_plan_set_score is refused.
+ * copies of Q, K and V, so that what padding holds reaches nothing.  A NaN in any
+ * other token makes NaN of what sees it, under a cap too; an infinity or a NaN
+ * there may also reach tokens that do not see it, as a weight of zero times it (V
+ * in the forward; Q, K, V and dO in the backward).  From the zeroing on until the
+ * next build or update unscored passes see those zeros, and another
+ * prism_plan_set_score is refused.
  * (The replay of a captured scored pass does the same unseen by that check:
  * bring the tensors in again before setting other scores by hand.)
  * PRISM_ERR_STATE in that case and before a build.                           */
