@@ -362,6 +362,8 @@ class PrismPlan:
             lse = torch.empty((p.batch, p.heads, p.N), dtype=torch.float32, device="cuda")
         if lse is not None:
             _need(lse, "lse", torch.float32, (p.batch, p.heads, p.N))
+        if scored:
+            _here(O=O, lse=lse)
         lib = load_library()
         fn = lib.prism_attn_fwd_taylor if taylor else lib.prism_attn_fwd_scored if scored else lib.prism_attn_fwd
         _check(fn(self._h, _ptr(O), _ptr(lse), _stream()))
@@ -377,6 +379,8 @@ class PrismPlan:
         dV = torch.empty(shp, dtype=torch.bfloat16, device="cuda") if dV is None else dV
         for t, n in ((dQ, "dQ"), (dK, "dK"), (dV, "dV")):
             _need(t, n, torch.bfloat16, shp)
+        if scored:
+            _here(O=O, dO=dO, dQ=dQ, dK=dK, dV=dV)
         fn = load_library().prism_attn_bwd_scored if scored else load_library().prism_attn_bwd
         _check(fn(self._h, _ptr(O), _ptr(dO), _ptr(dQ), _ptr(dK), _ptr(dV), _stream()))
         return dQ, dK, dV
