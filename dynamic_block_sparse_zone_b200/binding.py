@@ -658,6 +658,8 @@ def _rows(t: torch.Tensor, name: str, device=None, dtype=None):
         return prism_rows(t.data_ptr(), C, 0, 0), count, C
     if len(levels) == 1:
         return prism_rows(t.data_ptr(), levels[0][1], 0, 0), count, C
+    if count >= 1 << 31:  # the group is an int of the C interface
+        raise ValueError(f"{name}: rows in groups must be fewer than 2^31, got {count}")
     return prism_rows(t.data_ptr(), levels[0][1], levels[1][1], levels[0][0]), count, C
 
 
