@@ -415,7 +415,6 @@ prism_status configure_attn_scored_kernels() {
 template <int D, int kScore>
 static prism_status run(Plan &pl, void *O, float *lse, cudaStream_t st) {
     const Geo &g = pl.g;
-    TimerScope ts(pl, kTAttnFwd, st);
     segtc::k_attn_fwd_scored<D, kScore>
         <<<dim3(g.nbmax, g.batch * g.heads), segtc::kThreads, segtc::Layout<D>::kAlloc, st>>>(
             pl.tmQ, pl.tmK, pl.tmV, g, pl.qt_row, pl.qt_blk, pl.blk_off, pl.row_ptr, pl.score.col, pl.perm,
@@ -445,6 +444,7 @@ prism_status launch_attn_fwd_scored(Plan &pl, void *O, float *lse, cudaStream_t 
     prism_status s = launch_zero_padding(pl, st);
     if (s != PRISM_OK) return s;
     PRISM_CUDA_OK(cudaMemsetAsync(pl.score.redo, 0, sizeof(int), st));
+    TimerScope ts(pl, kTAttnFwd, st);  // one record for the tiles and those of them that are done again
     s = pl.g.D == 64 ? run_any<64>(pl, O, lse, st) : run_any<128>(pl, O, lse, st);
     return s == PRISM_OK ? launch_attn_fwd_scored_redo(pl, O, lse, st) : s;
 }

@@ -747,6 +747,7 @@ prism_status make_tensor_maps(Plan &pl) {
     return s;
 }
 
+// (timed by the caller)
 template <int D, bool kTaylor, int kScore = 0>
 static prism_status fwd_tc_impl(Plan &pl, void *O, float *lse, cudaStream_t st) {
     const Geo &g = pl.g;
@@ -754,7 +755,6 @@ static prism_status fwd_tc_impl(Plan &pl, void *O, float *lse, cudaStream_t st) 
     const uint32_t smem = kTaylor  ? fwdtc::Layout<D>::taylor_alloc(g.nbmax)
                           : kScore ? fwdtc::Layout<D>::kScoreAlloc
                                    : fwdtc::Layout<D>::kAlloc;
-    TimerScope ts(pl, kTaylor ? kTAttnFwdTaylor : kTAttnFwd, st);
     fwdtc::k_attn_fwd_tc<D, kTaylor, kScore><<<dim3(g.nbmax, g.batch * g.heads),
                                                 kScore ? fwdtc::kScoredThreads : fwdtc::kThreads, smem, st>>>(
         pl.tmQ, pl.tmK, pl.tmV, pl.tmKb, pl.tmVb, pl.nb, g, pl.nqt, pl.qt_row, pl.qt_blk, pl.blk_off, pl.row_ptr,
@@ -791,6 +791,7 @@ prism_status configure_attn_tc_kernels() {
 }
 
 prism_status launch_attn_fwd_tc(Plan &pl, void *O, float *lse, cudaStream_t st) {
+    TimerScope ts(pl, kTAttnFwd, st);
     return pl.g.D == 64 ? fwd_tc_impl<64, false>(pl, O, lse, st) : fwd_tc_impl<128, false>(pl, O, lse, st);
 }
 
@@ -861,6 +862,7 @@ prism_status launch_attn_fwd_taylor(Plan &pl, void *O, float *lse, cudaStream_t 
                                                                         pl.Kb, pl.Vb);
         PRISM_CUDA_OK(cudaGetLastError());
     }
+    TimerScope ts(pl, kTAttnFwdTaylor, st);
     return g.D == 64 ? fwd_tc_impl<64, true>(pl, O, lse, st) : fwd_tc_impl<128, true>(pl, O, lse, st);
 }
 
