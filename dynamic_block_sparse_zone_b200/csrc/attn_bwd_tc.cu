@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     int tile = blockIdx.x, bh = blockIdx.y;
     if constexpr (kEnc) {  // long tiles first
+        if (!own_scores(status, sc)) return;
         const int t = sc.order[blockIdx.y * gridDim.x + blockIdx.x];
         if (t < 0) return;
         bh = t / g.nbmax;

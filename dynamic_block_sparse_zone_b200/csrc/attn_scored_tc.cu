@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_u32(smem);
 
+    if (!own_scores(status, sc)) return;
     const int tid = sc.order[blockIdx.y * gridDim.x + blockIdx.x];
     if (tid < 0) return;
     const int bh = tid / g.nbmax, tile = tid - bh * g.nbmax, b = bh / g.heads, h = bh % g.heads;

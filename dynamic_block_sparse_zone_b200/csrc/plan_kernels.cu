@@ -922,7 +922,9 @@ __global__ void __launch_bounds__(1024) k_scan_add(int *__restrict__ out, int n,
 
 // Compact the padded selection into the CSR and count entries per column.
 __global__ void k_csr_compact(Geo g, int cap_stride, const int *__restrict__ cnt, const int *__restrict__ cols_pad,
-                              const int *__restrict__ row_ptr, int *__restrict__ col, int *__restrict__ col_count) {
+                              const int *__restrict__ row_ptr, int *__restrict__ col, int *__restrict__ col_count,
+                              int *__restrict__ status) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) status[kStKind] = 0;  // scores belong to the previous build
     const size_t rows = (size_t)g.batch * g.heads * g.nbmax;
     const int lane = threadIdx.x & 31;
     for (size_t r = (size_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < rows;
@@ -1099,7 +1101,8 @@ static prism_status launch_gather_select(Plan &pl, const __nv_bfloat16 *Q, const
     prism_status s = scan_ints(pl.cnt, rows, pl.row_ptr, pl.scan_tmp, st);
     if (s != PRISM_OK) return s;
     PRISM_CUDA_OK(cudaMemsetAsync(pl.colT_cursor, 0, rows * sizeof(int), st));
-    k_csr_compact<<<1184, 256, 0, st>>>(g, pl.cap_stride, pl.cnt, pl.cols_pad, pl.row_ptr, pl.col, pl.colT_cursor);
+    k_csr_compact<<<1184, 256, 0, st>>>(g, pl.cap_stride, pl.cnt, pl.cols_pad, pl.row_ptr, pl.col, pl.colT_cursor,
+                                         pl.status);
     PRISM_CUDA_OK(cudaGetLastError());
     s = scan_ints(pl.colT_cursor, rows, pl.colT_ptr, pl.scan_tmp, st);
     if (s != PRISM_OK) return s;

@@ -699,14 +699,20 @@ prism_status prism_plan_check(prism_plan *plan, void *stream) {
     prism_status s = device_guard(pl);
     if (s != PRISM_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int word[2] = {0, 0};
+    int word[kStWords] = {0};
     PRISM_CUDA_OK(cudaMemcpyAsync(word, pl.status, sizeof word, cudaMemcpyDeviceToHost, st));
     PRISM_CUDA_OK(cudaStreamSynchronize(st));
     PRISM_CUDA_OK(cudaGetLastError());
-    if (word[0] != 0) {
-        PRISM_CUDA_OK(cudaMemsetAsync(pl.status, 0, 16 * sizeof(int), st));
+    if (word[kStError] != 0) {
+        PRISM_CUDA_OK(cudaMemsetAsync(pl.status, 0, 2 * sizeof(int), st));
         PRISM_CUDA_OK(cudaStreamSynchronize(st));
-        return fail(PRISM_ERR_TIMEOUT, "device-side wait gave up (code %d, site %d)", word[0], word[1]);
+        return fail(PRISM_ERR_TIMEOUT, "device-side wait gave up (code %d, site %d)", word[kStError], word[kStSite]);
+    }
+    if (word[kStOther] != 0) {
+        PRISM_CUDA_OK(cudaMemsetAsync(pl.status + kStOther, 0, sizeof(int), st));
+        PRISM_CUDA_OK(cudaStreamSynchronize(st));
+        return fail(PRISM_ERR_STATE, "a scored pass met other scores than it was captured with, or none since the last "
+                                     "build: it has computed nothing");
     }
     return PRISM_OK;
 }

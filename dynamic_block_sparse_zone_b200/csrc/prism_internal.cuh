@@ -37,6 +37,16 @@ struct Geo {
     int Ctot, chunk0, nchunk_tot;
 };
 
+// The plan's status words.  The scores that the device's lists belong to are
+// kept on the device, too: a captured scored pass is replayed past the host's
+// checks, and with lists of another build it would read out of range.
+enum StatusWord {
+    kStError = 0, kStSite,   // a bounded wait that gave up (0: none), and where
+    kStKind, kStCap,         // score_kind (0: none since the last build) and cap of the last prism_plan_set_score
+    kStOther,                // a scored pass met others than its own
+    kStWords
+};
+
 // The scored attention of a plan (score.cu): the caller's scores and masks in
 // block-contiguous order, and the selection without the block pairs that the
 // mask hides.  Buffers are allocated by the first prism_plan_set_score.
@@ -122,7 +132,7 @@ struct Plan {
     __nv_bfloat16 *dOp;     // [batch*heads][N][D]
     float *delta;           // [batch*heads][N]
     float *dQacc;           // [batch*heads][N][D]
-    int *status;            // device error word (0 = ok)
+    int *status;            // device error words, see StatusWord
     int *host_nb;           // pinned host copy of nb
     TimerState *timers;     // NULL unless timing is on
     HostPipe *pipe;         // NULL until the first host-buffer step
@@ -194,11 +204,15 @@ struct ScoreArgs {
     float cap_one;              // sqrt(D) cap: unscaled scores up to here have |u| <= 1
     float cap_in;               // 2 log2(e) / (sqrt(D) cap)
     float cap_out;              // cap log2(e)
+    int kind;                   // score_kind and cap, which a launch is made for
+    float cap;
 };
 ScoreArgs score_args(const Plan &pl, bool backward);
 constexpr int kScored = 1, kCap = 2, kBias = 4, kMask = 8;  // template flags of those kernels (kMask: some pair may be hidden)
 inline int score_flags(const Score &s) { return kScored | (s.cap > 0.f ? kCap : 0) | (s.has_bias ? kBias : 0); }
 inline bool score_masks(const Score &s) { return s.has_doc || s.causal; }
+// What a scored pass's launches depend on besides the cap: its kernels and (documents) the zeroing of padding.
+inline int score_kind(const Score &s) { return score_flags(s) | (score_masks(s) ? kMask : 0) | (s.has_doc ? 16 : 0); }
 
 prism_status launch_audio_norms(const void *h, float *a, long long rows, int C, cudaStream_t st);
 

@@ -199,7 +199,12 @@ __global__ void __launch_bounds__(kThreads) k_score_work(Geo g, const int *__res
 // sums arrive.
 constexpr int kBins = 1024;
 __global__ void __launch_bounds__(kBins) k_score_order(Geo g, bool sort_f, bool sort_b, const int *__restrict__ work,
-                                                       int *__restrict__ order) {
+                                                       int *__restrict__ order, int *__restrict__ status, int kind,
+                                                       float cap) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) {  // the last kernel of a set_score: from here on the lists are these
+        status[kStKind] = kind;
+        status[kStCap] = __float_as_int(cap);
+    }
     __shared__ int cursor[kBins];
     __shared__ int sums[kBins / 32];
     const size_t tiles = (size_t)g.batch * g.heads * g.nbmax;
@@ -240,7 +245,9 @@ __global__ void __launch_bounds__(kBins) k_score_order(Geo g, bool sort_f, bool 
 // reach other rows through products with P = 0.  A thread looks at one token;
 // CTAs without padding are done then.
 __global__ void __launch_bounds__(kThreads) k_zero_padding(Geo g, const int *__restrict__ doc, __nv_bfloat16 *__restrict__ Qp,
-                                                           __nv_bfloat16 *__restrict__ Kp, __nv_bfloat16 *__restrict__ Vp) {
+                                                           __nv_bfloat16 *__restrict__ Kp, __nv_bfloat16 *__restrict__ Vp,
+                                                           int *__restrict__ status, ScoreArgs sc) {
+    if (!tc::own_scores(status, sc)) return;
     const int b = blockIdx.y, n0 = blockIdx.x * kThreads + (threadIdx.x & ~31), lane = threadIdx.x & 31;
     const bool pad = n0 + lane < g.N && doc[(size_t)b * g.N + n0 + lane] < 0;
     const int per = g.D / 8;
@@ -304,7 +311,8 @@ prism_status launch_zero_padding(Plan &pl, cudaStream_t st) {
     const Geo &g = pl.g;
     if (!pl.score.has_doc) return PRISM_OK;
     pl.score.zeroed = true;
-    k_zero_padding<<<dim3((g.N + kThreads - 1) / kThreads, g.batch), kThreads, 0, st>>>(g, pl.score.doc, pl.Qp, pl.Kp, pl.Vp);
+    k_zero_padding<<<dim3((g.N + kThreads - 1) / kThreads, g.batch), kThreads, 0, st>>>(g, pl.score.doc, pl.Qp, pl.Kp, pl.Vp,
+                                                                                           pl.status, score_args(pl, false));
     PRISM_CUDA_OK(cudaGetLastError());
     return PRISM_OK;
 }
@@ -363,7 +371,7 @@ prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
     // us; 13 per SM: 2.08 -> 2.41 ms, so not there).
     const int BH = g.batch * g.heads;
     const bool sort_f = (double)BH * g.N * g.D * 4 <= 160e6, sort_b = (long long)BH * (g.N / 128) <= 8 * 148;
-    k_score_order<<<dim3(1, 2), kBins, 0, st>>>(g, sort_f, sort_b, s.work, s.order);
+    k_score_order<<<dim3(1, 2), kBins, 0, st>>>(g, sort_f, sort_b, s.work, s.order, pl.status, score_kind(s), s.cap);
     PRISM_CUDA_OK(cudaGetLastError());
     s.set = true;
     return PRISM_OK;
@@ -382,6 +390,8 @@ ScoreArgs score_args(const Plan &pl, bool backward) {
     a.slopes = s.slopes;
     a.Olo = s.Olo;
     a.redo = s.redo;
+    a.kind = score_kind(s);
+    a.cap = s.cap;
     if (s.cap > 0.f) {
         a.cap_one = (float)(sqrt((double)pl.g.D) * (double)s.cap);
         a.cap_u = (float)(1.0 / (sqrt((double)pl.g.D) * (double)s.cap));

@@ -59,6 +59,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int *st
     return false;
 }
 
+// Are the lists on the device those of the scores that this pass was launched
+// for?  If not it has to leave everything alone.
+__device__ __forceinline__ bool own_scores(int *status, const ScoreArgs &sc) {
+    const volatile int *st = status;
+    if (st[kStKind] == sc.kind && __int_as_float(st[kStCap]) == sc.cap) return true;
+    if (threadIdx.x == 0) status[kStOther] = 1;
+    return false;
+}
+
 // ---- the block lists a 128-row tile streams ----
 // A tile holds one block (qt_blk = j) or the two 64-token blocks j, j+1
 // (qt_blk = ~j); j2 = -1 when there is no second block.

@@ -271,9 +271,16 @@ PRISM_API prism_status prism_attn_bwd(prism_plan *plan, const void *O, const voi
  * in the forward; Q, K, V and dO in the backward).  From the zeroing on until the
  * next build or update unscored passes see those zeros, and another
  * prism_plan_set_score is refused.
- * (The replay of a captured scored pass does the same unseen by that check:
- * bring the tensors in again before setting other scores by hand.)
- * PRISM_ERR_STATE in that case and before a build.                           */
+ * (The replay of a captured scored pass does the same unseen by that check, and
+ * a captured update counts from its capture on: bring the tensors in again before
+ * setting other scores by hand.)
+ * PRISM_ERR_STATE in that case and before a build.
+ * A captured scored pass may be replayed under later scores, and after later
+ * builds with scores of their own, of the same kind: the same cap, and slopes,
+ * doc and causal given or not as before (positions, documents and slopes
+ * themselves may differ).  Under others, or after a build without a
+ * prism_plan_set_score, its replay writes neither O nor dK nor dV, dQ is zero,
+ * and the next prism_plan_check returns PRISM_ERR_STATE.                     */
 typedef struct prism_score {
     float cap;
     const float *slopes, *pos;
@@ -463,7 +470,8 @@ PRISM_API prism_status prism_step_wait(prism_plan *plan, unsigned long long tick
 PRISM_API prism_status prism_plan_view_get(prism_plan *plan, prism_plan_view *view, void *stream);
 
 /* Synchronises `stream` and reports a device-side error recorded by a
- * kernel of this plan (PRISM_ERR_TIMEOUT for a bounded wait that gave up),
+ * kernel of this plan (PRISM_ERR_TIMEOUT for a bounded wait that gave up,
+ * PRISM_ERR_STATE for the replay of a captured scored pass under other scores),
  * then clears it.                                                          */
 PRISM_API prism_status prism_plan_check(prism_plan *plan, void *stream);
 
