@@ -61,7 +61,6 @@ namespace fwdtc {
 constexpr int kThreads = 192, kScoredThreads = 320;
 constexpr uint32_t kTmemCols = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr float kScoredThreshold = 24.0f;  // P and the sums are floating point: 2^24 costs them no digits
 
 template <int D>
 struct Layout {
@@ -312,7 +311,10 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
         // Two threads per row, one for each 64-key segment of the chunk (warps
         // 2..5 the first, 6..9 the second).  They share the row's reference m:
         // one barrier with an OR per chunk tells the two warps of a quadrant
-        // whether any of their rows' maxima has outgrown it, which is rare.
+        // whether any of their rows' maxima has outgrown it.  m is the maximum itself,
+        // without a margin: P <= 1 leaves O in range up to values of 2^128 / (keys),
+        // and range is what these tiles are here for (16 x 32 x 32, all tiles done
+        // again: a margin of 2^24 or 2^8 would save 5 to 7%, and lose as much range).
         const int quad = warp & 3, seg = (warp - 2) >> 2;
         const int rowid = quad * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
             // one barrier per chunk on every path: a warp whose wait failed meets its
             // partner here and they leave together
             if (!ok && lane == 0) *failed = 1;
-            if (named_bar_or(1 + quad, 64, !ok || mx > m + kScoredThreshold)) {
+            if (named_bar_or(1 + quad, 64, !ok || mx > m)) {
                 if (*failed) {
                     ok = false;
                     break;
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kScore ? kScoredThreads : kThreads, 2)
                 named_bar_sync(1 + quad, 64);
                 const float both = fmaxf(mx, exch[(seg ^ 1) * 128 + rowid]);
                 // the same answer in both threads; a row that has seen no key has m = -inf, l = 0, O = 0
-                const float mnew = both > m + kScoredThreshold ? both : m;
+                const float mnew = fmaxf(both, m);
                 const float corr = ex2(m - (mnew == -INFINITY ? 0.f : mnew));
                 if (c > 0) {  // each thread one half of O's columns
 #pragma unroll 1
