@@ -16,9 +16,11 @@
 // nothing ties one segment to the next but the sum in O:
 //   - the reference of the exponential is 0, not a running maximum: P and the
 //     sums are floating point, so a row is right as long as its sum lies in
-//     [2^-30, 2^80] (largest logits of -20 to 55) and O stays finite.  A tile with a row outside is put on a
-//     list and done again by the variant with a running maximum (attn_tc.cu),
-//     launched behind this kernel; the list is empty for ordinary scores;
+//     [2^-30, 2^80] (largest logits of -20 to 55) and O stays finite.  A tile with
+//     a row outside is put on a list and done again by the variant with a running
+//     maximum (attn_tc.cu), launched behind this kernel; the list is empty for
+//     ordinary scores (16 x 32 x 32 tokens, 8 heads of 128, without scores: 393 us,
+//     with every tile done again 1001 us);
 //   - segments alternate between two independent chains, each with its own 64
 //     columns of S / P in TMEM, K and V buffers, barriers and four softmax warps
 //     (one query row per thread).  Two CTAs share an SM: four chains.

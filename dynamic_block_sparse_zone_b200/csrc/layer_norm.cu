@@ -19,10 +19,11 @@
 //   92160 x 2048      140 us 0.83   162 us 0.91      190 us 0.92   222 us 0.66
 //   40000 x 5120      157 us 0.81   239 us 0.67      281 us 0.68   456 us 0.35
 //   40000 x 1001       72 us 0.34   127 us 0.24       87 us 0.43   100 us 0.31
-// What holds the others: from 8 bits, the instructions of the decoding (a byte
-// permute, a multiply-add and a multiply per pair beside the gradient's own);
-// rows of more than 4096 channels backward, one CTA per SM, whose barrier is not
-// hidden by another's work; odd rows, element-wise loads and stores.
+// What holds the others: from 8 bits, latency (168 registers leave 12 warps per
+// SM, which issue 0.50 instructions per cycle and scheduler; the decoding adds a
+// byte permute, a multiply-add and a multiply per pair to their chains); rows of
+// more than 4096 channels backward, one CTA per SM, whose barrier is not hidden by
+// another's work; odd rows, element-wise loads and stores.
 #include <atomic>
 
 #include "rows.cuh"

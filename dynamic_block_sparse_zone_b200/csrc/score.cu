@@ -366,9 +366,17 @@ prism_status set_score(Plan &pl, const prism_score &in, cudaStream_t st) {
         g, pl.nqt, pl.qt_row, pl.qt_blk, pl.blk_off, pl.row_ptr, s.row_end, s.col, pl.colT_ptr, s.colT_end, s.rowT, s.work);
     PRISM_CUDA_OK(cudaGetLastError());
     // Sorted while the tail counts more than neighbouring tiles' common blocks in L2:
-    // forward, K and V of all heads within L2 or nearly (8 heads of 30720 tokens, 126
-    // MB: 2.29 -> 2.16 ms); backward, up to eight tiles per SM (3 per SM: 990 -> 828
-    // us; 13 per SM: 2.08 -> 2.41 ms, so not there).
+    // forward, K and V of all heads within L2 or nearly; backward, up to eight tiles
+    // per SM.  Measured as they are -> sorted, in ms, cap and bias | packed causal clips,
+    // heads of 128, random block shapes:
+    //   tokens, heads   K and V  forward                   tiles per SM  backward
+    //   16x32x32, 8      67 MB   0.63->0.52 | 0.44->0.32     6.9  1.40->1.24 | 0.92->0.75
+    //   24x32x40, 8     126 MB   2.06->1.81 | 0.76->0.63    13    4.75->4.35 | 1.61->1.53
+    //   24x48x80, 4     189 MB   1.94->1.79 | 0.75->0.67    19    5.49->5.00 | 1.95->1.86
+    //   24x48x80, 24    1.1 GB   12.4->10.8 | 4.14->3.91   117    34.0->32.0 | 10.7->11.6
+    //   24x96x160, 24   4.5 GB   193->199 | 58.2->57.0     467    564->586 | 162->198
+    // Both limits are on the safe side: where they stop, the order still gains up to a
+    // tenth; the largest packed backward loses a fifth.
     const int BH = g.batch * g.heads;
     const bool sort_f = (double)BH * g.N * g.D * 4 <= 160e6, sort_b = (long long)BH * (g.N / 128) <= 8 * 148;
     k_score_order<<<dim3(1, 2), kBins, 0, st>>>(g, sort_f, sort_b, s.work, s.order, pl.status, score_kind(s), s.cap);

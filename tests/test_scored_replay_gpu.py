@@ -113,3 +113,15 @@ def test_a_scored_backward_from_a_checkpoint(P):  # noqa: F811
     rebuild(c, 56)
     t.refused(P)
     c.plan.close()
+
+
+@pytest.mark.gpu
+def test_a_reported_timeout_leaves_the_scores(P):  # noqa: F811
+    c = Case(P, 8, 16, 16, 2, 64, cap=10.0, clips=2, seed=57)
+    want = c.run()
+    c.plan.selftest_timeout()
+    with pytest.raises(P.PrismError, match="ERR_TIMEOUT"):
+        c.plan.check()
+    got = c.run()  # checks the plan
+    assert torch.equal(got["O"], want["O"]) and torch.equal(got["dV"], want["dV"])
+    c.plan.close()
